@@ -1,4 +1,4 @@
-"""ctypes declarations of the C ABI in include/gdn_cpr.h.
+"""ctypes declarations of the C ABI in include/gdn_cpr.h and include/gdn_attn.h.
 
 Loading fails loudly (RuntimeError) when the shared library has not been
 built: there is no fallback implementation anywhere in this package.
@@ -29,7 +29,13 @@ GDN_OP_PREFILL_CONTINUE = 3
 GDN_CMP_RECURRENT = 0
 GDN_CMP_CHUNKWISE = 1
 
-# every symbol the header declares
+GDN_ATTN_BLOCK = 64
+
+GDN_ATTN_OP_PREFILL = 0
+GDN_ATTN_OP_DECODE = 1
+GDN_ATTN_OP_NORM_ROPE_BWD = 2
+
+# every symbol gdn_cpr.h declares
 EXPORTED = (
     "gdn_cpr_workspace_size",
     "gdn_cpr_prefill",
@@ -47,6 +53,18 @@ EXPORTED = (
     "gdn_cmp_prefill",
     "gdn_cmp_decode_step",
     "gdn_cmp_chunk_decode_step",
+)
+
+# every symbol gdn_attn.h declares
+ATTN_EXPORTED = (
+    "gdn_attn_plan",
+    "gdn_attn_release",
+    "gdn_attn_workspace_size",
+    "gdn_attn_qk_norm_rope",
+    "gdn_attn_qk_norm_rope_bwd",
+    "gdn_attn_prefill",
+    "gdn_attn_decode_step",
+    "gdn_attn_cache_read",
 )
 
 
@@ -75,8 +93,54 @@ class Cache(ctypes.Structure):
     ]
 
 
+class AttnShapeC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_heads", "num_kv_heads", "head_dim", "dtype")]
+
+
+class AttnPoolC(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("block_table", "blocks_held", "free_blocks", "free_count", "seq_len")]
+                + [(n, ctypes.c_int32) for n in ("num_slots", "max_blocks", "num_blocks")])
+
+
+class AttnStepC(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("ctx_len", "positions", "slot_map", "status", "block_table",
+                                                "slot_index")]
+                + [(n, ctypes.c_int32) for n in ("max_blocks", "num_slots")])
+
+
+class AttnCacheC(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k8", "v8", "k_scale", "v_scale", "tail_k", "tail_v")]
+                + [(n, ctypes.c_int32) for n in ("num_blocks", "num_slots")])
+
+
+class AttnRopeC(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rotary_dim", "interleaved", "zero_centered", "num_positions")]
+                + [("eps", ctypes.c_float)])
+
+
 _vp = ctypes.c_void_p
 _lib = None
+
+
+def _declare_attn(lib: ctypes.CDLL) -> None:
+    i32, i64, size, f32, ptr = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float, ctypes.POINTER
+    shape, pool, step, cache, rope = map(ptr, (AttnShapeC, AttnPoolC, AttnStepC, AttnCacheC, AttnRopeC))
+    args = {
+        "gdn_attn_plan": [pool, i32, i64, _vp, i32, step, _vp],
+        "gdn_attn_release": [pool, i32, _vp, _vp],
+        "gdn_attn_qk_norm_rope": [shape, rope, i64, _vp, _vp, i64, i64, _vp, _vp, _vp, _vp, _vp, _vp, i64, i64, _vp],
+        "gdn_attn_qk_norm_rope_bwd": [shape, rope, i64, _vp, _vp, i64, i64, _vp, _vp, _vp, _vp, _vp, _vp, i64, i64,
+                                      _vp, _vp, i64, i64, _vp, _vp, _vp, size, _vp],
+        "gdn_attn_prefill": [shape, i32, i64, i32, _vp, _vp, _vp, i64, i64, i64, _vp, step, cache, f32, _vp, _vp, size,
+                             _vp],
+        "gdn_attn_decode_step": [shape, i32, _vp, _vp, _vp, i64, i64, i64, step, cache, f32, _vp, _vp, size, _vp],
+        "gdn_attn_cache_read": [shape, i32, i64, _vp, step, cache, _vp, _vp, _vp],
+    }
+    for name, types in args.items():
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = types
+    lib.gdn_attn_workspace_size.restype = size
+    lib.gdn_attn_workspace_size.argtypes = [shape, i32, i64, i32, i32]
 
 
 def load() -> ctypes.CDLL:
@@ -133,6 +197,7 @@ def load() -> ctypes.CDLL:
     lib.gdn_cpr_last_error.argtypes = []
     lib.gdn_cpr_numerics_id.restype = ctypes.c_char_p
     lib.gdn_cpr_numerics_id.argtypes = []
+    _declare_attn(lib)
     _lib = lib
     return lib
 

@@ -15,7 +15,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "gdn_cpr.hip")
+SRCS = [os.path.join(HERE, "csrc", n) for n in ("gdn_cpr.hip", "gdn_attn.hip")]
 OUT = os.path.join(HERE, "libgdn_cpr.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -89,7 +89,8 @@ def check_dpp_hazards(asm_text: str) -> list:
 # launch and memory traffic per spill, so the build rejects them
 HOT_KERNELS = ("k_scanIN3cpr4Bf16", "k_chain_scan_bf16", "k_decodeIN3cpr4Bf16", "k_resync_bf16",
                "k_cont_headIN3cpr4Bf16", "k_chunk_local_prefill_bf16", "k_chain_prefill_bf16", "k_bwd_local_bf16",
-               "k_bwd_chain_bf16", "k_bwd_state_grads_bf16", "k_plan")
+               "k_bwd_chain_bf16", "k_bwd_state_grads_bf16", "k_plan", "k_attn_decode", "k_attn_join",
+               "k_attn_norm_rope", "k_attn_plan", "k_attn_append")
 
 
 def check_spills(asm_text: str, hot=HOT_KERNELS) -> list:
@@ -105,25 +106,15 @@ def check_spills(asm_text: str, hot=HOT_KERNELS) -> list:
     return bad
 
 
-def check_isa(verbose: bool = True) -> None:
-    """Compile the device code to assembly and check the DPP hazard rule and
-    that no hot kernel spills."""
-    import tempfile
-    with tempfile.TemporaryDirectory() as d:
-        out = os.path.join(d, "gdn_cpr.s")
-        cmd = [HIPCC, *[f for f in FLAGS if f not in ("-shared", "-fPIC")], "--cuda-device-only", "-S",
-               "-o", out, SRC]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError("device assembly failed:\n" + res.stderr[-2000:])
-        with open(out) as f:
-            text = f.read()
-    n_dpp = text.count("v_fmac_f32_dpp")
-    bad = check_dpp_hazards(text)
+def check_isa(texts: list, verbose: bool = True) -> None:
+    """Check the sources' device assembly: the DPP hazard rule, and that no
+    hot kernel spills."""
+    n_dpp = sum(t.count("v_fmac_f32_dpp") for t in texts)
+    bad = [v for t in texts for v in check_dpp_hazards(t)]
     if bad:
         raise RuntimeError(f"DPP hazard in generated code ({len(bad)}): " + "; ".join(
             f"{fn} line {no}: {t}" for fn, no, t in bad[:5]))
-    spills = check_spills(text)
+    spills = [v for t in texts for v in check_spills(t)]
     if spills:
         raise RuntimeError("register spills in hot kernels: " + "; ".join(f"{n} ({k})" for n, k in spills))
     if verbose:
@@ -131,22 +122,42 @@ def check_isa(verbose: bool = True) -> None:
               "no spills in the hot kernels")
 
 
-def build(verbose: bool = True) -> str:
-    tmp = OUT + ".tmp"
-    cmd = [HIPCC, *FLAGS, "-o", tmp, SRC]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
+def _run(cmds: list) -> str:
+    """Run the compiler commands side by side; their messages."""
+    procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in cmds]
+    outs = [p.communicate()[0] for p in procs]
     # the host pass does not know the packed-fp32 target feature; that warning is expected
-    lines = [ln for ln in (res.stdout + res.stderr).splitlines() if "packed-fp32-ops" not in ln
+    lines = [ln for o in outs for ln in o.splitlines() if "packed-fp32-ops" not in ln
              and ln.strip() and not ln.startswith("1 warning")]
-    if res.returncode != 0:
+    bad = [p.returncode for p in procs if p.returncode != 0]
+    if bad:
         sys.stderr.write("\n".join(lines) + "\n")
-        raise RuntimeError(f"hipcc failed with status {res.returncode}")
-    if verbose and lines:
-        print("\n".join(lines))
+        raise RuntimeError(f"hipcc failed with status {bad[0]}")
+    return "\n".join(lines)
+
+
+def build(verbose: bool = True) -> str:
+    """Objects and device assembly of every source, side by side, then the link."""
+    import tempfile
+    tmp = OUT + ".tmp"
+    with tempfile.TemporaryDirectory() as d:
+        stem = [os.path.join(d, os.path.basename(s)) for s in SRCS]
+        base = [f for f in FLAGS if f != "-shared"]
+        cmds = [[HIPCC, *base, "-c", "-o", o + ".o", s] for s, o in zip(SRCS, stem)]
+        cmds += [[HIPCC, *[f for f in base if f != "-fPIC"], "--cuda-device-only", "-S", "-o", o + ".s", s]
+                 for s, o in zip(SRCS, stem)]
+        if verbose:
+            print("\n".join(" ".join(c) for c in cmds[:len(SRCS)]), flush=True)
+        said = _run(cmds)
+        if verbose and said:
+            print(said)
+        _run([[HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *[o + ".o" for o in stem]]])
+        texts = []
+        for o in stem:
+            with open(o + ".s") as f:
+                texts.append(f.read())
+    check_isa(texts, verbose)
     os.replace(tmp, OUT)
-    check_isa(verbose)
     return OUT
 
 

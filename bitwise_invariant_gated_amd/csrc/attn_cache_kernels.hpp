@@ -1,0 +1,242 @@
+// The attention cache's write side (tails, block quantisation) and its
+// read-out.
+//
+// A block is quantised from its 64 tokens at once: the largest finite
+// magnitude gives the scale's exponent, then every element is scaled (exactly,
+// by a power of two) and rounded to e4m3.  All of it is bound by memory and
+// small beside the attention that reads the cache: per token and head 4 d bytes in
+// and 2 d out.
+#pragma once
+
+#include "attn_device.hpp"
+
+namespace attn {
+
+struct CacheArgs {
+  uint8_t *k8, *v8;
+  float *k_scale, *v_scale;
+  uint16_t *tail_k, *tail_v;
+  int num_blocks, num_slots;
+};
+
+// The tokens of a call and where they belong.
+struct StepArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *cu, *ctx_len, *table, *slot;
+  int N, T, H, Hk, G, max_blocks;
+  uint16_t* o;
+  float c;  // softmax scale * log2(e)
+  CacheArgs cache;
+  uint16_t *old_k, *old_v;  // [N, Hk, 64, d], [N, Hk, d, 64]: the tails as they were before the call
+};
+
+// the pool block of a row's block b, held to the pool
+__device__ __forceinline__ int pool_block(const StepArgs& a, int row, int b) {
+  const int id = a.table[(size_t)row * a.max_blocks + min(b, a.max_blocks - 1)];
+  return min(max(id, 0), a.cache.num_blocks - 1);
+}
+
+// largest finite magnitude among eight bf16, as its bits (ordered like the values)
+__device__ __forceinline__ uint32_t amax8(u32x4 x, uint32_t m) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = x[i] & 0x7fffu, hi = (x[i] >> 16) & 0x7fffu;
+    m = max(m, lo < 0x7f80u ? lo : 0u);
+    m = max(m, hi < 0x7f80u ? hi : 0u);
+  }
+  return m;
+}
+
+// exponent e of the scale: the least e >= -100 with amax <= 448 * 2^e
+// (448 = 1.75 * 2^8; amax as bf16 bits)
+__device__ __forceinline__ int scale_exponent(uint32_t amax) {
+  return max((int)(amax >> 7) - 127 - 8 + ((amax & 0x7fu) > 0x60u ? 1 : 0), -100);
+}
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// eight bf16 times inv (a power of two) -> eight e4m3, nearest even; what is
+// not finite becomes NaN
+__device__ __forceinline__ u32x2 to_e4m3(u32x4 x, float inv) {
+  u32x2 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      f[2 * j] = __uint_as_float(x[2 * i + j] << 16) * inv;
+      f[2 * j + 1] = __uint_as_float(x[2 * i + j] & 0xffff0000u) * inv;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = __builtin_isinf(f[j]) ? __uint_as_float(0x7fc00000u) : f[j];
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
+    r[i] = (uint32_t)w;
+  }
+  return r;
+}
+
+// 16 e4m3 times a power of two -> 16 bf16 (exact)
+__device__ __forceinline__ void from_e4m3(u32x4 x, float scale, u32x4& lo, u32x4& hi) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[i], scale, false));
+    const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[i], scale, true));
+    (i < 2 ? lo : hi)[2 * (i & 1)] = a;
+    (i < 2 ? lo : hi)[2 * (i & 1) + 1] = b;
+  }
+}
+
+// max over a work-group of 256 threads; `red` is reused by every call
+__device__ __forceinline__ uint32_t block_max256(uint32_t m, uint32_t* red) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  return max(max(red[0], red[1]), max(red[2], red[3]));
+}
+
+// Quantises one block of one head by 256 threads.  kc(i) is K's chunk i (key
+// i / (D / 8), dims 8 (i % (D / 8)) ..), vc(i) is V's chunk i (dim i / 8, keys 8 (i % 8) ..).
+template <int D, class FK, class FV>
+__device__ __forceinline__ void quantise_block(const CacheArgs& c, int64_t at, FK&& kc, FV&& vc, uint32_t* red) {
+  constexpr int n = 64 * D / 8 / 256;
+  u32x4 x[n];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < n; ++i) m = amax8(x[i] = kc(threadIdx.x + 256 * i), m);
+  int e = scale_exponent(block_max256(m, red));
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    const int ch = threadIdx.x + 256 * i, key = ch / (D / 8), dim = ch % (D / 8) * 8;
+    *(u32x2*)(c.k8 + at * (64 * D) + (dim >> 6) * 4096 + key * 64 + (dim & 63)) = to_e4m3(x[i], pow2(-e));
+  }
+  if (threadIdx.x == 0) c.k_scale[at] = pow2(e);
+  m = 0;
+#pragma unroll
+  for (int i = 0; i < n; ++i) m = amax8(x[i] = vc(threadIdx.x + 256 * i), m);
+  e = scale_exponent(block_max256(m, red));
+#pragma unroll
+  for (int i = 0; i < n; ++i)
+    *(u32x2*)(c.v8 + at * (64 * D) + (int64_t)(threadIdx.x + 256 * i) * 8) = to_e4m3(x[i], pow2(-e));
+  if (threadIdx.x == 0) c.v_scale[at] = pow2(e);
+}
+
+// The i with slots(i) <= x < slots(i + 1), slots(i) = cu[i] / 64 + per * i: room for every block that
+// sequence i's tokens can touch, found without a prefix sum over the batch.
+__device__ __forceinline__ int seq_of_item(const int32_t* cu, int N, int x) {
+  int lo = 0, hi = N - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((cu[mid] >> 6) + 2 * mid <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// Appends a call's tokens: a work-group per (touched block, key/value head).
+// Full blocks are quantised.  The work-group of a sequence's first touched
+// block also keeps the tail as it was for the attention that follows (its
+// rows are that block's earlier tokens) and then writes the new tail, so that
+// no two work-groups touch one tail.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_append(const StepArgs a) {
+  constexpr int kLd = 72;  // V^T row in LDS: 64 keys and 16 bytes, rows start in different banks
+  __shared__ uint16_t vt[D * kLd];
+  __shared__ uint32_t red[4];
+  const int hk = blockIdx.y, tid = threadIdx.x;
+  const int i = seq_of_item(a.cu, a.N, blockIdx.x);
+  const int ctx = a.ctx_len[i], c0 = a.cu[i], len = a.cu[i + 1] - c0;
+  if (ctx < 0 || len <= 0) return;
+  const int first = ctx >> 6, last = (ctx + len - 1) >> 6;
+  const int b = first + (int)blockIdx.x - ((c0 >> 6) + 2 * i);
+  if (b > last) return;
+  const int row = row_of(a.slot, i, a.cache.num_slots);
+  if (row < 0) return;
+  const uint16_t* tk = a.cache.tail_k + ((int64_t)row * a.Hk + hk) * (64 * D);
+  const uint16_t* tv = a.cache.tail_v + ((int64_t)row * a.Hk + hk) * (64 * D);
+  const uint16_t* nk = a.k + (int64_t)hk * D;
+  const uint16_t* nv = a.v + (int64_t)hk * D;
+  const int old = b == first ? ctx & 63 : 0;  // tokens of this block that were there
+
+  if (b == first && old) {
+    u32x4* ok = (u32x4*)(a.old_k + ((int64_t)i * a.Hk + hk) * (64 * D));
+    u32x4* ov = (u32x4*)(a.old_v + ((int64_t)i * a.Hk + hk) * (64 * D));
+    for (int x = tid; x < 64 * D / 8; x += 256) {
+      ok[x] = ((const u32x4*)tk)[x];
+      ov[x] = ((const u32x4*)tv)[x];
+    }
+  }
+  if ((int64_t)(b + 1) * 64 <= (int64_t)ctx + len) {  // full now
+    const int64_t from = (int64_t)c0 + (int64_t)b * 64 - ctx;  // packed row of the block's key 0
+    for (int x = tid; x < 64 * D / 8; x += 256) {
+      const int key = x / (D / 8), dim = x % (D / 8) * 8;
+      if (key < old) continue;
+      const u32x4 w = *(const u32x4*)(nv + (from + key) * a.v_stride + dim);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        vt[(dim + 2 * j) * kLd + key] = (uint16_t)w[j];
+        vt[(dim + 2 * j + 1) * kLd + key] = (uint16_t)(w[j] >> 16);
+      }
+    }
+    for (int x = tid; x < D * old; x += 256) vt[x / old * kLd + x % old] = tv[x / old * 64 + x % old];
+    __syncthreads();
+    quantise_block<D>(
+        a.cache, (int64_t)pool_block(a, row, b) * a.Hk + hk,
+        [&](int x) {
+          const int key = x / (D / 8), dim = x % (D / 8) * 8;
+          return *(const u32x4*)(key < old ? tk + key * D + dim : nk + (from + key) * a.k_stride + dim);
+        },
+        [&](int x) { return *(const u32x4*)(vt + x / 8 * kLd + x % 8 * 8); }, red);
+  }
+  if (b != first) return;
+  __syncthreads();  // the old tail has been read
+  uint16_t* wk = a.cache.tail_k + ((int64_t)row * a.Hk + hk) * (64 * D);
+  uint16_t* wv = a.cache.tail_v + ((int64_t)row * a.Hk + hk) * (64 * D);
+  const int p0 = max(last * 64, ctx), n = ctx + len - p0;
+  for (int x = tid; x < n * (D / 8); x += 256) {
+    const int p = p0 + x / (D / 8), dim = x % (D / 8) * 8;
+    *(u32x4*)(wk + (p & 63) * D + dim) = *(const u32x4*)(nk + ((int64_t)c0 + p - ctx) * a.k_stride + dim);
+  }
+  for (int x = tid; x < n * D; x += 256) {
+    const int p = p0 + x % n, dim = x / n;
+    wv[dim * 64 + (p & 63)] = nv[((int64_t)c0 + p - ctx) * a.v_stride + dim];
+  }
+}
+
+// Read-out: a work-group per (touched block, key/value head) of the packed output.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_cache_read(const StepArgs a, uint16_t* k_out, uint16_t* v_out) {
+  const int hk = blockIdx.y;
+  const int i = seq_of_item(a.cu, a.N, blockIdx.x);
+  const int c0 = a.cu[i], len = a.cu[i + 1] - c0;
+  const int b = (int)blockIdx.x - ((c0 >> 6) + 2 * i);
+  if (len <= 0 || b > ((len - 1) >> 6)) return;
+  const int row = row_of(a.slot, i, a.cache.num_slots);
+  const bool full = (int64_t)(b + 1) * 64 <= len;
+  const int64_t at = row < 0 ? 0 : (int64_t)(full ? pool_block(a, row, b) : row) * a.Hk + hk;
+  const float ks = row >= 0 && full ? a.cache.k_scale[at] : 1.f, vs = row >= 0 && full ? a.cache.v_scale[at] : 1.f;
+  for (int x = threadIdx.x; x < 64 * D; x += 256) {
+    const int key = x / D, dim = x % D;
+    if (b * 64 + key >= len) break;
+    float kf = 0.f, vf = 0.f;
+    if (row >= 0 && full) {
+      const int kb = a.cache.k8[at * (64 * D) + (dim >> 6) * 4096 + key * 64 + (dim & 63)];
+      const int vb = a.cache.v8[at * (64 * D) + dim * 64 + key];
+      kf = __builtin_amdgcn_cvt_f32_fp8(kb, 0) * ks;
+      vf = __builtin_amdgcn_cvt_f32_fp8(vb, 0) * vs;
+    } else if (row >= 0) {
+      kf = __uint_as_float((uint32_t)a.cache.tail_k[at * (64 * D) + key * D + dim] << 16);
+      vf = __uint_as_float((uint32_t)a.cache.tail_v[at * (64 * D) + dim * 64 + key] << 16);
+    }
+    const int64_t to = ((int64_t)(c0 + b * 64 + key) * a.Hk + hk) * D + dim;
+    k_out[to] = (uint16_t)pack2(kf, 0.f);
+    v_out[to] = (uint16_t)pack2(vf, 0.f);
+  }
+}
+
+}  // namespace attn

@@ -1,0 +1,563 @@
+// The attention layer for gfx950: host side and the C ABI (gdn_attn.h).
+// The kernels live in attn_plan_kernels.hpp, attn_norm_rope_kernels.hpp,
+// attn_cache_kernels.hpp and attn_kernels.hpp.
+//
+// Per call, on the caller's stream:
+//   plan           k_attn_plan (and k_attn_plan_tokens for many tokens)
+//   norm + rope    k_attn_norm_rope; its gradient k_attn_norm_rope_bwd and
+//                  k_attn_norm_rope_dw
+//   prefill        k_attn_append (tails, full blocks), k_attn_prefill
+//   decode step    k_attn_decode (attention and append), k_attn_join
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <string>
+
+#include "../../include/gdn_attn.h"
+#include "attn_kernels.hpp"
+#include "attn_norm_rope_kernels.hpp"
+#include "attn_plan_kernels.hpp"
+
+std::string& gdn_last_error_text();  // gdn_cpr.hip
+
+namespace {
+
+using namespace attn;
+
+gdn_status fail(gdn_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  gdn_last_error_text() = buf;
+  return st;
+}
+
+gdn_status done() {
+  gdn_last_error_text().clear();
+  return GDN_OK;
+}
+
+gdn_status launch_status(const char* fn) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(GDN_ERR_HIP, "%s: kernel launch failed: %s", fn, hipGetErrorString(e));
+  return done();
+}
+
+size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+#define CHECK_PTR(p, name)                                                                          \
+  do {                                                                                              \
+    if (!(p)) return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);                         \
+    if (!aligned16(p)) return fail(GDN_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", fn, name); \
+  } while (0)
+
+#define CHECK_OPT_PTR(p, name)                                                                      \
+  do {                                                                                              \
+    if (!aligned16(p)) return fail(GDN_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", fn, name); \
+  } while (0)
+
+#define CHECK(call)                  \
+  do {                               \
+    const gdn_status r_ = (call);    \
+    if (r_ != GDN_OK) return r_;     \
+  } while (0)
+
+int kv_heads(const gdn_attn_shape& s) { return s.num_kv_heads > 0 ? s.num_kv_heads : s.num_heads; }
+
+constexpr int kMaxHeads = 1 << 15;
+
+gdn_status check_shape(const char* fn, const gdn_attn_shape* s) {
+  if (!s) return fail(GDN_ERR_INVALID_ARG, "%s: shape is NULL", fn);
+  if (s->num_heads < 1 || s->num_heads > kMaxHeads)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: num_heads must be in [1, %d]", fn, kMaxHeads);
+  if (s->num_kv_heads < 0 || s->num_kv_heads > s->num_heads ||
+      (s->num_kv_heads > 0 && s->num_heads % s->num_kv_heads != 0))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: num_kv_heads must be 0 or divide num_heads", fn);
+  if (s->head_dim != 64 && s->head_dim != 128 && s->head_dim != 256)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: head_dim must be 64, 128 or 256", fn);
+  if (s->dtype != GDN_DTYPE_F32 && s->dtype != GDN_DTYPE_BF16)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: dtype must be GDN_DTYPE_F32 or GDN_DTYPE_BF16", fn);
+  return GDN_OK;
+}
+
+gdn_status check_sizes(const char* fn, int64_t num_seqs, int64_t total_tokens) {
+  if (num_seqs < 0 || total_tokens < 0) return fail(GDN_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (total_tokens > INT32_MAX / 2 || num_seqs > INT32_MAX / 2) return fail(GDN_ERR_UNSUPPORTED, "%s: too many tokens", fn);
+  return GDN_OK;
+}
+
+// A token stride as given, resolved: 0 is `row` elements.
+gdn_status check_stride(const char* fn, const char* name, int64_t given, int64_t row, int64_t* out) {
+  *out = given ? given : row;
+  if (*out < row || *out % 8 != 0 || *out > INT64_MAX / INT32_MAX)
+    return fail(GDN_ERR_INVALID_ARG, "%s: %s must be 0 or a multiple of 8 of at least %lld", fn, name, (long long)row);
+  return GDN_OK;
+}
+
+gdn_status check_pool(const char* fn, const gdn_attn_pool* p) {
+  if (!p) return fail(GDN_ERR_INVALID_ARG, "%s: pool is NULL", fn);
+  CHECK_PTR(p->block_table, "pool.block_table");
+  CHECK_PTR(p->blocks_held, "pool.blocks_held");
+  CHECK_PTR(p->free_blocks, "pool.free_blocks");
+  CHECK_PTR(p->free_count, "pool.free_count");
+  CHECK_PTR(p->seq_len, "pool.seq_len");
+  if (p->num_slots < 1 || p->max_blocks < 1 || p->num_blocks < 1)
+    return fail(GDN_ERR_INVALID_ARG, "%s: pool sizes must be positive", fn);
+  return GDN_OK;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// plan
+
+extern "C" gdn_status gdn_attn_plan(const gdn_attn_pool* pool, int32_t num_seqs, int64_t total_tokens,
+                                    const int32_t* cu_seqlens, int32_t advance, const gdn_attn_step* step,
+                                    void* stream) {
+  const char* fn = "gdn_attn_plan";
+  CHECK(check_sizes(fn, num_seqs, total_tokens));
+  CHECK(check_pool(fn, pool));
+  if (!step) return fail(GDN_ERR_INVALID_ARG, "%s: step is NULL", fn);
+  CHECK_PTR(cu_seqlens, "cu_seqlens");
+  CHECK_PTR(step->status, "step.status");
+  CHECK_OPT_PTR(step->slot_index, "step.slot_index");
+  if (num_seqs > 0) CHECK_PTR(step->ctx_len, "step.ctx_len");
+  if (total_tokens > 0) {
+    CHECK_PTR(step->positions, "step.positions");
+    CHECK_PTR(step->slot_map, "step.slot_map");
+  }
+  if (num_seqs == 0 && total_tokens > 0) return fail(GDN_ERR_INVALID_ARG, "%s: tokens without requests", fn);
+  PlanArgs a{};
+  a.table = pool->block_table;
+  a.held = pool->blocks_held;
+  a.free = pool->free_blocks;
+  a.free_count = pool->free_count;
+  a.seq_len = pool->seq_len;
+  a.num_slots = pool->num_slots;
+  a.max_blocks = pool->max_blocks;
+  a.num_blocks = pool->num_blocks;
+  a.N = num_seqs;
+  a.T = (int)total_tokens;
+  a.advance = advance != 0;
+  a.tokens_here = total_tokens <= kTokensInPlan;
+  a.cu = cu_seqlens;
+  a.slot = step->slot_index;
+  a.ctx_len = step->ctx_len;
+  a.positions = step->positions;
+  a.slot_map = step->slot_map;
+  a.status = step->status;
+  hipLaunchKernelGGL(k_attn_plan, dim3(1), dim3(kPlanThreads), 0, (hipStream_t)stream, a);
+  if (!a.tokens_here)
+    hipLaunchKernelGGL(k_attn_plan_tokens, dim3((a.T + 255) / 256), dim3(256), 0, (hipStream_t)stream, a);
+  return launch_status(fn);
+}
+
+extern "C" gdn_status gdn_attn_release(const gdn_attn_pool* pool, int32_t num_seqs, const int32_t* slot_index,
+                                       void* stream) {
+  const char* fn = "gdn_attn_release";
+  CHECK(check_sizes(fn, num_seqs, 0));
+  CHECK(check_pool(fn, pool));
+  CHECK_OPT_PTR(slot_index, "slot_index");
+  if (num_seqs == 0) return done();
+  ReleaseArgs a{};
+  a.table = pool->block_table;
+  a.held = pool->blocks_held;
+  a.free = pool->free_blocks;
+  a.free_count = pool->free_count;
+  a.seq_len = pool->seq_len;
+  a.num_slots = pool->num_slots;
+  a.max_blocks = pool->max_blocks;
+  a.num_blocks = pool->num_blocks;
+  a.N = num_seqs;
+  a.slot = slot_index;
+  hipLaunchKernelGGL(k_attn_release, dim3(1), dim3(kPlanThreads), 0, (hipStream_t)stream, a);
+  return launch_status(fn);
+}
+
+// ---------------------------------------------------------------------------
+// norm and rotation
+
+namespace {
+
+// work-groups of the gradient's row pass, each with a partial dw: enough to
+// fill the card (4 on each of 256 CUs), few enough that adding them up is short
+constexpr int kNormBwdGroups = 1024;
+
+int norm_bwd_groups(const gdn_attn_shape& s, int64_t T) {
+  const int64_t rows = T * s.num_heads, per = kNormThreads / (s.head_dim / 8);
+  return (int)std::min<int64_t>(kNormBwdGroups, std::max<int64_t>(1, (rows + per - 1) / per));
+}
+
+gdn_status check_norm(const char* fn, const gdn_attn_shape* shape, const gdn_attn_rope* rope, int64_t T, const void* q,
+                      const void* k, int64_t q_stride, int64_t k_stride, const float* w_q, const float* w_k,
+                      const float* cos_sin, const int32_t* positions, NormRopeArgs* a) {
+  CHECK(check_shape(fn, shape));
+  CHECK(check_sizes(fn, 0, T));
+  if (!rope) return fail(GDN_ERR_INVALID_ARG, "%s: rope is NULL", fn);
+  const int d = shape->head_dim, H = shape->num_heads, Hk = kv_heads(*shape);
+  if (T * H > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%s: too many rows", fn);
+  if (rope->rotary_dim < 0 || rope->rotary_dim > d || rope->rotary_dim % 8 != 0)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: rotary_dim must be a multiple of 8 up to head_dim", fn);
+  if (!(rope->eps >= 0.f) || std::isinf(rope->eps)) return fail(GDN_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
+  CHECK_PTR(w_q, "w_q");
+  CHECK_PTR(w_k, "w_k");
+  CHECK(check_stride(fn, "q_stride", q_stride, (int64_t)H * d, &a->x_stride[0]));
+  CHECK(check_stride(fn, "k_stride", k_stride, (int64_t)Hk * d, &a->x_stride[1]));
+  if (T > 0) {
+    CHECK_PTR(q, "q");
+    CHECK_PTR(k, "k");
+    if (rope->rotary_dim > 0) {
+      if (rope->num_positions < 1) return fail(GDN_ERR_INVALID_ARG, "%s: num_positions must be positive", fn);
+      CHECK_PTR(cos_sin, "cos_sin");
+      CHECK_PTR(positions, "positions");
+    }
+  }
+  a->x[0] = q;
+  a->x[1] = k;
+  a->w[0] = w_q;
+  a->w[1] = w_k;
+  a->heads[0] = H;
+  a->heads[1] = Hk;
+  a->rows[0] = T * H;
+  a->rows[1] = T * Hk;
+  a->cos_sin = cos_sin;
+  a->positions = positions;
+  a->rd = rope->rotary_dim;
+  a->interleaved = rope->interleaved != 0;
+  a->num_positions = rope->num_positions;
+  a->eps = rope->eps;
+  a->w_add = rope->zero_centered ? 1.f : 0.f;
+  return GDN_OK;
+}
+
+template <class E, int D, int U>
+void launch_norm(NormRopeArgs& a, hipStream_t st) {
+  const int64_t per = (int64_t)(kNormThreads / (D / 8)) * U;
+  for (int i = 0; i < 2; ++i) a.groups[i] = (int)((a.rows[i] + per - 1) / per);
+  hipLaunchKernelGGL((k_attn_norm_rope<E, D, U>), dim3(a.groups[0] + a.groups[1]), dim3(kNormThreads), 0, st, a);
+}
+
+// Four rows per lane group once that still leaves 8 work-groups per CU.
+template <class E, int D>
+void run_norm(NormRopeArgs& a, hipStream_t st) {
+  const int64_t per = kNormThreads / (D / 8);
+  if (a.rows[0] + a.rows[1] >= per * 4 * 2048)
+    launch_norm<E, D, 4>(a, st);
+  else
+    launch_norm<E, D, 1>(a, st);
+}
+
+template <class E, int D>
+void run_norm_bwd(const NormRopeArgs& a, int groups, float* dw_q, float* dw_k, hipStream_t st) {
+  hipLaunchKernelGGL((k_attn_norm_rope_bwd<E, D>), dim3(groups), dim3(kNormThreads), 0, st, a);
+  hipLaunchKernelGGL(k_attn_norm_rope_dw, dim3(2 * D / 32), dim3(1024), 0, st, a.partial, groups, D, dw_q, dw_k);
+}
+
+#define GDN_ATTN_DISPATCH(shape, fn_, ...)                                \
+  do {                                                                    \
+    const bool bf_ = (shape).dtype == GDN_DTYPE_BF16;                     \
+    switch ((shape).head_dim) {                                           \
+      case 64: bf_ ? fn_<ElemBf16, 64>(__VA_ARGS__) : fn_<ElemF32, 64>(__VA_ARGS__); break;    \
+      case 128: bf_ ? fn_<ElemBf16, 128>(__VA_ARGS__) : fn_<ElemF32, 128>(__VA_ARGS__); break; \
+      default: bf_ ? fn_<ElemBf16, 256>(__VA_ARGS__) : fn_<ElemF32, 256>(__VA_ARGS__); break;  \
+    }                                                                     \
+  } while (0)
+
+}  // namespace
+
+extern "C" gdn_status gdn_attn_qk_norm_rope(const gdn_attn_shape* shape, const gdn_attn_rope* rope,
+                                            int64_t total_tokens, const void* q, const void* k, int64_t q_stride,
+                                            int64_t k_stride, const float* w_q, const float* w_k,
+                                            const float* cos_sin, const int32_t* positions, void* q_out, void* k_out,
+                                            int64_t q_out_stride, int64_t k_out_stride, void* stream) {
+  const char* fn = "gdn_attn_qk_norm_rope";
+  NormRopeArgs a{};
+  CHECK(check_norm(fn, shape, rope, total_tokens, q, k, q_stride, k_stride, w_q, w_k, cos_sin, positions, &a));
+  const int64_t d = shape->head_dim;
+  CHECK(check_stride(fn, "q_out_stride", q_out_stride, shape->num_heads * d, &a.out_stride[0]));
+  CHECK(check_stride(fn, "k_out_stride", k_out_stride, kv_heads(*shape) * d, &a.out_stride[1]));
+  if (total_tokens == 0) return done();
+  CHECK_PTR(q_out, "q_out");
+  CHECK_PTR(k_out, "k_out");
+  a.out[0] = q_out;
+  a.out[1] = k_out;
+  for (int i = 0; i < 2; ++i)
+    if (a.out[i] == a.x[i] && a.out_stride[i] != a.x_stride[i])
+      return fail(GDN_ERR_INVALID_ARG, "%s: in place needs equal strides", fn);
+  GDN_ATTN_DISPATCH(*shape, run_norm, a, (hipStream_t)stream);
+  return launch_status(fn);
+}
+
+extern "C" gdn_status gdn_attn_qk_norm_rope_bwd(const gdn_attn_shape* shape, const gdn_attn_rope* rope,
+                                                int64_t total_tokens, const void* q, const void* k, int64_t q_stride,
+                                                int64_t k_stride, const float* w_q, const float* w_k,
+                                                const float* cos_sin, const int32_t* positions, const void* d_q_out,
+                                                const void* d_k_out, int64_t dqo_stride, int64_t dko_stride, void* dq,
+                                                void* dk, int64_t dq_stride, int64_t dk_stride, float* dw_q,
+                                                float* dw_k, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "gdn_attn_qk_norm_rope_bwd";
+  NormRopeArgs a{};
+  CHECK(check_norm(fn, shape, rope, total_tokens, q, k, q_stride, k_stride, w_q, w_k, cos_sin, positions, &a));
+  const int64_t d = shape->head_dim;
+  CHECK(check_stride(fn, "dqo_stride", dqo_stride, shape->num_heads * d, &a.dy_stride[0]));
+  CHECK(check_stride(fn, "dko_stride", dko_stride, kv_heads(*shape) * d, &a.dy_stride[1]));
+  CHECK(check_stride(fn, "dq_stride", dq_stride, shape->num_heads * d, &a.out_stride[0]));
+  CHECK(check_stride(fn, "dk_stride", dk_stride, kv_heads(*shape) * d, &a.out_stride[1]));
+  CHECK_PTR(dw_q, "dw_q");
+  CHECK_PTR(dw_k, "dw_k");
+  if (total_tokens > 0) {
+    CHECK_PTR(d_q_out, "d_q_out");
+    CHECK_PTR(d_k_out, "d_k_out");
+    CHECK_PTR(dq, "dq");
+    CHECK_PTR(dk, "dk");
+  }
+  a.dy[0] = d_q_out;
+  a.dy[1] = d_k_out;
+  a.out[0] = dq;
+  a.out[1] = dk;
+  for (int i = 0; i < 2; ++i)
+    if ((a.out[i] == a.dy[i] && a.out_stride[i] != a.dy_stride[i]) || (a.out[i] == a.x[i] && a.out_stride[i] != a.x_stride[i]))
+      return fail(GDN_ERR_INVALID_ARG, "%s: in place needs equal strides", fn);
+  const size_t need = gdn_attn_workspace_size(shape, GDN_ATTN_OP_NORM_ROPE_BWD, total_tokens, 0, 0);
+  if (!workspace || workspace_bytes < need)
+    return fail(GDN_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (!aligned16(workspace)) return fail(GDN_ERR_INVALID_ARG, "%s: workspace is not 16-byte aligned", fn);
+  a.partial = (float*)workspace;
+  GDN_ATTN_DISPATCH(*shape, run_norm_bwd, a, norm_bwd_groups(*shape, total_tokens), dw_q, dw_k, (hipStream_t)stream);
+  return launch_status(fn);
+}
+
+// ---------------------------------------------------------------------------
+// attention
+
+namespace {
+
+struct PrefillLayout {
+  size_t old_k, old_v, total;
+};
+
+PrefillLayout prefill_layout(const gdn_attn_shape& s, int32_t N) {
+  const size_t tail = align_up((size_t)N * kv_heads(s) * kBlock * s.head_dim * sizeof(uint16_t));
+  return {0, tail, 2 * tail};
+}
+
+struct DecodeLayout {
+  size_t base, total_word, rec_ml, rec_o, total;
+  int64_t max_parts;
+};
+
+DecodeLayout decode_layout(const gdn_attn_shape& s, int32_t N, int32_t num_blocks) {
+  DecodeLayout L;
+  L.max_parts = (int64_t)num_blocks / kPartBlocks + N;
+  size_t off = 0;
+  L.base = off;
+  off = align_up(off + sizeof(int32_t) * (size_t)N);
+  L.total_word = off;
+  off = align_up(off + sizeof(int32_t));
+  L.rec_ml = off;
+  off = align_up(off + (size_t)L.max_parts * s.num_heads * 8 * sizeof(float));
+  L.rec_o = off;
+  off = align_up(off + (size_t)L.max_parts * s.num_heads * s.head_dim * sizeof(float));
+  L.total = off;
+  return L;
+}
+
+gdn_status check_step(const char* fn, const gdn_attn_step* step, const gdn_attn_cache* cache) {
+  if (!step) return fail(GDN_ERR_INVALID_ARG, "%s: step is NULL", fn);
+  if (!cache) return fail(GDN_ERR_INVALID_ARG, "%s: cache is NULL", fn);
+  CHECK_PTR(step->block_table, "step.block_table");
+  CHECK_OPT_PTR(step->slot_index, "step.slot_index");
+  CHECK_PTR(cache->k8, "cache.k8");
+  CHECK_PTR(cache->v8, "cache.v8");
+  CHECK_PTR(cache->k_scale, "cache.k_scale");
+  CHECK_PTR(cache->v_scale, "cache.v_scale");
+  CHECK_PTR(cache->tail_k, "cache.tail_k");
+  CHECK_PTR(cache->tail_v, "cache.tail_v");
+  if (step->max_blocks < 1 || step->num_slots < 1 || cache->num_blocks < 1 || cache->num_slots < 1)
+    return fail(GDN_ERR_INVALID_ARG, "%s: step and cache sizes must be positive", fn);
+  if (step->num_slots != cache->num_slots)
+    return fail(GDN_ERR_INVALID_ARG, "%s: the step's table has %d rows, the cache %d", fn, step->num_slots, cache->num_slots);
+  return GDN_OK;
+}
+
+void fill_cache(StepArgs& s, const gdn_attn_shape& shape, int32_t N, int64_t T, const gdn_attn_step& step,
+                const gdn_attn_cache& cache) {
+  s.ctx_len = step.ctx_len;
+  s.table = step.block_table;
+  s.slot = step.slot_index;
+  s.max_blocks = step.max_blocks;
+  s.N = N;
+  s.T = (int)T;
+  s.H = shape.num_heads;
+  s.Hk = kv_heads(shape);
+  s.G = s.H / s.Hk;
+  s.cache.k8 = cache.k8;
+  s.cache.v8 = cache.v8;
+  s.cache.k_scale = cache.k_scale;
+  s.cache.v_scale = cache.v_scale;
+  s.cache.tail_k = (uint16_t*)cache.tail_k;
+  s.cache.tail_v = (uint16_t*)cache.tail_v;
+  s.cache.num_blocks = cache.num_blocks;
+  s.cache.num_slots = cache.num_slots;
+}
+
+// Checks shared by prefill and decode; fills everything but cu, the old tails and records.
+gdn_status check_attention(const char* fn, const gdn_attn_shape* shape, int32_t N, int64_t T, const void* q,
+                           const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                           const gdn_attn_step* step, const gdn_attn_cache* cache, float scale, void* o, StepArgs* a) {
+  CHECK(check_shape(fn, shape));
+  if (shape->dtype != GDN_DTYPE_BF16) return fail(GDN_ERR_UNSUPPORTED, "%s: attention takes bf16", fn);
+  CHECK(check_sizes(fn, N, T));
+  if (T * shape->num_heads > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%s: too many rows", fn);
+  CHECK(check_step(fn, step, cache));
+  if (!(scale > 0.f) || std::isinf(scale)) return fail(GDN_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
+  if (N == 0 && T > 0) return fail(GDN_ERR_INVALID_ARG, "%s: tokens without sequences", fn);
+  const int64_t d = shape->head_dim;
+  CHECK(check_stride(fn, "q_stride", q_stride, shape->num_heads * d, &a->q_stride));
+  CHECK(check_stride(fn, "k_stride", k_stride, kv_heads(*shape) * d, &a->k_stride));
+  CHECK(check_stride(fn, "v_stride", v_stride, kv_heads(*shape) * d, &a->v_stride));
+  if (N > 0) CHECK_PTR(step->ctx_len, "step.ctx_len");
+  if (T > 0) {
+    CHECK_PTR(q, "q");
+    CHECK_PTR(k, "k");
+    CHECK_PTR(v, "v");
+    CHECK_PTR(o, "o");
+  }
+  a->q = (const uint16_t*)q;
+  a->k = (const uint16_t*)k;
+  a->v = (const uint16_t*)v;
+  a->o = (uint16_t*)o;
+  a->c = scale * 1.44269504088896340736f;
+  fill_cache(*a, *shape, N, T, *step, *cache);
+  return GDN_OK;
+}
+
+gdn_status check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
+  if (!workspace || bytes < need)
+    return fail(GDN_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need, workspace ? bytes : (size_t)0);
+  if (!aligned16(workspace)) return fail(GDN_ERR_INVALID_ARG, "%s: workspace is not 16-byte aligned", fn);
+  return GDN_OK;
+}
+
+template <int D>
+void run_append(const StepArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL(k_attn_append<D>, dim3(a.T / kBlock + 2 * a.N, a.Hk), dim3(256), 0, st, a);
+}
+
+template <int D>
+gdn_status run_prefill(const StepArgs& a, hipStream_t st, const char* fn) {
+  typedef PrefillTile<D> P;
+  run_append<D>(a, st);
+  const int64_t tiles = (int64_t)a.T * a.G / P::kRows + a.N;
+  hipLaunchKernelGGL(k_attn_prefill<D>, dim3((unsigned)tiles, a.Hk), dim3(512), 0, st, a);
+  return launch_status(fn);
+}
+
+template <int D>
+gdn_status run_decode(const DecodeArgs& a, hipStream_t st, const char* fn) {
+  // two work-groups on each of 256 CUs, over the key/value heads and groups of 16 query heads
+  const int z = (a.s.G + 15) / 16;
+  const int W = std::max(1, std::min(512 / std::max(1, a.s.Hk * z), a.max_parts));
+  hipLaunchKernelGGL(k_attn_decode<D>, dim3(W, a.s.Hk, z), dim3(256), 0, st, a);
+  const int jz = (a.s.G * (D / 4) + 255) / 256;
+  hipLaunchKernelGGL(k_attn_join<D>, dim3(a.s.N, a.s.Hk, jz), dim3(256), 0, st, a, W);
+  return launch_status(fn);
+}
+
+}  // namespace
+
+extern "C" gdn_status gdn_attn_prefill(const gdn_attn_shape* shape, int32_t num_seqs, int64_t total_tokens,
+                                       int32_t max_new, const void* q, const void* k, const void* v, int64_t q_stride,
+                                       int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens,
+                                       const gdn_attn_step* step, const gdn_attn_cache* cache, float scale, void* o,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "gdn_attn_prefill";
+  StepArgs a{};
+  CHECK(check_attention(fn, shape, num_seqs, total_tokens, q, k, v, q_stride, k_stride, v_stride, step, cache, scale, o, &a));
+  if (max_new < 0) return fail(GDN_ERR_INVALID_ARG, "%s: max_new is negative", fn);
+  CHECK_PTR(cu_seqlens, "cu_seqlens");
+  if (total_tokens == 0) return done();
+  const PrefillLayout L = prefill_layout(*shape, num_seqs);
+  CHECK(check_workspace(fn, workspace, workspace_bytes, L.total));
+  a.cu = cu_seqlens;
+  a.old_k = (uint16_t*)((char*)workspace + L.old_k);
+  a.old_v = (uint16_t*)((char*)workspace + L.old_v);
+  switch (shape->head_dim) {
+    case 64: return run_prefill<64>(a, (hipStream_t)stream, fn);
+    case 128: return run_prefill<128>(a, (hipStream_t)stream, fn);
+    default: return run_prefill<256>(a, (hipStream_t)stream, fn);
+  }
+}
+
+extern "C" gdn_status gdn_attn_decode_step(const gdn_attn_shape* shape, int32_t num_seqs, const void* q, const void* k,
+                                           const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                           const gdn_attn_step* step, const gdn_attn_cache* cache, float scale,
+                                           void* o, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "gdn_attn_decode_step";
+  DecodeArgs a{};
+  CHECK(check_attention(fn, shape, num_seqs, num_seqs, q, k, v, q_stride, k_stride, v_stride, step, cache, scale, o, &a.s));
+  if (num_seqs == 0) return done();
+  const DecodeLayout L = decode_layout(*shape, num_seqs, cache->num_blocks);
+  CHECK(check_workspace(fn, workspace, workspace_bytes, L.total));
+  a.base = (int32_t*)((char*)workspace + L.base);
+  a.total = (int32_t*)((char*)workspace + L.total_word);
+  a.rec_ml = (float*)((char*)workspace + L.rec_ml);
+  a.rec_o = (float*)((char*)workspace + L.rec_o);
+  a.max_parts = (int)std::min<int64_t>(L.max_parts, INT32_MAX);
+  switch (shape->head_dim) {
+    case 64: return run_decode<64>(a, (hipStream_t)stream, fn);
+    case 128: return run_decode<128>(a, (hipStream_t)stream, fn);
+    default: return run_decode<256>(a, (hipStream_t)stream, fn);
+  }
+}
+
+extern "C" gdn_status gdn_attn_cache_read(const gdn_attn_shape* shape, int32_t num_seqs, int64_t total_tokens,
+                                          const int32_t* cu_seqlens, const gdn_attn_step* step,
+                                          const gdn_attn_cache* cache, void* k_out, void* v_out, void* stream) {
+  const char* fn = "gdn_attn_cache_read";
+  CHECK(check_shape(fn, shape));
+  if (shape->dtype != GDN_DTYPE_BF16) return fail(GDN_ERR_UNSUPPORTED, "%s: attention takes bf16", fn);
+  CHECK(check_sizes(fn, num_seqs, total_tokens));
+  CHECK(check_step(fn, step, cache));
+  CHECK_PTR(cu_seqlens, "cu_seqlens");
+  if (total_tokens == 0) return done();
+  if (num_seqs == 0) return fail(GDN_ERR_INVALID_ARG, "%s: tokens without sequences", fn);
+  CHECK_PTR(k_out, "k_out");
+  CHECK_PTR(v_out, "v_out");
+  StepArgs a{};
+  fill_cache(a, *shape, num_seqs, total_tokens, *step, *cache);
+  a.cu = cu_seqlens;
+  const dim3 grid(a.T / kBlock + 2 * a.N, a.Hk);
+  switch (shape->head_dim) {
+    case 64:
+      hipLaunchKernelGGL(k_attn_cache_read<64>, grid, dim3(256), 0, (hipStream_t)stream, a, (uint16_t*)k_out, (uint16_t*)v_out);
+      break;
+    case 128:
+      hipLaunchKernelGGL(k_attn_cache_read<128>, grid, dim3(256), 0, (hipStream_t)stream, a, (uint16_t*)k_out, (uint16_t*)v_out);
+      break;
+    default:
+      hipLaunchKernelGGL(k_attn_cache_read<256>, grid, dim3(256), 0, (hipStream_t)stream, a, (uint16_t*)k_out, (uint16_t*)v_out);
+  }
+  return launch_status(fn);
+}
+
+extern "C" size_t gdn_attn_workspace_size(const gdn_attn_shape* shape, int32_t op, int64_t total_tokens,
+                                          int32_t num_seqs, int32_t num_blocks) {
+  const std::string before = gdn_last_error_text();
+  const bool ok = check_shape("gdn_attn_workspace_size", shape) == GDN_OK &&
+                  check_sizes("gdn_attn_workspace_size", num_seqs, total_tokens) == GDN_OK && num_blocks >= 0;
+  gdn_last_error_text() = before;  // a size query is no call
+  if (!ok) return 0;
+  if (op == GDN_ATTN_OP_PREFILL) return prefill_layout(*shape, num_seqs).total;
+  if (op == GDN_ATTN_OP_DECODE) return decode_layout(*shape, num_seqs, num_blocks).total;
+  if (op == GDN_ATTN_OP_NORM_ROPE_BWD)
+    return align_up((size_t)norm_bwd_groups(*shape, total_tokens) * 2 * shape->head_dim * sizeof(float));
+  return 0;
+}

@@ -1439,6 +1439,9 @@ extern "C" void gdn_cpr_set_stage_events(void* const* events, int32_t n_events) 
 
 extern "C" const char* gdn_cpr_last_error(void) { return g_last_error.c_str(); }
 
+// gdn_attn.hip's access to the calling thread's last error
+__attribute__((visibility("hidden"))) std::string& gdn_last_error_text() { return g_last_error; }
+
 extern "C" const char* gdn_cpr_numerics_id(void) {
   return "gdn_cpr numerics v7: "
          "per-token step (one routine for the prefill scan, decode and the continuation head; k and q by DPP "

@@ -29,6 +29,7 @@ struct StepArgs {
   float c;  // softmax scale * log2(e)
   CacheArgs cache;
   uint16_t *old_k, *old_v;  // [N, Hk, 64, d], [N, Hk, d, 64]: the tails as they were before the call
+  int32_t* bad;             // per touched block and head: does its V hold a value that is not finite?
 };
 
 // the pool block of a row's block b, held to the pool
@@ -55,6 +56,14 @@ __device__ __forceinline__ int scale_exponent(uint32_t amax) {
 }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// whether one of eight bf16 is not finite
+__device__ __forceinline__ bool not_finite8(u32x4 x) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad |= (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
+  return bad;
+}
 
 // eight bf16 times inv (a power of two) -> eight e4m3, nearest even; what is
 // not finite becomes NaN
@@ -142,7 +151,8 @@ __device__ __forceinline__ int seq_of_item(const int32_t* cu, int N, int x) {
 // Full blocks are quantised.  The work-group of a sequence's first touched
 // block also keeps the tail as it was for the attention that follows (its
 // rows are that block's earlier tokens) and then writes the new tail, so that
-// no two work-groups touch one tail.
+// no two work-groups touch one tail.  Every work-group notes whether its
+// block's V has a value that is not finite.
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_append(const StepArgs a) {
   constexpr int kLd = 72;  // V^T row in LDS: 64 keys and 16 bytes, rows start in different banks
@@ -162,6 +172,16 @@ __global__ __launch_bounds__(256) void k_attn_append(const StepArgs a) {
   const uint16_t* nk = a.k + (int64_t)hk * D;
   const uint16_t* nv = a.v + (int64_t)hk * D;
   const int old = b == first ? ctx & 63 : 0;  // tokens of this block that were there
+  const int64_t from = (int64_t)c0 + (int64_t)b * 64 - ctx;  // packed row of the block's key 0
+  const int keys = min(64, ctx + len - b * 64);
+  bool bad = false;
+  for (int x = tid; x < keys * (D / 8); x += 256) {
+    const int key = x / (D / 8), dim = x % (D / 8) * 8;
+    if (key >= old) bad |= not_finite8(*(const u32x4*)(nv + (from + key) * a.v_stride + dim));
+  }
+  for (int x = tid; x < D * old; x += 256) bad |= (tv[x / old * 64 + x % old] & 0x7f80u) == 0x7f80u;
+  const int any_bad = __syncthreads_or(bad);
+  if (tid == 0) a.bad[(int64_t)blockIdx.x * a.Hk + hk] = any_bad;
 
   if (b == first && old) {
     u32x4* ok = (u32x4*)(a.old_k + ((int64_t)i * a.Hk + hk) * (64 * D));
@@ -171,8 +191,7 @@ __global__ __launch_bounds__(256) void k_attn_append(const StepArgs a) {
       ov[x] = ((const u32x4*)tv)[x];
     }
   }
-  if ((int64_t)(b + 1) * 64 <= (int64_t)ctx + len) {  // full now
-    const int64_t from = (int64_t)c0 + (int64_t)b * 64 - ctx;  // packed row of the block's key 0
+  if (keys == 64) {  // full now
     for (int x = tid; x < 64 * D / 8; x += 256) {
       const int key = x / (D / 8), dim = x % (D / 8) * 8;
       if (key < old) continue;

@@ -85,26 +85,59 @@ __device__ __forceinline__ void fold_weights(float& m, float mp, float& a, float
 // prefill
 
 // Rows of a (sequence, key/value head): row r is token r / G, query head
-// hk G + r % G.  A work-group of 8 waves takes 8 * 16 * RT of them, a wave 16
-// RT, and all of it walks the keys together: a tile is converted to bf16 once
-// per work-group into LDS, in the order the MFMA operands are read
-// (conflict-free, 16 bytes per lane), while the bytes of the next one are in
-// flight from memory.
+// hk G + r % G.  A work-group takes kRows of them, a wave 16 kRT, and all of it
+// walks the keys together: a tile is converted to bf16 once per work-group
+// into LDS, in the order the MFMA operands are read (conflict-free, 16
+// bytes per lane), while the bytes of the next one are in flight from memory.
+//
+// The 8-bit blocks come first, all in one loop (those from the work-group's
+// first own block on are masked per row), then the rows' own blocks, kRaw of
+// them staged at once, so that every wave does its own without waiting for
+// the others'.
 template <int D>
 struct PrefillTile {
-  static constexpr int kRT = D == 256 ? 1 : 2;  // d = 256: the accumulators of two row tiles would not fit
-  static constexpr int kRows = 8 * 16 * kRT;
+  static constexpr int kRT = D == 256 ? 1 : 2;   // 16-row tiles of a wave
+  static constexpr int kWaves = 8;
+  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int kRows = 16 * kRT * kWaves;
   static constexpr int kFrags = 4 * (D / 32);    // 1 KiB each, K; as many for V
   static constexpr int kUnits = 4 * (D / 64);    // 1 KiB loads of an 8-bit block, K; as many for V
-  static constexpr int kPer = kUnits < 8 ? 1 : kUnits / 8;  // per wave
+  static constexpr bool kSplit = kUnits < kWaves;  // d = 64: half of the waves load K, half V
+  static constexpr int kPer = kSplit ? 1 : kUnits / kWaves;  // units of a wave, K and V each
+  static constexpr int kRaw = D == 64 ? 4 : 2;  // LDS buffers
+  // dim tiles of the folded total that are kept in LDS (each thread its own), for want of registers
+  static constexpr int kOtLds = D == 128 ? 4 : 0;
 };
 
 template <int D>
 struct PrefillLds {
   u32x4 k[PrefillTile<D>::kFrags * 64];
   u32x4 v[PrefillTile<D>::kFrags * 64];
-  uint64_t bad[8];  // per staging wave: the keys with a V that is no finite number (masked tiles only)
 };
+
+// Where V's fragment (dt, h) keeps a lane's 16 bytes: rows change places by dt in
+// groups of four, so that writing four keys of neighbouring dims (own blocks) spreads over the banks.
+__device__ __forceinline__ int v_slot(int dt, int h, int lane) { return (dt * 2 + h) * 64 + (lane ^ (dt & 3)); }
+
+// Pool blocks and scales of 64 blocks of a row at a time, one per lane: the
+// loop over the blocks then waits for none of the two dependent loads.
+struct BlockRun {
+  int id;
+  float ks, vs;
+};
+
+__device__ __forceinline__ BlockRun load_run(const StepArgs& a, int row, int hk, int b, int lane) {
+  BlockRun x;
+  x.id = pool_block(a, row, b + lane);
+  const int64_t at = (int64_t)x.id * a.Hk + hk;
+  x.ks = a.cache.k_scale[at];
+  x.vs = a.cache.v_scale[at];
+  return x;
+}
+
+__device__ __forceinline__ float lane_of(float x, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
 
 template <int D>
 struct Bytes {  // a wave's share of an 8-bit block in flight
@@ -113,18 +146,21 @@ struct Bytes {  // a wave's share of an 8-bit block in flight
 };
 
 template <int D>
-__device__ __forceinline__ void load_block(const StepArgs& a, int row, int hk, int b, Bytes<D>& y, int wave, int lane) {
+__device__ __forceinline__ void load_block(const StepArgs& a, const BlockRun& run, int hk, int b, Bytes<D>& y, int wave,
+                                           int lane) {
   typedef PrefillTile<D> P;
   const int r = lane & 15, g = lane >> 4;
-  const int64_t at = (int64_t)pool_block(a, row, b) * a.Hk + hk;
-  y.ks = a.cache.k_scale[at];
-  y.vs = a.cache.v_scale[at];
+  const int64_t at = (int64_t)__builtin_amdgcn_readlane(run.id, b & 63) * a.Hk + hk;
+  y.ks = lane_of(run.ks, b & 63);
+  y.vs = lane_of(run.vs, b & 63);
 #pragma unroll
   for (int n = 0; n < P::kPer; ++n) {
-    const int unit = wave + 8 * n;  // d = 64: waves 4..7 repeat units 0..3
-    const int sub = unit & 3, kp = (unit >> 2) % (D / 64), dt = unit % (D / 16);
-    y.k[n] = *(const u32x4*)(a.cache.k8 + at * (64 * D) + kp * 4096 + key_of(sub, r) * 64 + g * 16);
-    y.v[n] = *(const u32x4*)(a.cache.v8 + at * (64 * D) + (dt * 16 + r) * 64 + g * 16);
+    const int unit = (wave + P::kWaves * n) % P::kUnits;
+    const int sub = unit & 3, kp = unit >> 2;
+    if (!P::kSplit || wave < P::kUnits)
+      y.k[n] = *(const u32x4*)(a.cache.k8 + at * (64 * D) + kp * 4096 + key_of(sub, r) * 64 + g * 16);
+    if (!P::kSplit || wave >= P::kUnits)
+      y.v[n] = *(const u32x4*)(a.cache.v8 + at * (64 * D) + (unit * 16 + r) * 64 + g * 16);
   }
 }
 
@@ -150,157 +186,175 @@ __device__ __forceinline__ u32x4 drop_keys(u32x4 v, uint64_t drop, int g, int h)
 }
 
 template <int D>
-__device__ __forceinline__ void store_block(const Bytes<D>& y, PrefillLds<D>& sm, int wave, int lane, bool masked) {
+__device__ __forceinline__ void store_block(const Bytes<D>& y, PrefillLds<D>& sm, int wave, int lane) {
   typedef PrefillTile<D> P;
-  if (masked) {
-    uint32_t nan16 = 0;
+#pragma unroll
+  for (int n = 0; n < P::kPer; ++n) {
+    const int unit = (wave + P::kWaves * n) % P::kUnits;
+    const int sub = unit & 3, kp = unit >> 2;
+    u32x4 lo, hi;
+    if (!P::kSplit || wave < P::kUnits) {
+      from_e4m3(y.k[n], y.ks, lo, hi);
+      sm.k[(sub * (D / 32) + 2 * kp) * 64 + lane] = lo;
+      sm.k[(sub * (D / 32) + 2 * kp + 1) * 64 + lane] = hi;
+    }
+    if (!P::kSplit || wave >= P::kUnits) {
+      from_e4m3(y.v[n], y.vs, lo, hi);
+      sm.v[v_slot(unit, 0, lane)] = lo;
+      sm.v[v_slot(unit, 1, lane)] = hi;
+    }
+  }
+}
+
+// The keys of this wave's share of V that are not finite.
+template <int D>
+__device__ __forceinline__ uint64_t bad_in_block(const Bytes<D>& y, int wave) {
+  typedef PrefillTile<D> P;
+  uint32_t nan16 = 0;
+  if (!P::kSplit || wave >= P::kUnits) {
 #pragma unroll
     for (int n = 0; n < P::kPer; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) nan16 |= ((y.v[n][e >> 2] >> (8 * (e & 3))) & 0x7f) == 0x7f ? 1u << e : 0u;
-    const uint64_t bad = bad_keys(nan16);
-    if (lane == 0) sm.bad[wave] = bad;
   }
-#pragma unroll
-  for (int n = 0; n < P::kPer; ++n) {
-    const int unit = wave + 8 * n;
-    if (unit >= P::kUnits) continue;
-    const int sub = unit & 3, kp = unit >> 2;
-    u32x4 lo, hi;
-    from_e4m3(y.k[n], y.ks, lo, hi);
-    sm.k[(sub * (D / 32) + 2 * kp) * 64 + lane] = lo;
-    sm.k[(sub * (D / 32) + 2 * kp + 1) * 64 + lane] = hi;
-    from_e4m3(y.v[n], y.vs, lo, hi);
-    sm.v[(unit * 2) * 64 + lane] = lo;
-    sm.v[(unit * 2 + 1) * 64 + lane] = hi;
-  }
+  return bad_keys(nan16);
 }
 
 // A block in the input type: the call's tokens, and the tail as it was for
-// the ones before.  Past the sequence's end: zeros.
+// the ones before.  Past the sequence's end: zeros.  K goes as it is; of V a
+// thread takes four keys of four dims and writes them turned.  Returns the
+// wave's keys with a V that is not finite.
 template <int D>
-__device__ __forceinline__ void stage_raw(const StepArgs& a, int i, int hk, int ctx, int end, int c0, int b,
-                                          PrefillLds<D>& sm, int wave, int lane) {
+__device__ __forceinline__ uint64_t stage_raw(const StepArgs& a, int i, int hk, int ctx, int end, int c0, int b,
+                                              PrefillLds<D>& sm, int wave, int lane) {
   typedef PrefillTile<D> P;
+  constexpr int NK = (P::kUnits + P::kWaves - 1) / P::kWaves, NV = (64 / 4) * (D / 4) / P::kThreads;
   const int r = lane & 15, g = lane >> 4;
   const int64_t tail = ((int64_t)i * a.Hk + hk) * (64 * D);
   const int64_t from = (int64_t)c0 - ctx;
-  uint32_t nan16 = 0;
-#pragma unroll 1
-  for (int unit = wave; unit < P::kUnits; unit += 8) {
-    const int sub = unit & 3, kp = unit >> 2, key = key_of(sub, r), p = b * 64 + key;
-    u32x4 lo = {0, 0, 0, 0}, hi = lo;
-    if (p < end) {
-      const uint16_t* src = (p >= ctx ? a.k + (from + p) * a.k_stride + (int64_t)hk * D : a.old_k + tail + key * D) + kp * 64 + g * 16;
-      lo = *(const u32x4*)src;
-      hi = *(const u32x4*)(src + 8);
-    }
-    sm.k[(sub * (D / 32) + 2 * kp) * 64 + lane] = lo;
-    sm.k[(sub * (D / 32) + 2 * kp + 1) * 64 + lane] = hi;
-    const int dim = unit * 16 + r;
-    uint32_t x[16];
+  u32x4 lo[NK], hi[NK];
+  u32x2 x[NV < 1 ? 1 : NV][4];
+  constexpr int NVR = NV < 1 ? 1 : NV;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int pv = b * 64 + g * 16 + j;
-      x[j] = 0;
-      if (pv < end)
-        x[j] = *(pv >= ctx ? a.v + (from + pv) * a.v_stride + (int64_t)hk * D + dim : a.old_v + tail + dim * 64 + (pv & 63));
-      nan16 |= (x[j] & 0x7f80u) == 0x7f80u ? 1u << j : 0u;
+  for (int n = 0; n < NK; ++n) {
+    const int unit = wave + P::kWaves * n, sub = unit & 3, kp = unit >> 2, key = key_of(sub, r), p = b * 64 + key;
+    lo[n] = hi[n] = u32x4{0, 0, 0, 0};
+    if (unit < P::kUnits && p < end) {
+      const uint16_t* src = (p >= ctx ? a.k + (from + p) * a.k_stride + (int64_t)hk * D : a.old_k + tail + key * D) + kp * 64 + g * 16;
+      lo[n] = *(const u32x4*)src;
+      hi[n] = *(const u32x4*)(src + 8);
     }
+  }
+  uint64_t bad = 0;
+#pragma unroll
+  for (int n = 0; n < NVR; ++n) {
+    const int it = wave * 64 + lane + P::kThreads * n, kq = it / (D / 4), dim = it % (D / 4) * 4;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      lo[j] = x[2 * j] | x[2 * j + 1] << 16;
-      hi[j] = x[8 + 2 * j] | x[8 + 2 * j + 1] << 16;
+      const int key = 4 * kq + j, p = b * 64 + key;
+      x[n][j] = u32x2{0, 0};
+      if (kq < 16 && p < end) {
+        if (p >= ctx) {
+          x[n][j] = *(const u32x2*)(a.v + (from + p) * a.v_stride + (int64_t)hk * D + dim);
+        } else {
+          const uint16_t* tv = a.old_v + tail + dim * 64 + key;
+          x[n][j] = u32x2{tv[0] | (uint32_t)tv[64] << 16, tv[128] | (uint32_t)tv[192] << 16};
+        }
+      }
     }
-    sm.v[(unit * 2) * 64 + lane] = lo;
-    sm.v[(unit * 2 + 1) * 64 + lane] = hi;
   }
-  const uint64_t bad = bad_keys(nan16);
-  if (lane == 0) sm.bad[wave] = bad;
+#pragma unroll
+  for (int n = 0; n < NK; ++n) {
+    const int unit = wave + P::kWaves * n, sub = unit & 3, kp = unit >> 2;
+    if (unit < P::kUnits) {
+      sm.k[(sub * (D / 32) + 2 * kp) * 64 + lane] = lo[n];
+      sm.k[(sub * (D / 32) + 2 * kp + 1) * 64 + lane] = hi[n];
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NVR; ++n) {
+    const int it = wave * 64 + lane + P::kThreads * n, kq = it / (D / 4), dim = it % (D / 4) * 4;
+    uint32_t nan4 = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w0 = x[n][j][0] & 0x7f807f80u, w1 = x[n][j][1] & 0x7f807f80u;
+      if ((w0 & 0xffffu) == 0x7f80u || w0 >> 16 == 0x7f80u || (w1 & 0xffffu) == 0x7f80u || w1 >> 16 == 0x7f80u) nan4 |= 1u << j;
+    }
+    if (__any(nan4 != 0)) {
+      uint64_t m = kq < 16 ? (uint64_t)nan4 << (4 * kq) : 0;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) m |= (uint64_t)__shfl_xor((long long)m, o);
+      bad |= m;
+    }
+    if (kq < 16) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // dim + e of the four keys
+        const uint32_t w0 = x[n][0][e >> 1], w1 = x[n][1][e >> 1], w2 = x[n][2][e >> 1], w3 = x[n][3][e >> 1];
+        const u32x2 t = e & 1 ? u32x2{w0 >> 16 | (w1 & 0xffff0000u), w2 >> 16 | (w3 & 0xffff0000u)}
+                              : u32x2{(w0 & 0xffffu) | w1 << 16, (w2 & 0xffffu) | w3 << 16};
+        const int dd = dim + e;
+        ((u32x2*)&sm.v[v_slot(dd >> 4, (kq >> 1) & 1, (kq >> 2) * 16 + (dd & 15))])[kq & 1] = t;
+      }
+    }
+  }
+  return bad;
 }
 
-template <int D>
-__global__ __launch_bounds__(512) void k_attn_prefill(const StepArgs a) {
+// A work-group's rows [row0, row0 + kRows) of sequence i.  SLOW: a block that is
+// masked for some of them holds a V that is not finite.
+template <int D, bool SLOW>
+__device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* sm, f32x4 (*s_ot)[PrefillTile<D>::kThreads],
+                                             uint64_t (*s_bad)[PrefillTile<D>::kWaves],
+                                             int hk, int i, int cache_row, uint32_t row0, uint32_t rows, int c0, int ctx,
+                                             int end) {
   typedef PrefillTile<D> P;
   constexpr int RT = P::kRT, KS = D / 32, DT = D / 16;
-  __shared__ PrefillLds<D> sm[2];
-  const int hk = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-
-  // which sequence and rows: sequence i has the row-tile slots floor(cu[i] G / kRows) + i ..
-  const int item = gridDim.x - 1 - blockIdx.x;  // later rows, which see more keys, first
-  int lo = 0, hi = a.N - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((int)((int64_t)a.cu[mid] * a.G / P::kRows) + mid <= item)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  const int i = lo, c0 = a.cu[i], len = a.cu[i + 1] - c0;
-  const int64_t row0 = (int64_t)(item - ((int)((int64_t)c0 * a.G / P::kRows) + i)) * P::kRows;
-  const int64_t rows = (int64_t)len * a.G;
-  if (row0 >= rows) return;
-  const int ctx = a.ctx_len[i], cache_row = row_of(a.slot, i, a.cache.num_slots);
-  const bool on = ctx >= 0 && cache_row >= 0;
-  const int end = ctx + len;
-
-  // this lane's rows: their token, head and position
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const uint32_t G = (uint32_t)a.G, last_row = min(row0 + P::kRows, rows) - 1;
+  const uint32_t w0 = row0 + wave * RT * 16;
+  u32x4 q[RT][KS];
   int pos[RT];
-  int64_t qat[RT], oat[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    const int64_t row = row0 + (wave * RT + t) * 16 + r, in = row < rows ? row : rows - 1;
-    const int token = (int)(in / a.G), head = hk * a.G + (int)(in % a.G);
+    const uint32_t row = min(w0 + t * 16 + r, rows - 1);
+    const int token = (int)(row / G), head = hk * a.G + (int)(row % G);
     pos[t] = ctx + token;
-    qat[t] = (int64_t)(c0 + token) * a.q_stride + (int64_t)head * D;
-    oat[t] = row < rows ? ((int64_t)(c0 + token) * a.H + head) * D : -1;
+    const uint16_t* qp = a.q + (int64_t)(c0 + token) * a.q_stride + (int64_t)head * D;
+#pragma unroll
+    for (int x = 0; x < KS; ++x) q[t][x] = *(const u32x4*)(qp + (x >> 1) * 64 + g * 16 + (x & 1) * 8);
   }
-  if (!on) {  // refused: o = 0
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-      if (oat[t] >= 0)
-        for (int x = 0; x < DT; ++x) *(u32x2*)(a.o + oat[t] + x * 16 + g * 4) = u32x2{0, 0};
-    return;
-  }
-  u32x4 q[RT][KS];
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int x = 0; x < KS; ++x) q[t][x] = *(const u32x4*)(a.q + qat[t] + (x >> 1) * 64 + g * 16 + (x & 1) * 8);
+  // own blocks: of the work-group's rows and of this wave's
+  const int b_lo = (ctx + (int)(row0 / G)) >> 6, b_hi = (ctx + (int)(last_row / G)) >> 6;
+  const bool has = w0 <= last_row;
+  const int w_lo = (ctx + (int)(min(w0, last_row) / G)) >> 6;
+  const int w_hi = (ctx + (int)(min(w0 + RT * 16 - 1, last_row) / G)) >> 6;
 
-  // blocks: of the work-group's rows and of this wave's
-  const int64_t last_row = min(row0 + P::kRows, rows) - 1;
-  const int b_lo = (ctx + (int)(row0 / a.G)) >> 6, b_hi = (ctx + (int)(last_row / a.G)) >> 6;
-  const int64_t w0 = row0 + wave * RT * 16;
-  const bool has = w0 < rows;
-  const int w_lo = (ctx + (int)(min(w0, rows - 1) / a.G)) >> 6;
-  const int w_hi = (ctx + (int)(min(w0 + RT * 16 - 1, rows - 1) / a.G)) >> 6;
-
-  f32x4 O[RT][DT], Ot[RT][DT];
+  constexpr int OL = P::kOtLds, OR = DT - OL;
+  f32x4 O[RT][DT], Ot[RT][OR];
   float m[RT], l[RT], mt[RT], lt[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     m[t] = mt[t] = kNegInf;
     l[t] = lt[t] = 0.f;
 #pragma unroll
-    for (int x = 0; x < DT; ++x) O[t][x] = Ot[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < DT; ++x) O[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int x = 0; x < DT; ++x) (x < OR ? Ot[t][x < OR ? x : 0] : s_ot[t * OL + x - OR][threadIdx.x]) = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
   // one tile from LDS; MASKED: rows see keys up to upto[t] of it
-  auto tile = [&](auto masked_, const PrefillLds<D>& s_, const int (&upto)[RT]) {
+  auto tile = [&](auto masked_, int buf, const int (&upto)[RT]) {
     constexpr bool MASKED = decltype(masked_)::value;
+    const PrefillLds<D>& s_ = sm[buf];
     f32x4 s[RT][4];
 #pragma unroll
-    for (int sub = 0; sub < 4; ++sub) {
+    for (int x = 0; x < KS; ++x)  // sub-tiles inside: neighbouring MFMAs do not wait for each other
 #pragma unroll
-      for (int t = 0; t < RT; ++t) s[t][sub] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int x = 0; x < KS; ++x) {
+      for (int sub = 0; sub < 4; ++sub) {
         const u32x4 kf = s_.k[(sub * KS + x) * 64 + lane];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) s[t][sub] = mma(kf, q[t][x], s[t][sub]);
+        for (int t = 0; t < RT; ++t) s[t][sub] = mma(kf, q[t][x], x ? s[t][sub] : f32x4{0.f, 0.f, 0.f, 0.f});
       }
-    }
     u32x4 p[RT][2];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -319,23 +373,21 @@ __global__ __launch_bounds__(512) void k_attn_prefill(const StepArgs a) {
         for (int x = 0; x < DT; ++x) O[t][x] *= alpha;
       }
     }
-    uint64_t bad = 0;
-    if (MASKED) {
+    if (!(MASKED && SLOW)) {
 #pragma unroll
-      for (int w = 0; w < 8; ++w) bad |= s_.bad[w];
-    }
-    if (!MASKED || bad == 0) {
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int x = 0; x < DT; ++x)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32x4 vf = s_.v[(x * 2 + h) * 64 + lane];
+        for (int x = 0; x < DT; ++x) {
+          const u32x4 vf = s_.v[v_slot(x, h, lane)];
 #pragma unroll
           for (int t = 0; t < RT; ++t) O[t][x] = mma(vf, p[t][h], O[t][x]);
         }
     } else {
-      // one product for every number n of such keys that a row may see: the
-      // first n stay, the others are zero; a row takes its own
+      // keys with a V that is not finite: one product for every number n of
+      // them that a row may see, the first n as they are, the others zero; a row takes its own
+      uint64_t bad = 0;
+#pragma unroll
+      for (int w = 0; w < P::kWaves; ++w) bad |= s_bad[buf][w];
       int sees[RT];
 #pragma unroll
       for (int t = 0; t < RT; ++t) sees[t] = upto[t] < 0 ? 0 : __popcll(bad & (~0ull >> (63 - upto[t])));
@@ -347,7 +399,8 @@ __global__ __launch_bounds__(512) void k_attn_prefill(const StepArgs a) {
         uint64_t drop = bad;
 #pragma unroll 1
         for (int n = 0; n <= __popcll(bad); ++n, drop &= drop - 1) {
-          const u32x4 v0 = drop_keys(s_.v[(x * 2) * 64 + lane], drop, g, 0), v1 = drop_keys(s_.v[(x * 2 + 1) * 64 + lane], drop, g, 1);
+          const u32x4 v0 = drop_keys(s_.v[v_slot(x, 0, lane)], drop, g, 0);
+          const u32x4 v1 = drop_keys(s_.v[v_slot(x, 1, lane)], drop, g, 1);
 #pragma unroll
           for (int t = 0; t < RT; ++t) {
             const f32x4 y_ = mma(v1, p[t][1], mma(v0, p[t][0], base[t]));
@@ -358,10 +411,11 @@ __global__ __launch_bounds__(512) void k_attn_prefill(const StepArgs a) {
       }
     }
   };
-  // the end of a partition
-  auto fold = [&]() {
+  // the end of a partition; rows whose own block is in it go on (MASKED)
+  auto fold = [&](auto masked_, int b) {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
+      if (decltype(masked_)::value && b >= pos[t] >> 6) continue;
       float wa, wb;
       fold_weights(mt[t], m[t], wa, wb);
       lt[t] = __builtin_fmaf(l[t], wb, lt[t] * wa);
@@ -369,70 +423,145 @@ __global__ __launch_bounds__(512) void k_attn_prefill(const StepArgs a) {
       l[t] = 0.f;
 #pragma unroll
       for (int x = 0; x < DT; ++x) {
+        f32x4& to = x < OR ? Ot[t][x < OR ? x : 0] : s_ot[t * OL + x - OR][threadIdx.x];
+        f32x4 y_ = to;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) Ot[t][x][e] = __builtin_fmaf(O[t][x][e], wb, Ot[t][x][e] * wa);
+        for (int e = 0; e < 4; ++e) y_[e] = __builtin_fmaf(O[t][x][e], wb, y_[e] * wa);
+        to = y_;
         O[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
     }
   };
+
+  // the 8-bit blocks that every row sees
+  Bytes<D> y;
+  BlockRun run;
+  auto fetch = [&](int b) {
+    if ((b & 63) == 0) run = load_run(a, cache_row, hk, b, lane);
+    load_block<D>(a, run, hk, b, y, wave, lane);
+  };
   int upto[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) upto[t] = 63;
-
-  // 8-bit blocks that every row sees in full
-  Bytes<D> y;
-  if (b_lo > 0) {
-    load_block<D>(a, cache_row, hk, 0, y, wave, lane);
-    store_block<D>(y, sm[0], wave, lane, false);
-    if (b_lo > 1) load_block<D>(a, cache_row, hk, 1, y, wave, lane);
-    __syncthreads();
+  if (b_hi > 0) {
+    fetch(0);
+    store_block<D>(y, sm[0], wave, lane);
+    if (SLOW && b_lo == 0) {
+      const uint64_t bad = bad_in_block<D>(y, wave);
+      if (lane == 0) s_bad[0][wave] = bad;
+    }
+    if (b_hi > 1) fetch(1);
   }
+  __syncthreads();
 #pragma unroll 1
   for (int b = 0; b < b_lo; ++b) {
-    if (b + 1 < b_lo) store_block<D>(y, sm[(b + 1) & 1], wave, lane, false);
-    if (b + 2 < b_lo) load_block<D>(a, cache_row, hk, b + 2, y, wave, lane);
-    if (has) {
-      tile(std::false_type{}, sm[b & 1], upto);
-      if ((b + 1) % kPartBlocks == 0) fold();
-    }
-    __syncthreads();
-  }
-  // then, for every b from b_lo on, block b in the input type (for its own
-  // rows) and in 8 bits (for later ones).  A barrier a tile: a buffer is
-  // written again after the barrier of the tile between.
-#pragma unroll 1
-  for (int j = 0; j <= 2 * (b_hi - b_lo); ++j) {
-    const int b = b_lo + (j >> 1);
-    const bool raw = (j & 1) == 0;
-    PrefillLds<D>& s_ = sm[j & 1];
-    if (raw) {
-      stage_raw<D>(a, i, hk, ctx, end, c0, b, s_, wave, lane);
-    } else {
-      load_block<D>(a, cache_row, hk, b, y, wave, lane);
-      store_block<D>(y, s_, wave, lane, true);
-    }
-    __syncthreads();
-    if (!has) continue;
-    if (raw ? b >= w_lo && b <= w_hi : b < w_hi) {
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const int own = pos[t] >> 6;
-        upto[t] = raw ? (own == b ? pos[t] & 63 : -1) : (b < own ? 63 : -1);
+    if (b + 1 < b_hi) {
+      store_block<D>(y, sm[(b + 1) & 1], wave, lane);
+      if (SLOW && b + 1 == b_lo) {
+        const uint64_t bad = bad_in_block<D>(y, wave);
+        if (lane == 0) s_bad[(b + 1) & 1][wave] = bad;
       }
-      tile(std::true_type{}, s_, upto);
     }
-    if (!raw && (b + 1) % kPartBlocks == 0) fold();
+    if (b + 2 < b_hi) fetch(b + 2);
+    if (has) tile(std::false_type{}, b & 1, upto);
+    if ((b + 1) % kPartBlocks == 0) fold(std::false_type{}, b);
+    __syncthreads();
   }
-  fold();
+  // those that only later rows see
+#pragma unroll 1
+  for (int b = b_lo; b < b_hi; ++b) {
+    if (b + 1 < b_hi) {
+      store_block<D>(y, sm[(b + 1) & 1], wave, lane);
+      if (SLOW) {
+        const uint64_t bad = bad_in_block<D>(y, wave);
+        if (lane == 0) s_bad[(b + 1) & 1][wave] = bad;
+      }
+    }
+    if (b + 2 < b_hi) fetch(b + 2);
+    if (has && b < w_hi) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) upto[t] = b < pos[t] >> 6 ? 63 : -1;
+      tile(std::true_type{}, b & 1, upto);
+    }
+    if ((b + 1) % kPartBlocks == 0) fold(std::true_type{}, b);
+    __syncthreads();
+  }
+  // the own blocks
+#pragma unroll 1
+  for (int b0 = b_lo; b0 <= b_hi; b0 += P::kRaw) {
+    if (b0 > b_lo) __syncthreads();
+#pragma unroll 1
+    for (int n = 0; n < P::kRaw && b0 + n <= b_hi; ++n) {
+      const uint64_t bad = stage_raw<D>(a, i, hk, ctx, end, c0, b0 + n, sm[n], wave, lane);
+      if (SLOW && lane == 0) s_bad[n][wave] = bad;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int n = 0; has && n < P::kRaw; ++n) {
+      const int b = b0 + n;
+      if (b < w_lo || b > w_hi) continue;
+#pragma unroll
+      for (int t = 0; t < RT; ++t) upto[t] = pos[t] >> 6 == b ? pos[t] & 63 : -1;
+      tile(std::true_type{}, n, upto);
+    }
+  }
+  fold(std::false_type{}, 0);
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const float inv = 1.f / sum_over_groups(lt[t]);
-    if (oat[t] < 0) continue;
+    const uint32_t row = w0 + t * 16 + r;
+    if (row >= rows) continue;
+    uint16_t* o = a.o + ((int64_t)(c0 + (int)(row / G)) * a.H + hk * a.G + (int)(row % G)) * D + g * 4;
 #pragma unroll
-    for (int x = 0; x < DT; ++x)
-      *(u32x2*)(a.o + oat[t] + x * 16 + g * 4) =
-          u32x2{pack2(Ot[t][x][0] * inv, Ot[t][x][1] * inv), pack2(Ot[t][x][2] * inv, Ot[t][x][3] * inv)};
+    for (int x = 0; x < DT; ++x) {
+      const f32x4 y_ = x < OR ? Ot[t][x < OR ? x : 0] : s_ot[t * OL + x - OR][threadIdx.x];
+      *(u32x2*)(o + x * 16) = u32x2{pack2(y_[0] * inv, y_[1] * inv), pack2(y_[2] * inv, y_[3] * inv)};
+    }
   }
+}
+
+template <int D>
+__global__ __launch_bounds__(PrefillTile<D>::kThreads) void k_attn_prefill(const StepArgs a) {
+  typedef PrefillTile<D> P;
+  __shared__ PrefillLds<D> sm[P::kRaw];
+  __shared__ f32x4 s_ot[P::kOtLds ? P::kRT * P::kOtLds : 1][P::kThreads];
+  __shared__ uint64_t s_bad[P::kRaw][P::kWaves];
+  // neighbouring work-groups take different heads: with 2, 4, 8 .. heads each
+  // chiplet, and its L2, sees the keys of some of them only
+  const int hk = blockIdx.x % a.Hk;
+  // which sequence and rows: sequence i has the row-tile slots floor(cu[i] G / kRows) + i ..
+  const int item = (int)((gridDim.x - 1 - blockIdx.x) / a.Hk);  // later rows, which see more keys, first
+  int lo = 0, hi = a.N - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((int)((int64_t)a.cu[mid] * a.G / P::kRows) + mid <= item)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int i = lo, c0 = a.cu[i], len = a.cu[i + 1] - c0;
+  const int64_t row0 = (int64_t)(item - ((int)((int64_t)c0 * a.G / P::kRows) + i)) * P::kRows;
+  const int64_t rows = (int64_t)len * a.G;
+  if (row0 >= rows) return;
+  const int ctx = a.ctx_len[i], cache_row = row_of(a.slot, i, a.cache.num_slots);
+  if (ctx < 0 || cache_row < 0) {  // refused: o = 0
+    const int n = (int)min(rows - row0, (int64_t)P::kRows);
+    for (int x = threadIdx.x; x < n * (D / 8); x += P::kThreads) {
+      const uint32_t row = (uint32_t)row0 + x / (D / 8);
+      u32x4* o = (u32x4*)(a.o + ((int64_t)(c0 + (int)(row / a.G)) * a.H + hk * a.G + (int)(row % a.G)) * D);
+      o[x % (D / 8)] = u32x4{0, 0, 0, 0};
+    }
+    return;
+  }
+  // does one of the rows' own blocks hold a V that is not finite?
+  const int b_lo = (ctx + (int)((uint32_t)row0 / (uint32_t)a.G)) >> 6;
+  const int b_hi = (ctx + (int)((uint32_t)(min(row0 + P::kRows, rows) - 1) / (uint32_t)a.G)) >> 6;
+  int bad = 0;
+  for (int b = b_lo; b <= b_hi; ++b) bad |= a.bad[(int64_t)((c0 >> 6) + 2 * i + b - (ctx >> 6)) * a.Hk + hk];
+  if (bad == 0)
+    prefill_rows<D, false>(a, sm, s_ot, s_bad, hk, i, cache_row, (uint32_t)row0, (uint32_t)rows, c0, ctx, ctx + len);
+  else
+    prefill_rows<D, true>(a, sm, s_ot, s_bad, hk, i, cache_row, (uint32_t)row0, (uint32_t)rows, c0, ctx, ctx + len);
 }
 
 // ---------------------------------------------------------------------------

@@ -340,12 +340,16 @@ extern "C" gdn_status gdn_attn_qk_norm_rope_bwd(const gdn_attn_shape* shape, con
 namespace {
 
 struct PrefillLayout {
-  size_t old_k, old_v, total;
+  size_t old_k, old_v, bad, total;
 };
 
-PrefillLayout prefill_layout(const gdn_attn_shape& s, int32_t N) {
+// work items of the append: room for every block that the tokens can touch
+int64_t touched_blocks(int32_t N, int64_t T) { return T / kBlock + 2 * (int64_t)N; }
+
+PrefillLayout prefill_layout(const gdn_attn_shape& s, int32_t N, int64_t T) {
   const size_t tail = align_up((size_t)N * kv_heads(s) * kBlock * s.head_dim * sizeof(uint16_t));
-  return {0, tail, 2 * tail};
+  const size_t bad = align_up((size_t)touched_blocks(N, T) * kv_heads(s) * sizeof(int32_t));
+  return {0, tail, 2 * tail, 2 * tail + bad};
 }
 
 struct DecodeLayout {
@@ -448,7 +452,7 @@ gdn_status check_workspace(const char* fn, const void* workspace, size_t bytes, 
 
 template <int D>
 void run_append(const StepArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL(k_attn_append<D>, dim3(a.T / kBlock + 2 * a.N, a.Hk), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_attn_append<D>, dim3((unsigned)touched_blocks(a.N, a.T), a.Hk), dim3(256), 0, st, a);
 }
 
 template <int D>
@@ -456,7 +460,7 @@ gdn_status run_prefill(const StepArgs& a, hipStream_t st, const char* fn) {
   typedef PrefillTile<D> P;
   run_append<D>(a, st);
   const int64_t tiles = (int64_t)a.T * a.G / P::kRows + a.N;
-  hipLaunchKernelGGL(k_attn_prefill<D>, dim3((unsigned)tiles, a.Hk), dim3(512), 0, st, a);
+  hipLaunchKernelGGL(k_attn_prefill<D>, dim3((unsigned)(tiles * a.Hk)), dim3(P::kThreads), 0, st, a);
   return launch_status(fn);
 }
 
@@ -484,11 +488,12 @@ extern "C" gdn_status gdn_attn_prefill(const gdn_attn_shape* shape, int32_t num_
   if (max_new < 0) return fail(GDN_ERR_INVALID_ARG, "%s: max_new is negative", fn);
   CHECK_PTR(cu_seqlens, "cu_seqlens");
   if (total_tokens == 0) return done();
-  const PrefillLayout L = prefill_layout(*shape, num_seqs);
+  const PrefillLayout L = prefill_layout(*shape, num_seqs, total_tokens);
   CHECK(check_workspace(fn, workspace, workspace_bytes, L.total));
   a.cu = cu_seqlens;
   a.old_k = (uint16_t*)((char*)workspace + L.old_k);
   a.old_v = (uint16_t*)((char*)workspace + L.old_v);
+  a.bad = (int32_t*)((char*)workspace + L.bad);
   switch (shape->head_dim) {
     case 64: return run_prefill<64>(a, (hipStream_t)stream, fn);
     case 128: return run_prefill<128>(a, (hipStream_t)stream, fn);
@@ -534,7 +539,7 @@ extern "C" gdn_status gdn_attn_cache_read(const gdn_attn_shape* shape, int32_t n
   StepArgs a{};
   fill_cache(a, *shape, num_seqs, total_tokens, *step, *cache);
   a.cu = cu_seqlens;
-  const dim3 grid(a.T / kBlock + 2 * a.N, a.Hk);
+  const dim3 grid((unsigned)touched_blocks(a.N, a.T), a.Hk);
   switch (shape->head_dim) {
     case 64:
       hipLaunchKernelGGL(k_attn_cache_read<64>, grid, dim3(256), 0, (hipStream_t)stream, a, (uint16_t*)k_out, (uint16_t*)v_out);
@@ -555,7 +560,7 @@ extern "C" size_t gdn_attn_workspace_size(const gdn_attn_shape* shape, int32_t o
                   check_sizes("gdn_attn_workspace_size", num_seqs, total_tokens) == GDN_OK && num_blocks >= 0;
   gdn_last_error_text() = before;  // a size query is no call
   if (!ok) return 0;
-  if (op == GDN_ATTN_OP_PREFILL) return prefill_layout(*shape, num_seqs).total;
+  if (op == GDN_ATTN_OP_PREFILL) return prefill_layout(*shape, num_seqs, total_tokens).total;
   if (op == GDN_ATTN_OP_DECODE) return decode_layout(*shape, num_seqs, num_blocks).total;
   if (op == GDN_ATTN_OP_NORM_ROPE_BWD)
     return align_up((size_t)norm_bwd_groups(*shape, total_tokens) * 2 * shape->head_dim * sizeof(float));

@@ -29,6 +29,7 @@ struct StepArgs {
   float c;  // softmax scale * log2(e)
   CacheArgs cache;
   uint16_t *old_k, *old_v;  // [N, Hk, 64, d], [N, Hk, d, 64]: the tails as they were before the call
+  uint16_t *raw_k, *raw_v;  // as the old tails, per touched block: those that the call fills, in the input type
   int32_t* bad;             // per touched block and head: does its V hold a value that is not finite?
 };
 
@@ -147,17 +148,39 @@ __device__ __forceinline__ int seq_of_item(const int32_t* cu, int N, int x) {
   return lo;
 }
 
+// Four keys of four dims (two words a key) -> four dims of four keys.
+__device__ __forceinline__ void transpose4(const u32x2 (&x)[4], u32x2 (&t)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t w0 = x[0][e >> 1], w1 = x[1][e >> 1], w2 = x[2][e >> 1], w3 = x[3][e >> 1];
+    t[e] = e & 1 ? u32x2{w0 >> 16 | (w1 & 0xffff0000u), w2 >> 16 | (w3 & 0xffff0000u)}
+                 : u32x2{(w0 & 0xffffu) | w1 << 16, (w2 & 0xffffu) | w3 << 16};
+  }
+}
+
 // Appends a call's tokens: a work-group per (touched block, key/value head).
 // Full blocks are quantised.  The work-group of a sequence's first touched
 // block also keeps the tail as it was for the attention that follows (its
 // rows are that block's earlier tokens) and then writes the new tail, so that
 // no two work-groups touch one tail.  Every work-group notes whether its
 // block's V has a value that is not finite.
+//
+// A block is read once, into registers: K in runs of 8 dims of a key, V in
+// squares of four keys by four dims, which turn over in the thread; only V's
+// bytes go through LDS, to leave in whole lines.
+//
+// RAW: for k_attn_rows, which reads no V by token: the blocks that the call
+// fills, except a sequence's last, are left in raw_k and raw_v in the tail's layout.
 template <int D>
-__global__ __launch_bounds__(256) void k_attn_append(const StepArgs a) {
-  constexpr int kLd = 72;  // V^T row in LDS: 64 keys and 16 bytes, rows start in different banks
-  __shared__ uint16_t vt[D * kLd];
-  __shared__ uint32_t red[4];
+constexpr int kAppendThreads = D == 256 ? 512 : 256;  // a thread's share of a block stays in registers
+
+template <int D, bool RAW>
+__global__ __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4) void k_attn_append(const StepArgs a) {
+  constexpr int TH = kAppendThreads<D>;
+  constexpr int n = 64 * D / 8 / TH, nsq = 64 * D / 16 / TH;  // K runs and V squares of a thread
+  constexpr int kLd = 17;              // words of a dim's 64 bytes in LDS, and one so that dims start in different banks
+  __shared__ uint32_t vt[D * kLd];
+  __shared__ uint32_t red[TH / 64][3];
   const int hk = blockIdx.y, tid = threadIdx.x;
   const int i = seq_of_item(a.cu, a.N, blockIdx.x);
   const int ctx = a.ctx_len[i], c0 = a.cu[i], len = a.cu[i + 1] - c0;
@@ -167,63 +190,155 @@ __global__ __launch_bounds__(256) void k_attn_append(const StepArgs a) {
   if (b > last) return;
   const int row = row_of(a.slot, i, a.cache.num_slots);
   if (row < 0) return;
-  const uint16_t* tk = a.cache.tail_k + ((int64_t)row * a.Hk + hk) * (64 * D);
-  const uint16_t* tv = a.cache.tail_v + ((int64_t)row * a.Hk + hk) * (64 * D);
+  uint16_t* tk = a.cache.tail_k + ((int64_t)row * a.Hk + hk) * (64 * D);
+  uint16_t* tv = a.cache.tail_v + ((int64_t)row * a.Hk + hk) * (64 * D);
   const uint16_t* nk = a.k + (int64_t)hk * D;
   const uint16_t* nv = a.v + (int64_t)hk * D;
   const int old = b == first ? ctx & 63 : 0;  // tokens of this block that were there
   const int64_t from = (int64_t)c0 + (int64_t)b * 64 - ctx;  // packed row of the block's key 0
   const int keys = min(64, ctx + len - b * 64);
-  bool bad = false;
-  for (int x = tid; x < keys * (D / 8); x += 256) {
-    const int key = x / (D / 8), dim = x % (D / 8) * 8;
-    if (key >= old) bad |= not_finite8(*(const u32x4*)(nv + (from + key) * a.v_stride + dim));
-  }
-  for (int x = tid; x < D * old; x += 256) bad |= (tv[x / old * 64 + x % old] & 0x7f80u) == 0x7f80u;
-  const int any_bad = __syncthreads_or(bad);
-  if (tid == 0) a.bad[(int64_t)blockIdx.x * a.Hk + hk] = any_bad;
 
-  if (b == first && old) {
+  // run i: key x / (D / 8), dims 8 (x % (D / 8)) ..; square i: keys 4 (x / (D / 4)) .., dims 4 (x % (D / 4)) ..,
+  // x = thread + TH i
+  u32x4 kx[n];
+  u32x2 vx[nsq][4];
+#pragma unroll
+  for (int j = 0; j < n; ++j) {
+    const int x = tid + TH * j, key = x / (D / 8), dim = x % (D / 8) * 8;
+    kx[j] = u32x4{0, 0, 0, 0};
+    if (key < keys) kx[j] = *(const u32x4*)(key < old ? tk + key * D + dim : nk + (from + key) * a.k_stride + dim);
+  }
+#pragma unroll
+  for (int j = 0; j < nsq; ++j) {
+    const int x = tid + TH * j, key = x / (D / 4) * 4, dim = x % (D / 4) * 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      vx[j][e] = u32x2{0, 0};
+      if (key + e >= keys) continue;
+      if (key + e >= old) {
+        vx[j][e] = *(const u32x2*)(nv + (from + key + e) * a.v_stride + dim);
+      } else {
+        const uint16_t* t = tv + dim * 64 + key + e;
+        vx[j][e] = u32x2{t[0] | (uint32_t)t[64] << 16, t[128] | (uint32_t)t[192] << 16};
+      }
+    }
+  }
+  if (old) {
     u32x4* ok = (u32x4*)(a.old_k + ((int64_t)i * a.Hk + hk) * (64 * D));
     u32x4* ov = (u32x4*)(a.old_v + ((int64_t)i * a.Hk + hk) * (64 * D));
-    for (int x = tid; x < 64 * D / 8; x += 256) {
+    for (int x = tid; x < 64 * D / 8; x += TH) {
       ok[x] = ((const u32x4*)tk)[x];
       ov[x] = ((const u32x4*)tv)[x];
     }
   }
-  if (keys == 64) {  // full now
-    for (int x = tid; x < 64 * D / 8; x += 256) {
-      const int key = x / (D / 8), dim = x % (D / 8) * 8;
-      if (key < old) continue;
-      const u32x4 w = *(const u32x4*)(nv + (from + key) * a.v_stride + dim);
+  uint32_t km = 0, vm = 0, bad = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        vt[(dim + 2 * j) * kLd + key] = (uint16_t)w[j];
-        vt[(dim + 2 * j + 1) * kLd + key] = (uint16_t)(w[j] >> 16);
+  for (int j = 0; j < n; ++j) km = amax8(kx[j], km);
+#pragma unroll
+  for (int j = 0; j < nsq; ++j) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const u32x4 w = {vx[j][e][0], vx[j][e][1], vx[j][e + 1][0], vx[j][e + 1][1]};
+      vm = amax8(w, vm);
+      bad |= not_finite8(w);
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    km = max(km, (uint32_t)__shfl_xor((int)km, o));
+    vm = max(vm, (uint32_t)__shfl_xor((int)vm, o));
+  }
+  bad = __any(bad != 0);
+  if ((tid & 63) == 0) {
+    red[tid >> 6][0] = km;
+    red[tid >> 6][1] = vm;
+    red[tid >> 6][2] = bad;
+  }
+  __syncthreads();  // also: the old tail has been read
+#pragma unroll
+  for (int w = 0; w < TH / 64; ++w) {
+    km = max(km, red[w][0]);
+    vm = max(vm, red[w][1]);
+    bad |= red[w][2];
+  }
+  if (tid == 0) a.bad[(int64_t)blockIdx.x * a.Hk + hk] = bad;
+
+  if (keys == 64) {  // full now
+    const int64_t at = (int64_t)pool_block(a, row, b) * a.Hk + hk;
+    const int ek = scale_exponent(km), ev = scale_exponent(vm);
+    if (tid == 0) {
+      a.cache.k_scale[at] = pow2(ek);
+      a.cache.v_scale[at] = pow2(ev);
+    }
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const int x = tid + TH * j, key = x / (D / 8), dim = x % (D / 8) * 8;
+      *(u32x2*)(a.cache.k8 + at * (64 * D) + (dim >> 6) * 4096 + key * 64 + (dim & 63)) = to_e4m3(kx[j], pow2(-ek));
+      if (RAW && b != last) ((u32x4*)(a.raw_k + ((int64_t)blockIdx.x * a.Hk + hk) * (64 * D)))[x] = kx[j];
+    }
+#pragma unroll
+    for (int j = 0; j < nsq; ++j) {
+      const int x = tid + TH * j, kq = x / (D / 4), dim = x % (D / 4) * 4;
+      u32x2 t[4];
+      transpose4(vx[j], t);
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const u32x2 w = to_e4m3(u32x4{t[e][0], t[e][1], t[e + 1][0], t[e + 1][1]}, pow2(-ev));
+        vt[(dim + e) * kLd + kq] = w[0];
+        vt[(dim + e + 1) * kLd + kq] = w[1];
+      }
+      if (RAW && b != last) {
+        uint16_t* rv = a.raw_v + ((int64_t)blockIdx.x * a.Hk + hk) * (64 * D);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *(u32x2*)(rv + (dim + e) * 64 + kq * 4) = t[e];
       }
     }
-    for (int x = tid; x < D * old; x += 256) vt[x / old * kLd + x % old] = tv[x / old * 64 + x % old];
     __syncthreads();
-    quantise_block<D>(
-        a.cache, (int64_t)pool_block(a, row, b) * a.Hk + hk,
-        [&](int x) {
-          const int key = x / (D / 8), dim = x % (D / 8) * 8;
-          return *(const u32x4*)(key < old ? tk + key * D + dim : nk + (from + key) * a.k_stride + dim);
-        },
-        [&](int x) { return *(const u32x4*)(vt + x / 8 * kLd + x % 8 * 8); }, red);
+    for (int x = tid; x < D * 4; x += TH) {
+      const uint32_t* w = vt + x / 4 * kLd + x % 4 * 4;
+      *(u32x4*)(a.cache.v8 + at * (64 * D) + x * 16) = u32x4{w[0], w[1], w[2], w[3]};
+    }
   }
   if (b != first) return;
-  __syncthreads();  // the old tail has been read
-  uint16_t* wk = a.cache.tail_k + ((int64_t)row * a.Hk + hk) * (64 * D);
-  uint16_t* wv = a.cache.tail_v + ((int64_t)row * a.Hk + hk) * (64 * D);
-  const int p0 = max(last * 64, ctx), n = ctx + len - p0;
-  for (int x = tid; x < n * (D / 8); x += 256) {
-    const int p = p0 + x / (D / 8), dim = x % (D / 8) * 8;
-    *(u32x4*)(wk + (p & 63) * D + dim) = *(const u32x4*)(nk + ((int64_t)c0 + p - ctx) * a.k_stride + dim);
+  // the new tail: the tokens of the last block, from registers if that is this one
+  if (last != first) {
+    const int64_t src = (int64_t)c0 + (int64_t)last * 64 - ctx;
+    const int there = ctx + len - last * 64;
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const int x = tid + TH * j, key = x / (D / 8), dim = x % (D / 8) * 8;
+      if (key < there) kx[j] = *(const u32x4*)(nk + (src + key) * a.k_stride + dim);
+    }
+#pragma unroll
+    for (int j = 0; j < nsq; ++j) {
+      const int x = tid + TH * j, vkey = x / (D / 4) * 4, vdim = x % (D / 4) * 4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (vkey + e < there) vx[j][e] = *(const u32x2*)(nv + (src + vkey + e) * a.v_stride + vdim);
+    }
   }
-  for (int x = tid; x < n * D; x += 256) {
-    const int p = p0 + x % n, dim = x / n;
-    wv[dim * 64 + (p & 63)] = nv[((int64_t)c0 + p - ctx) * a.v_stride + dim];
+  const int lo = last != first ? 0 : old, hi = last != first ? ctx + len - last * 64 : keys;  // keys to write
+#pragma unroll
+  for (int j = 0; j < n; ++j) {
+    const int x = tid + TH * j, key = x / (D / 8), dim = x % (D / 8) * 8;
+    if (key >= lo && key < hi) *(u32x4*)(tk + key * D + dim) = kx[j];
+  }
+#pragma unroll
+  for (int j = 0; j < nsq; ++j) {
+    const int x = tid + TH * j, vkey = x / (D / 4) * 4, vdim = x % (D / 4) * 4;
+    u32x2 t[4];
+    transpose4(vx[j], t);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint16_t* to = tv + (vdim + e) * 64 + vkey;
+      if (vkey >= lo && vkey + 4 <= hi) {
+        *(u32x2*)to = t[e];
+      } else {
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (vkey + y >= lo && vkey + y < hi) to[y] = (uint16_t)(t[e][y >> 1] >> (16 * (y & 1)));
+      }
+    }
   }
 }
 

@@ -44,6 +44,11 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Waits here for a load whose first use would otherwise be inside a loop: the
+// wait counts loads, so in the loop it would also wait for every load that
+// the loop itself keeps in flight.
+__device__ __forceinline__ void settle(u32x4& x) { asm volatile("" : "+v"(x)); }
+
 // key of a sub-tile's A row x
 __device__ __forceinline__ int key_of(int a, int x) { return 16 * (x >> 2) + 4 * a + (x & 3); }
 
@@ -132,6 +137,7 @@ __device__ __forceinline__ BlockRun load_run(const StepArgs& a, int row, int hk,
   const int64_t at = (int64_t)x.id * a.Hk + hk;
   x.ks = a.cache.k_scale[at];
   x.vs = a.cache.v_scale[at];
+  asm volatile("" : "+v"(x.ks), "+v"(x.vs));  // as settle()
   return x;
 }
 
@@ -287,13 +293,12 @@ __device__ __forceinline__ uint64_t stage_raw(const StepArgs& a, int i, int hk, 
       bad |= m;
     }
     if (kq < 16) {
+      u32x2 turned[4];
+      transpose4(x[n], turned);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {  // dim + e of the four keys
-        const uint32_t w0 = x[n][0][e >> 1], w1 = x[n][1][e >> 1], w2 = x[n][2][e >> 1], w3 = x[n][3][e >> 1];
-        const u32x2 t = e & 1 ? u32x2{w0 >> 16 | (w1 & 0xffff0000u), w2 >> 16 | (w3 & 0xffff0000u)}
-                              : u32x2{(w0 & 0xffffu) | w1 << 16, (w2 & 0xffffu) | w3 << 16};
         const int dd = dim + e;
-        ((u32x2*)&sm.v[v_slot(dd >> 4, (kq >> 1) & 1, (kq >> 2) * 16 + (dd & 15))])[kq & 1] = t;
+        ((u32x2*)&sm.v[v_slot(dd >> 4, (kq >> 1) & 1, (kq >> 2) * 16 + (dd & 15))])[kq & 1] = turned[e];
       }
     }
   }
@@ -323,6 +328,10 @@ __device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* s
 #pragma unroll
     for (int x = 0; x < KS; ++x) q[t][x] = *(const u32x4*)(qp + (x >> 1) * 64 + g * 16 + (x & 1) * 8);
   }
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int x = 0; x < KS; ++x) settle(q[t][x]);
   // own blocks: of the work-group's rows and of this wave's
   const int b_lo = (ctx + (int)(row0 / G)) >> 6, b_hi = (ctx + (int)(last_row / G)) >> 6;
   const bool has = w0 <= last_row;
@@ -346,23 +355,50 @@ __device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* s
   auto tile = [&](auto masked_, int buf, const int (&upto)[RT]) {
     constexpr bool MASKED = decltype(masked_)::value;
     const PrefillLds<D>& s_ = sm[buf];
-    f32x4 s[RT][4];
+    // Fragments are read from LDS a group ahead of the MFMAs that use them;
+    // the barriers keep the compiler from moving a read to its use, where
+    // its latency would show.
+    constexpr int GS = RT == 1 ? 8 : 4, NK = 4 * KS / GS, NV = 2 * DT / GS;
+    u32x4 fr[2][GS];
+    auto read_k = [&](int n) __attribute__((always_inline)) {
 #pragma unroll
-    for (int x = 0; x < KS; ++x)  // sub-tiles inside: neighbouring MFMAs do not wait for each other
-#pragma unroll
-      for (int sub = 0; sub < 4; ++sub) {
-        const u32x4 kf = s_.k[(sub * KS + x) * 64 + lane];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) s[t][sub] = mma(kf, q[t][x], x ? s[t][sub] : f32x4{0.f, 0.f, 0.f, 0.f});
+      for (int e = 0; e < GS; ++e) {
+        const int f = n * GS + e;  // sub-tiles inside: neighbouring MFMAs do not wait for each other
+        fr[n & 1][e] = s_.k[((f & 3) * KS + (f >> 2)) * 64 + lane];
       }
+    };
+    auto read_v = [&](int n) __attribute__((always_inline)) {
+#pragma unroll
+      for (int e = 0; e < GS; ++e) {
+        const int f = n * GS + e;
+        fr[n & 1][e] = s_.v[v_slot(f % DT, f / DT, lane)];
+      }
+    };
+    f32x4 s[RT][4];
+    read_k(0);
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+      if (n + 1 < NK) read_k(n + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int e = 0; e < GS; ++e) {
+        const int f = n * GS + e, sub = f & 3, x = f >> 2;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) s[t][sub] = mma(fr[n & 1][e], q[t][x], x ? s[t][sub] : f32x4{0.f, 0.f, 0.f, 0.f});
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (!(MASKED && SLOW)) read_v(0);
+    __builtin_amdgcn_sched_barrier(0);
     u32x4 p[RT][2];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       if (MASKED) {
+        const int lim = upto[t] - 16 * g;
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[t][sub][e] = 16 * g + 4 * sub + e <= upto[t] ? s[t][sub][e] : kNegInf;
+          for (int e = 0; e < 4; ++e) s[t][sub][e] = 4 * sub + e <= lim ? s[t][sub][e] : kNegInf;
       }
       const float mn = fmaxf(m[t], max_over_groups(max16(s[t])) * a.c), ref = ref_of(mn);
       const float alpha = exp2_(m[t] - ref);
@@ -375,13 +411,17 @@ __device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* s
     }
     if (!(MASKED && SLOW)) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int n = 0; n < NV; ++n) {
+        if (n + 1 < NV) read_v(n + 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int x = 0; x < DT; ++x) {
-          const u32x4 vf = s_.v[v_slot(x, h, lane)];
+        for (int e = 0; e < GS; ++e) {
+          const int f = n * GS + e;
 #pragma unroll
-          for (int t = 0; t < RT; ++t) O[t][x] = mma(vf, p[t][h], O[t][x]);
+          for (int t = 0; t < RT; ++t) O[t][f % DT] = mma(fr[n & 1][e], p[t][f / DT], O[t][f % DT]);
         }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     } else {
       // keys with a V that is not finite: one product for every number n of
       // them that a row may see, the first n as they are, the others zero; a row takes its own
@@ -565,65 +605,109 @@ __global__ __launch_bounds__(PrefillTile<D>::kThreads) void k_attn_prefill(const
 }
 
 // ---------------------------------------------------------------------------
-// decode
+// few rows per sequence: the decode step, and prefill of few new tokens
 
-// Records that join work-groups' shares of a row: per flat partition index
-// and key/value head, O [rows][D] and per row m and the four partial l.
-struct DecodeArgs {
+// Records that join work-groups' shares of a row: per partition's unit
+// and key/value head, O [rec_rows][D], and per row m and the four partial l.
+struct RowsArgs {
   StepArgs s;
   float* rec_o;
-  float* rec_ml;  // [..][rows][8]: m, l of the four lane groups
-  int32_t *base, *total;  // first flat partition of every sequence; how many there are
-  int max_parts;          // records that fit
+  float* rec_ml;  // [..][rec_rows][8]: m, -, -, -, l of the four lane groups
+  int32_t* base;  // first unit of every sequence
+  int32_t* total;  // how many units there are
+  int max_parts;  // records that fit
+  int rec_rows;   // rows of a record
+  int chunk_rows;  // rows of a chunk, 16 RT
 };
 
-__device__ __forceinline__ int parts_of(int ctx) { return ctx < 0 ? 0 : ctx / kPart + 1; }
+// A sequence's rows are cut into chunks.  A chunk's partitions reach to the
+// last row's own block.
+__device__ __forceinline__ int chunks_of(const RowsArgs& a, int len) {
+  return (int)(((uint32_t)len * (uint32_t)a.s.G + a.chunk_rows - 1) / a.chunk_rows);
+}
 
-// All partitions of the batch in a row, sequence by sequence, are dealt out
-// in equal runs to the W work-groups of a key/value head (blockIdx.x of
-// gridDim.x): a batch of any lengths is balanced to one partition.  A run
-// that begins a sequence folds its partitions as it goes; one that begins
-// inside a sequence must leave each partition by itself, because the fold goes
-// left to right.  If the batch has more partitions than there is room for
-// records (sequences that share blocks), sequences are dealt out whole.
+__device__ __forceinline__ int parts_of(const RowsArgs& a, int ctx, int len, int c) {
+  const uint32_t last = min((uint32_t)(c + 1) * a.chunk_rows, (uint32_t)len * a.s.G) - 1;
+  return ((ctx + (int)(last / (uint32_t)a.s.G)) >> 9) + 1;
+}
+
+__device__ __forceinline__ int len_of(const RowsArgs& a, int i) { return a.s.cu ? a.s.cu[i + 1] - a.s.cu[i] : 1; }
+
+// What a chunk costs, in units of a partition: its partitions, and its own
+// block, first loads and outputs, which took about as long as two (d = 128).
+constexpr int kChunkCost = 2;
+
+// units of all chunks of sequence i
+__device__ __forceinline__ int all_units_of(const RowsArgs& a, int i) {
+  const int ctx = a.s.ctx_len[i], len = len_of(a, i);
+  if (ctx < 0 || len <= 0) return 0;
+  const int n = chunks_of(a, len);
+  if ((ctx >> 9) == (ctx + len - 1) >> 9) return n * ((ctx >> 9) + 1 + kChunkCost);
+  int sum = 0;
+  for (int c = 0; c < n; ++c) sum += parts_of(a, ctx, len, c) + kChunkCost;
+  return sum;
+}
+
+// Work-group w's run of `total` things dealt to W of them: the first total % W get one more.
+__device__ __forceinline__ int run_begin(int total, int W, int w) {
+  return w * (total / W) + min(w, total % W);
+}
+__device__ __forceinline__ int run_of(int total, int W, int x) {
+  const int per = total / W, more = total % W, first = more * (per + 1);
+  return x < first ? x / (per + 1) : more + (x - first) / per;
+}
+
+// All units of the batch in a row, sequence by sequence and chunk by chunk,
+// are dealt out in equal runs to the W work-groups of a key/value head
+// (blockIdx.x of gridDim.x): a batch of any lengths is balanced to one
+// partition.  A chunk's first units are its partitions.  A run that begins a chunk folds its partitions as it goes; one
+// that begins inside a chunk must leave each partition by itself, because
+// the fold goes left to right.  If the batch has more partitions than there
+// is room for records (sequences that share blocks), sequences are dealt out whole.
 //
 // In a work-group the four waves share a partition, four tiles at a time: wave
 // w computes the scores and p of tile w; p goes through LDS and every wave
 // adds all four tiles to its own quarter of the dims.  So a partition's
-// bytes are spread over four waves' loads, and no byte is loaded twice.
-template <int D>
-__global__ __launch_bounds__(256) void k_attn_decode(const DecodeArgs da) {
-  const StepArgs& a = da.s;
-  constexpr int KS = D / 32, KP = D / 64, DT = D / 64;  // DT: dim tiles of a wave
-  __shared__ u32x4 s_p[4][2][64];
-  __shared__ float s_max[4][16], s_sum[4][64];
-  __shared__ int s_scan[4], s_at[3];
+// bytes are spread over four waves' loads, and no byte is loaded twice.  The
+// own block's scores are shared out by 16 keys.
+//
+// MULTI: any number of new tokens, which k_attn_append has put into the tail
+// (last block) or raw_k, raw_v (blocks that they filled).  Otherwise one each,
+// which this kernel appends itself.
+template <int D, int RT, bool MULTI>
+__global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(const RowsArgs ra) {
+  const StepArgs& a = ra.s;
+  constexpr int KS = D / 32, KP = D / 64, DT = D / 64, R = 16 * RT;  // DT: dim tiles of a wave
+  __shared__ u32x4 s_p[4][RT][2][64];
+  __shared__ f32x4 s_raw[4][RT][64];
+  __shared__ float s_max[4][RT][16], s_sum[4][RT][64];
+  __shared__ int s_scan[4], s_at[2];
   __shared__ uint32_t s_red[4];
   const int hk = blockIdx.y, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
-  const int W = gridDim.x, head0 = blockIdx.z * 16;  // of this key/value head's group
+  const int W = gridDim.x;
 
-  // the run [g0, g1) of flat partitions, and the sequence it begins in
+  // the run [g0, g1) of units, and the sequence it begins in
   const int per = (a.N + 255) / 256, n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
   int mine = 0;
-  for (int n = n0; n < n1; ++n) mine += parts_of(a.ctx_len[n]);
-  int upto = mine;
+  for (int n = n0; n < n1; ++n) mine += all_units_of(ra, n);
+  int upto_ = mine;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(upto, o);
-    if (lane >= o) upto += y;
+    const int y = __shfl_up(upto_, o);
+    if (lane >= o) upto_ += y;
   }
-  if (lane == 63) s_scan[wave] = upto;
+  if (lane == 63) s_scan[wave] = upto_;
   __syncthreads();
   const int total = s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
-  for (int w = 0; w < wave; ++w) upto += s_scan[w];
-  const bool whole_seqs = total > da.max_parts;
-  const int g0 = (int)((int64_t)blockIdx.x * total / W), g1 = (int)((int64_t)(blockIdx.x + 1) * total / W);
-  if (blockIdx.x == 0 && hk == 0 && blockIdx.z == 0 && tid == 0) *da.total = total;
+  for (int w = 0; w < wave; ++w) upto_ += s_scan[w];
+  const bool whole_seqs = total > ra.max_parts;
+  const int g0 = run_begin(total, W, blockIdx.x), g1 = run_begin(total, W, blockIdx.x + 1);
+  if (blockIdx.x == 0 && hk == 0 && tid == 0) *ra.total = total;
   if (g0 >= g1 && !whole_seqs) return;
-  if (g0 >= upto - mine && g0 < upto) {
-    int at = upto - mine, n = n0;
+  if (g0 >= upto_ - mine && g0 < upto_) {
+    int at = upto_ - mine, n = n0;
     for (; n < n1 - 1; ++n) {
-      const int x = parts_of(a.ctx_len[n]);
+      const int x = all_units_of(ra, n);
       if (g0 < at + x) break;
       at += x;
     }
@@ -631,254 +715,498 @@ __global__ __launch_bounds__(256) void k_attn_decode(const DecodeArgs da) {
     s_at[1] = at;
   }
   __syncthreads();
-  int i = whole_seqs ? blockIdx.x : s_at[0], base = whole_seqs ? 0 : s_at[1];
+  int i = whole_seqs ? blockIdx.x : s_at[0], base = whole_seqs ? 0 : s_at[1], c = 0;
 
   for (int f = g0; whole_seqs ? i < a.N : f < g1;) {
-    const int ctx = a.ctx_len[i], np = parts_of(ctx);
-    if (np == 0) {
-      i += whole_seqs ? W : 1;
+    const int ctx = a.ctx_len[i], len = MULTI ? len_of(ra, i) : 1;
+    const int np = ctx < 0 || len <= 0 ? 0 : parts_of(ra, ctx, len, c);
+    if (c == 0 && np > 0 && !whole_seqs && hk == 0 && tid == 0 && f == base) ra.base[i] = base;
+    if (np == 0 || (!whole_seqs && f >= base + np)) {  // nothing there, or behind it
+      if (np) base += np + kChunkCost;
+      f = max(f, base);
+      if (np && c + 1 < chunks_of(ra, len)) {
+        ++c;
+      } else {
+        c = 0;
+        i += whole_seqs ? W : 1;
+      }
       continue;
     }
-    const int own = ctx >> 6;  // the block of the new token
+    const int c0 = MULTI ? a.cu[i] : i, end = ctx + len;
+    const uint32_t rows = (uint32_t)len * (uint32_t)a.G, row0 = (uint32_t)c * R;
+    const uint32_t last_row = min(row0 + R, rows) - 1;
     const int p_lo = whole_seqs ? 0 : f - base, p_hi = whole_seqs ? np : min(np, g1 - base);
     const int cache_row = max(row_of(a.slot, i, a.cache.num_slots), 0);
-    if (p_lo == 0 && hk == 0 && blockIdx.z == 0 && tid == 0) da.base[i] = base;
-    const int head = head0 + r;
-    const bool live = head < a.G;
-    u32x4 q[KS];
-    {
-      const uint16_t* qp = a.q + (int64_t)i * a.q_stride + (int64_t)(hk * a.G + (live ? head : a.G - 1)) * D;
-#pragma unroll
-      for (int x = 0; x < KS; ++x) q[x] = *(const u32x4*)(qp + (x >> 1) * 64 + g * 16 + (x & 1) * 8);
-    }
-    f32x4 Ot[DT];
-    float mt = kNegInf, lt = 0.f;
-#pragma unroll
-    for (int x = 0; x < DT; ++x) Ot[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // own blocks of the chunk's rows (there are two at most)
+    const int b_lo = (ctx + (int)(row0 / (uint32_t)a.G)) >> 6, b_hi = (ctx + (int)(last_row / (uint32_t)a.G)) >> 6;
+    const int b_end = min(p_hi * kPartBlocks, b_hi);  // the 8-bit blocks end here
 
-    for (int p = p_lo; p < p_hi; ++p) {
-      f32x4 O[DT];
-      float m = kNegInf, l = 0.f;
+    u32x4 q[RT][KS];
+    int pos[RT];
 #pragma unroll
-      for (int x = 0; x < DT; ++x) O[x] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int b_end = min((p + 1) * kPartBlocks, own);
-#pragma unroll 1
-      for (int b0 = p * kPartBlocks; b0 < b_end; b0 += 4) {
-        const bool mytile = b0 + wave < b_end;
-        // V of all four tiles for this wave's dims; K of its own tile
-        u32x4 kb[4][KP], vb[4][DT];
-        float ks = 1.f, vs[4];
+    for (int t = 0; t < RT; ++t) {
+      const uint32_t row = min(row0 + t * 16 + r, rows - 1);
+      const int token = (int)(row / (uint32_t)a.G), head = hk * a.G + (int)(row % (uint32_t)a.G);
+      pos[t] = ctx + token;
+      const uint16_t* qp = a.q + (int64_t)(c0 + token) * a.q_stride + (int64_t)head * D;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int64_t at = (int64_t)pool_block(a, cache_row, min(b0 + t, b_end - 1)) * a.Hk + hk;
-          vs[t] = a.cache.v_scale[at];
-          const uint8_t* vp = a.cache.v8 + at * (64 * D) + (wave * DT * 16 + r) * 64 + g * 16;
+      for (int x = 0; x < KS; ++x) q[t][x] = *(const u32x4*)(qp + (x >> 1) * 64 + g * 16 + (x & 1) * 8);
+    }
+    f32x4 O[RT][DT], Ot[RT][DT];  // the partition's, the folded total
+    float m[RT], l[RT], mt[RT], lt[RT];
 #pragma unroll
-          for (int x = 0; x < DT; ++x) vb[t][x] = *(const u32x4*)(vp + x * 1024);
+    for (int t = 0; t < RT; ++t) {
+      m[t] = mt[t] = kNegInf;
+      l[t] = lt[t] = 0.f;
+#pragma unroll
+      for (int x = 0; x < DT; ++x) O[t][x] = Ot[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    auto record = [&](int p, const f32x4 (&o)[RT][DT], const float (&mr)[RT], const float (&lr)[RT]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        if (row0 + t * 16 + r > last_row) continue;
+        const int64_t rec = ((int64_t)(base + p) * a.Hk + hk) * ra.rec_rows + t * 16 + r;
+        float* to = ra.rec_o + rec * D + wave * DT * 16 + g * 4;
+#pragma unroll
+        for (int x = 0; x < DT; ++x) *(f32x4*)(to + x * 16) = o[t][x];
+        if (wave == 0) {
+          if (g == 0) ra.rec_ml[rec * 8] = mr[t];
+          ra.rec_ml[rec * 8 + 4 + g] = lr[t];
         }
-        {
-          const int64_t at = (int64_t)pool_block(a, cache_row, min(b0 + wave, b_end - 1)) * a.Hk + hk;
-          ks = a.cache.k_scale[at];
-          const uint8_t* kp_ = a.cache.k8 + at * (64 * D) + g * 16;
+      }
+    };
+    auto end_partition = [&](int p) __attribute__((always_inline)) {
+      if (p_lo > 0) record(p, O, m, l);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        if (p_lo == 0) {
+          float wa, wb;
+          fold_weights(mt[t], m[t], wa, wb);
+          lt[t] = __builtin_fmaf(l[t], wb, lt[t] * wa);
+#pragma unroll
+          for (int x = 0; x < DT; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) Ot[t][x][e] = __builtin_fmaf(O[t][x][e], wb, Ot[t][x][e] * wa);
+        }
+        m[t] = kNegInf;
+        l[t] = 0.f;
+#pragma unroll
+        for (int x = 0; x < DT; ++x) O[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+    };
+    // O += V^T p for a tile that some rows see less of (keys up to upto[t]):
+    // a key whose V is not finite must not reach them as 0 * NaN.  One
+    // product for every number n of such keys that a row may see.
+    auto masked_pv = [&](const u32x4 (&v)[DT][2], const u32x4 (&p)[RT][2], const int (&upto)[RT], uint64_t bad) __attribute__((always_inline)) {
+      int sees[RT];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) sees[t] = upto[t] < 0 ? 0 : __popcll(bad & (~0ull >> (63 - upto[t])));
+#pragma unroll
+      for (int x = 0; x < DT; ++x) {
+        f32x4 was[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) was[t] = O[t][x];
+        uint64_t drop = bad;
+#pragma unroll 1
+        for (int n = 0; n <= __popcll(bad); ++n, drop &= drop - 1) {
+          const u32x4 v0 = drop_keys(v[x][0], drop, g, 0), v1 = drop_keys(v[x][1], drop, g, 1);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            const f32x4 y_ = mma(v1, p[t][1], mma(v0, p[t][0], was[t]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) O[t][x][e] = sees[t] == n ? y_[e] : O[t][x][e];
+          }
+        }
+      }
+    };
+
+    // ---- the 8-bit blocks, four a step.  K of a step is asked for as soon as
+    // the scores of the step before have been taken from its registers, V
+    // as soon as its products have, so loads are in flight all the time.
+    BlockRun run;
+    u32x4 kb[4][KP], vb[4][DT];
+    auto fetch_ids = [&](int b) __attribute__((always_inline)) { run.id = pool_block(a, cache_row, b + lane); };
+    auto fetch_scales = [&]() __attribute__((always_inline)) {
+      const int64_t at = (int64_t)run.id * a.Hk + hk;
+      run.ks = a.cache.k_scale[at];
+      run.vs = a.cache.v_scale[at];
+    };
+    auto fetch_k = [&](int b0) __attribute__((always_inline)) {  // of this wave's own tile
+      const int bt = __builtin_amdgcn_readfirstlane(min(b0 + wave, b_end - 1) & 63);
+      const int64_t at = (int64_t)__builtin_amdgcn_readlane(run.id, bt) * a.Hk + hk;
+      const uint8_t* kp_ = a.cache.k8 + at * (64 * D) + g * 16;
+#pragma unroll
+      for (int sub = 0; sub < 4; ++sub)
+#pragma unroll
+        for (int x = 0; x < KP; ++x) kb[sub][x] = *(const u32x4*)(kp_ + x * 4096 + key_of(sub, r) * 64);
+    };
+    auto fetch_v = [&](int b0) __attribute__((always_inline)) {  // of all four, this wave's dims
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int64_t at = (int64_t)__builtin_amdgcn_readlane(run.id, min(b0 + t, b_end - 1) & 63) * a.Hk + hk;
+        const uint8_t* vp = a.cache.v8 + at * (64 * D) + (wave * DT * 16 + r) * 64 + g * 16;
+#pragma unroll
+        for (int x = 0; x < DT; ++x) vb[t][x] = *(const u32x4*)(vp + x * 1024);
+      }
+    };
+    // ---- an own block in the input type: this wave's 16 keys and its dims of V
+    u32x4 rk[KS], rv[DT][2];
+    uint32_t rn[DT];  // decode: V of the new token
+    auto fetch_raw = [&](int b) __attribute__((always_inline)) {
+      const bool in_tail = !MULTI || b == (end - 1) >> 6;
+      const int64_t at = in_tail ? ((int64_t)cache_row * a.Hk + hk) * (64 * D)
+                                 : ((int64_t)((c0 >> 6) + 2 * i + b - (ctx >> 6)) * a.Hk + hk) * (64 * D);
+      const uint16_t* tk = (in_tail ? a.cache.tail_k : a.raw_k) + at;
+      const uint16_t* tv = (in_tail ? a.cache.tail_v : a.raw_v) + at;
+      const int key = key_of(wave, r);
+      const uint16_t* kr = (!MULTI && key == (ctx & 63) ? a.k + (int64_t)i * a.k_stride + (int64_t)hk * D : tk + key * D) + g * 16;
+#pragma unroll
+      for (int x = 0; x < KS; ++x) rk[x] = *(const u32x4*)(kr + (x >> 1) * 64 + (x & 1) * 8);
+#pragma unroll
+      for (int x = 0; x < DT; ++x) {
+        const int dim = (wave * DT + x) * 16 + r;
+        rv[x][0] = *(const u32x4*)(tv + dim * 64 + g * 16);
+        rv[x][1] = *(const u32x4*)(tv + dim * 64 + g * 16 + 8);
+        if (!MULTI) rn[x] = a.v[(int64_t)i * a.v_stride + (int64_t)hk * D + dim];
+      }
+    };
+    auto do_raw = [&](int b) __attribute__((always_inline)) {
+      if (MULTI) __syncthreads();  // the scores of a raw block before have been read
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        f32x4 y_ = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < KS; ++x) y_ = mma(rk[x], q[t][x], y_);
+        s_raw[wave][t][lane] = y_;
+      }
+      __syncthreads();
+      u32x4 p[RT][2];
+      int upto[RT];
+      float alpha[RT];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        f32x4 s[4];
+        upto[t] = pos[t] >> 6 == b ? pos[t] & 63 : -1;
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub) {
+          s[sub] = s_raw[sub][t][lane];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[sub][e] = 16 * g + 4 * sub + e <= upto[t] ? s[sub][e] : kNegInf;
+        }
+        const float mn = fmaxf(m[t], max_over_groups(max16(s)) * a.c), ref = ref_of(mn);
+        alpha[t] = exp2_(m[t] - ref);
+        m[t] = mn;
+        l[t] = __builtin_fmaf(l[t], alpha[t], probabilities(s, a.c, ref, p[t]));
+      }
+      // V: keys past the sequence's end are not there yet (whatever the tail
+      // holds); decode's new one comes from the call
+      const int at = end - 1 - b * 64;
+      uint32_t nan16 = 0;
+#pragma unroll
+      for (int x = 0; x < DT; ++x) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int key = 16 * g + 2 * j;
+          uint32_t w = rv[x][j >> 2][j & 3];
+          w = key > at ? 0u : key + 1 > at ? w & 0xffffu : w;
+          if (!MULTI) w = key == at ? rn[x] : key + 1 == at ? (w & 0xffffu) | rn[x] << 16 : w;
+          if (MULTI) {
+            nan16 |= (w & 0x7f80u) == 0x7f80u ? 1u << (2 * j) : 0u;
+            nan16 |= (w & 0x7f800000u) == 0x7f800000u ? 2u << (2 * j) : 0u;
+          }
+          rv[x][j >> 2][j & 3] = w;
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) O[t][x] *= alpha[t];
+      }
+      const uint64_t bad = MULTI ? bad_keys(nan16) : 0;
+      if (bad) {
+        masked_pv(rv, p, upto, bad);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int x = 0; x < DT; ++x)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) O[t][x] = mma(rv[x][h], p[t][h], O[t][x]);
+      }
+    };
+
+    auto step = [&](int b0, auto more_) __attribute__((always_inline)) {
+      constexpr bool more = decltype(more_)::value;
+      f32x4 s[RT][4];
+      const float ks = lane_of(run.ks, __builtin_amdgcn_readfirstlane(min(b0 + wave, b_end - 1) & 63));
+      float vs[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) vs[t] = lane_of(run.vs, min(b0 + t, b_end - 1) & 63);
+#pragma unroll
+      for (int sub = 0; sub < 4; ++sub) {
+#pragma unroll
+        for (int x = 0; x < KP; ++x) {
+          u32x4 k0, k1;
+          from_e4m3(kb[sub][x], ks, k0, k1);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            s[t][sub] = mma(k0, q[t][2 * x], x ? s[t][sub] : f32x4{0.f, 0.f, 0.f, 0.f});
+            s[t][sub] = mma(k1, q[t][2 * x + 1], s[t][sub]);
+          }
+        }
+      }
+      if (more) {
+        if (((b0 + 4) & 63) == 0) {
+          fetch_ids(b0 + 4);
+          fetch_scales();
+          asm volatile("" : "+v"(run.ks), "+v"(run.vs));
+        }
+        fetch_k(b0 + 4);
+      } else if (!MULTI) {
+        fetch_raw(b_hi);
+      }
+      const bool mytile = more || b0 + wave < b_end;
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        if (MULTI && b0 + wave >= b_lo) {  // only rows whose own block comes later see it
+          const bool sees = b0 + wave < pos[t] >> 6;
 #pragma unroll
           for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
-            for (int x = 0; x < KP; ++x) kb[sub][x] = *(const u32x4*)(kp_ + x * 4096 + key_of(sub, r) * 64);
+            for (int e = 0; e < 4; ++e) s[t][sub][e] = sees ? s[t][sub][e] : kNegInf;
         }
-        f32x4 s[4];
+        const float smax = max_over_groups(max16(s[t]));
+        if (g == 0) s_max[wave][t][r] = smax;
+      }
+      __syncthreads();
+      float mm[RT][5];  // the running max before and after every tile
 #pragma unroll
-        for (int sub = 0; sub < 4; ++sub) {
-          s[sub] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < RT; ++t) {
+        mm[t][0] = m[t];
 #pragma unroll
-          for (int x = 0; x < KP; ++x) {
-            u32x4 k0, k1;
-            from_e4m3(kb[sub][x], ks, k0, k1);
-            s[sub] = mma(k0, q[2 * x], s[sub]);
-            s[sub] = mma(k1, q[2 * x + 1], s[sub]);
-          }
-        }
-        const float smax = max_over_groups(max16(s));
-        if (g == 0) s_max[wave][r] = smax;
-        __syncthreads();
-        float mm[5];  // the running max before and after every tile
-        mm[0] = m;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) mm[t + 1] = b0 + t < b_end ? fmaxf(mm[t], s_max[t][r] * a.c) : mm[t];
+        for (int n = 0; n < 4; ++n) mm[t][n + 1] = more || b0 + n < b_end ? fmaxf(mm[t][n], s_max[n][t][r] * a.c) : mm[t][n];
         if (mytile) {
           u32x4 pf[2];
-          const float mine_ = wave == 0 ? mm[1] : wave == 1 ? mm[2] : wave == 2 ? mm[3] : mm[4];
-          s_sum[wave][lane] = probabilities(s, a.c, ref_of(mine_), pf);
-          s_p[wave][0][lane] = pf[0];
-          s_p[wave][1][lane] = pf[1];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          if (b0 + t >= b_end) break;
-          const float alpha = exp2_(mm[t] - ref_of(mm[t + 1]));
-          l = __builtin_fmaf(l, alpha, s_sum[t][lane]);
-          const u32x4 p0 = s_p[t][0][lane], p1 = s_p[t][1][lane];
-#pragma unroll
-          for (int x = 0; x < DT; ++x) {
-            u32x4 v0, v1;
-            from_e4m3(vb[t][x], vs[t], v0, v1);
-            O[x] *= alpha;
-            O[x] = mma(v0, p0, O[x]);
-            O[x] = mma(v1, p1, O[x]);
-          }
-        }
-        m = mm[4];
-      }
-      if (p == np - 1) {
-        // the own block, in the input type: the tail, and the new token in
-        // its place; every wave computes all of its scores
-        const int at = ctx & 63;
-        const uint16_t* tk = a.cache.tail_k + ((int64_t)cache_row * a.Hk + hk) * (64 * D);
-        const uint16_t* tv = a.cache.tail_v + ((int64_t)cache_row * a.Hk + hk) * (64 * D);
-        const uint16_t* nk = a.k + (int64_t)i * a.k_stride + (int64_t)hk * D;
-        const uint16_t* nv = a.v + (int64_t)i * a.v_stride + (int64_t)hk * D;
-        u32x4 vb[DT][2];
-        uint32_t nvx[DT];
-#pragma unroll
-        for (int x = 0; x < DT; ++x) {
-          const int dim = (wave * DT + x) * 16 + r;
-          vb[x][0] = *(const u32x4*)(tv + dim * 64 + g * 16);
-          vb[x][1] = *(const u32x4*)(tv + dim * 64 + g * 16 + 8);
-          nvx[x] = nv[dim];
-        }
-        f32x4 s[4];
-#pragma unroll
-        for (int sub = 0; sub < 4; ++sub) {
-          const int key = key_of(sub, r);
-          const uint16_t* kr = (key == at ? nk : tk + key * D) + g * 16;
-          s[sub] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int x = 0; x < KS; ++x) s[sub] = mma(*(const u32x4*)(kr + (x >> 1) * 64 + (x & 1) * 8), q[x], s[sub]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[sub][e] = 16 * g + 4 * sub + e <= at ? s[sub][e] : kNegInf;
-        }
-        const float mn = fmaxf(m, max_over_groups(max16(s)) * a.c), ref = ref_of(mn);
-        const float alpha = exp2_(m - ref);
-        m = mn;
-        u32x4 pf[2];
-        l = __builtin_fmaf(l, alpha, probabilities(s, a.c, ref, pf));
-        // V: keys past the new one are not there yet (whatever the tail
-        // holds), the new one comes from the call
-#pragma unroll
-        for (int x = 0; x < DT; ++x) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int key = 16 * g + 2 * j;
-            uint32_t w = vb[x][j >> 2][j & 3];
-            w = key > at ? 0u : key + 1 > at ? w & 0xffffu : w;
-            w = key == at ? nvx[x] : key + 1 == at ? (w & 0xffffu) | nvx[x] << 16 : w;
-            vb[x][j >> 2][j & 3] = w;
-          }
-          O[x] *= alpha;
-          O[x] = mma(vb[x][0], pf[0], O[x]);
-          O[x] = mma(vb[x][1], pf[1], O[x]);
-        }
-        if (blockIdx.z == 0) {
-          // append: the tail's row and column; a full block is quantised
-          __syncthreads();  // every wave has read the tail
-          uint16_t* wk = (uint16_t*)tk;
-          uint16_t* wv = (uint16_t*)tv;
-          if (tid < D / 8) *(u32x4*)(wk + at * D + tid * 8) = *(const u32x4*)(nk + tid * 8);
-          for (int x = tid; x < D; x += 256) wv[x * 64 + at] = nv[x];
-          if (at == 63) {
-            __threadfence_block();
-            __syncthreads();
-            quantise_block<D>(
-                a.cache, (int64_t)pool_block(a, cache_row, own) * a.Hk + hk,
-                [&](int x) { return ((const u32x4*)wk)[x]; }, [&](int x) { return ((const u32x4*)wv)[x]; }, s_red);
-          }
+          const float mine_ = wave == 0 ? mm[t][1] : wave == 1 ? mm[t][2] : wave == 2 ? mm[t][3] : mm[t][4];
+          s_sum[wave][t][lane] = probabilities(s[t], a.c, ref_of(mine_), pf);
+          s_p[wave][t][0][lane] = pf[0];
+          s_p[wave][t][1][lane] = pf[1];
         }
       }
-      if (p_lo == 0) {
-        float wa, wb;
-        fold_weights(mt, m, wa, wb);
-        lt = __builtin_fmaf(l, wb, lt * wa);
+      __syncthreads();
 #pragma unroll
-        for (int x = 0; x < DT; ++x)
+      for (int n = 0; n < 4; ++n) {
+        if (!more && b0 + n >= b_end) break;
+        u32x4 p[RT][2], v[DT][2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) Ot[x][e] = __builtin_fmaf(O[x][e], wb, Ot[x][e] * wa);
-      }
-      const bool whole = p_lo == 0 && p == np - 1;
-      if (whole) {
-        const float inv = 1.f / sum_over_groups(lt);
-        if (live) {
-          uint16_t* o = a.o + ((int64_t)i * a.H + hk * a.G + head) * D + wave * DT * 16 + g * 4;
+        for (int t = 0; t < RT; ++t) {
+          const float alpha = exp2_(mm[t][n] - ref_of(mm[t][n + 1]));
+          l[t] = __builtin_fmaf(l[t], alpha, s_sum[n][t][lane]);
+          p[t][0] = s_p[n][t][0][lane];
+          p[t][1] = s_p[n][t][1][lane];
+#pragma unroll
+          for (int x = 0; x < DT; ++x) O[t][x] *= alpha;
+        }
+        uint64_t bad = 0;
+        if (MULTI && b0 + n >= b_lo) {
+          uint32_t nan16 = 0;
 #pragma unroll
           for (int x = 0; x < DT; ++x)
-            *(u32x2*)(o + x * 16) = u32x2{pack2(Ot[x][0] * inv, Ot[x][1] * inv), pack2(Ot[x][2] * inv, Ot[x][3] * inv)};
-        }
-      } else if (p_lo > 0 || p == p_hi - 1) {
-        const int64_t rec = ((int64_t)(base + (p_lo > 0 ? p : 0)) * a.Hk + hk) * a.G + head;
-        if (live) {
-          float* o = da.rec_o + rec * D + wave * DT * 16 + g * 4;
 #pragma unroll
-          for (int x = 0; x < DT; ++x) *(f32x4*)(o + x * 16) = p_lo > 0 ? O[x] : Ot[x];
-          if (wave == 0) {
-            if (g == 0) da.rec_ml[rec * 8] = p_lo > 0 ? m : mt;
-            da.rec_ml[rec * 8 + 4 + g] = p_lo > 0 ? l : lt;
-          }
+            for (int e = 0; e < 16; ++e) nan16 |= ((vb[n][x][e >> 2] >> (8 * (e & 3))) & 0x7f) == 0x7f ? 1u << e : 0u;
+          bad = bad_keys(nan16);
+        }
+#pragma unroll
+        for (int x = 0; x < DT; ++x) from_e4m3(vb[n][x], vs[n], v[x][0], v[x][1]);
+        if (MULTI && bad) {
+          int upto[RT];
+#pragma unroll
+          for (int t = 0; t < RT; ++t) upto[t] = b0 + n < pos[t] >> 6 ? 63 : -1;
+          masked_pv(v, p, upto, bad);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int x = 0; x < DT; ++x)
+#pragma unroll
+              for (int t = 0; t < RT; ++t) O[t][x] = mma(v[x][h], p[t][h], O[t][x]);
         }
       }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) m[t] = mm[t][4];
+      if (more) fetch_v(b0 + 4);
+      if (((b0 + 4) & (kPartBlocks - 1)) == 0 && b0 + 4 <= b_hi) {
+        const int p = b0 / kPartBlocks;
+        if (MULTI && b_lo / kPartBlocks == p) {  // the partition's last block is a row's own
+          fetch_raw(b_lo);
+          do_raw(b_lo);
+        }
+        end_partition(p);
+      }
+    };
+    if (p_lo * kPartBlocks < b_end) {
+      int b0 = p_lo * kPartBlocks;
+      fetch_ids(b0 & ~63);
+      fetch_scales();
+      fetch_k(b0);
+      fetch_v(b0);
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int x = 0; x < KS; ++x) settle(q[t][x]);
+      asm volatile("" : "+v"(run.ks), "+v"(run.vs));
+#pragma unroll 1
+      for (; b0 + 4 < b_end; b0 += 4) step(b0, std::true_type{});
+      // by itself, so that in the loop every load is followed by the others
+      // (if it might not be, a wait for K would be one for V as well)
+      step(b0, std::false_type{});
+    } else if (!MULTI) {
+      fetch_raw(b_hi);
     }
-    if (whole_seqs) {
-      i += W;
-    } else {
-      f = base + p_hi;
-      base += np;
-      ++i;
+    if (p_hi == np) {
+      if (MULTI) {
+        if (b_lo < b_hi && b_lo / kPartBlocks == np - 1) {
+          fetch_raw(b_lo);
+          do_raw(b_lo);
+        }
+        fetch_raw(b_hi);
+      }
+      do_raw(b_hi);
+      if (!MULTI && c == 0) {
+        // append: the tail's row and column; a full block is quantised
+        const int at = ctx & 63;
+        uint16_t* wk = a.cache.tail_k + ((int64_t)cache_row * a.Hk + hk) * (64 * D);
+        uint16_t* wv = a.cache.tail_v + ((int64_t)cache_row * a.Hk + hk) * (64 * D);
+        const uint16_t* nk = a.k + (int64_t)i * a.k_stride + (int64_t)hk * D;
+        const uint16_t* nv = a.v + (int64_t)i * a.v_stride + (int64_t)hk * D;
+        if (tid < D / 8) *(u32x4*)(wk + at * D + tid * 8) = *(const u32x4*)(nk + tid * 8);
+        for (int x = tid; x < D; x += 256) wv[x * 64 + at] = nv[x];
+        if (at == 63) {
+          __threadfence_block();
+          __syncthreads();
+          quantise_block<D>(
+              a.cache, (int64_t)pool_block(a, cache_row, b_hi) * a.Hk + hk,
+              [&](int x) { return ((const u32x4*)wk)[x]; }, [&](int x) { return ((const u32x4*)wv)[x]; }, s_red);
+        }
+      }
+      end_partition(np - 1);
+    }
+    if (p_lo == 0 && p_hi < np) record(0, Ot, mt, lt);
+    if (p_lo == 0 && p_hi == np) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const float inv = 1.f / sum_over_groups(lt[t]);
+        const uint32_t row = row0 + t * 16 + r;
+        if (row > last_row) continue;
+        uint16_t* o = a.o + ((int64_t)(c0 + (int)(row / (uint32_t)a.G)) * a.H + hk * a.G + (int)(row % (uint32_t)a.G)) * D +
+                      wave * DT * 16 + g * 4;
+#pragma unroll
+        for (int x = 0; x < DT; ++x)
+          *(u32x2*)(o + x * 16) = u32x2{pack2(Ot[t][x][0] * inv, Ot[t][x][1] * inv), pack2(Ot[t][x][2] * inv, Ot[t][x][3] * inv)};
+      }
+    }
+    __syncthreads();  // LDS is used again by the next chunk
+    f = whole_seqs ? 0 : base + p_hi;
+    if (whole_seqs || p_hi == np) {
+      base += np + kChunkCost;
+      f = max(f, base);
+      if (c + 1 < chunks_of(ra, len)) {
+        ++c;
+      } else {
+        c = 0;
+        i += whole_seqs ? W : 1;
+      }
     }
   }
 }
 
-// Joins what several work-groups did of a sequence, left to right; sequences
-// that one work-group did alone are finished, refused ones get o = 0.
+// Joins what several work-groups did of a chunk, left to right; chunks that
+// one work-group did alone are finished, refused requests' rows get o = 0.
+// A wave takes a row, a lane D / 64 of its dims.  The fold is a chain over the
+// records, but what it needs of each is not: the weights of 64 folds come
+// from prefix maxima (exact in any order), a lane each, and many records are
+// asked for before the first is used, so the chain is two operations a record.
 template <int D>
-__global__ __launch_bounds__(256) void k_attn_join(const DecodeArgs da, int W) {
-  const StepArgs& a = da.s;
-  const int i = blockIdx.x, hk = blockIdx.y;
-  const int np = parts_of(a.ctx_len[i]);
-  uint16_t* o = a.o + ((int64_t)i * a.H + hk * a.G) * D;
-  if (np == 0) {
-    for (int x = threadIdx.x; x < a.G * D / 4; x += 256) *(u32x2*)(o + x * 4) = u32x2{0, 0};
+__global__ __launch_bounds__(256) void k_attn_join(const RowsArgs ra, int W) {
+  constexpr int V = D / 64;
+  typedef float fv __attribute__((ext_vector_type(V)));
+  const StepArgs& a = ra.s;
+  const int i = blockIdx.x, hk = blockIdx.y, lane = threadIdx.x & 63;
+  const int ctx = a.ctx_len[i], len = len_of(ra, i);
+  const int x_ = __builtin_amdgcn_readfirstlane(blockIdx.z * 4 + (threadIdx.x >> 6));
+  const int c = x_ / ra.rec_rows, rr = x_ % ra.rec_rows;
+  const uint32_t row = (uint32_t)c * ra.chunk_rows + rr, G = (uint32_t)a.G;
+  if (len <= 0 || row >= (uint32_t)len * G) return;
+  uint16_t* o = a.o + ((int64_t)((a.cu ? a.cu[i] : i) + (int)(row / G)) * a.H + hk * a.G + (int)(row % G)) * D + lane * V;
+  if (ctx < 0) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0;
     return;
   }
-  const int base = da.base[i], total = *da.total;
-  if (total > da.max_parts) return;
-  // the work-group of the sequence's first partition, and where its run ends
-  const int w = (int)((((int64_t)base + 1) * W - 1) / total);
-  const int cut = (int)((int64_t)(w + 1) * total / W);
-  if (cut >= base + np) return;
-  const int n = base + np - cut;  // records after the first
-  for (int x = blockIdx.z * 256 + threadIdx.x; x < a.G * D / 4; x += 256 * gridDim.z) {
-    const int head = x / (D / 4), dim = x % (D / 4) * 4;
-    const int64_t row = (int64_t)hk * a.G + head, step = (int64_t)a.Hk * a.G;
-    const float* ml = da.rec_ml + ((int64_t)base * step + row) * 8;
-    f32x4 O = *(const f32x4*)(da.rec_o + ((int64_t)base * step + row) * D + dim);
-    float m = ml[0];
-    f32x4 l = *(const f32x4*)(ml + 4);
-    const float* po = da.rec_o + ((int64_t)cut * step + row) * D + dim;
-    const float* pm = da.rec_ml + ((int64_t)cut * step + row) * 8;
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) {
-      const f32x4 Op = *(const f32x4*)(po + (int64_t)j * step * D);
-      const float mp = pm[(int64_t)j * step * 8];
-      const f32x4 lp = *(const f32x4*)(pm + (int64_t)j * step * 8 + 4);
-      float wa, wb;
-      fold_weights(m, mp, wa, wb);
+  const int total = *ra.total;
+  if (total > ra.max_parts) return;
+  int base = ra.base[i];
+  for (int x = 0; x < c; ++x) base += parts_of(ra, ctx, len, x) + kChunkCost;
+  // where the run of the work-group with the chunk's first partition ends
+  const int cut = run_begin(total, W, run_of(total, W, base) + 1);
+  const int n = base + parts_of(ra, ctx, len, c) - cut + 1;  // records
+  if (n <= 1) return;
+  const int64_t step = (int64_t)a.Hk * ra.rec_rows, at = (int64_t)hk * ra.rec_rows + rr;
+  const int64_t rec0 = base * step + at;
+  fv O = *(const fv*)(ra.rec_o + rec0 * D + lane * V);
+  float m = ra.rec_ml[rec0 * 8], l = ra.rec_ml[rec0 * 8 + 4 + (lane & 3)];  // lanes 0 .. 3: the four partial sums
+  // the others follow each other
+  const int k = n - 1;
+  const float* po = ra.rec_o + (cut * step + at) * D;
+  const float* pm = ra.rec_ml + (cut * step + at) * 8;
+  const int64_t so = step * D, sm = step * 8;
+  auto batch = [&](auto size_, int j0, int u0, float mp, float& wa, float& wb) __attribute__((always_inline)) {
+    constexpr int S = decltype(size_)::value;  // records asked for at once
+    fv Op[S];
+    float lp[S];
+    const float *to = po + (j0 + u0) * so, *tm = pm + (j0 + u0) * sm;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        l[e] = __builtin_fmaf(lp[e], wb, l[e] * wa);
-        O[e] = __builtin_fmaf(Op[e], wb, O[e] * wa);
+    for (int u = 0; u < S; ++u) {
+      Op[u] = *(const fv*)(to + lane * V);
+      lp[u] = tm[4 + (lane & 3)];
+      if (j0 + u0 + u + 1 < k) {  // past the last: the last again
+        to += so;
+        tm += sm;
       }
     }
-    const float inv = 1.f / ((l[0] + l[1]) + (l[2] + l[3]));
-    *(u32x2*)(o + head * D + dim) = u32x2{pack2(O[0] * inv, O[1] * inv), pack2(O[2] * inv, O[3] * inv)};
+    __builtin_amdgcn_sched_barrier(0);  // or the loads are moved to where they are used
+    if (u0 == 0) {  // weights of the next 64 folds
+      float up = mp;
+#pragma unroll
+      for (int y = 1; y < 64; y <<= 1) {
+        const float z = __shfl_up(up, y);
+        if (lane >= y) up = fmaxf(up, z);
+      }
+      const float prev = __shfl_up(up, 1);
+      float before = lane ? fmaxf(m, prev) : m;
+      fold_weights(before, mp, wa, wb);
+      m = fmaxf(m, __shfl(up, 63));
+    }
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+      const bool there = j0 + u0 + u < k;
+      const float ya = lane_of(wa, u0 + u), yb = lane_of(wb, u0 + u);
+      l = there ? __builtin_fmaf(lp[u], yb, l * ya) : l;
+#pragma unroll
+      for (int e = 0; e < V; ++e) O[e] = there ? __builtin_fmaf(Op[u][e], yb, O[e] * ya) : O[e];
+    }
+  };
+  for (int j0 = 0; j0 < k; j0 += 64) {
+    const float mp = j0 + lane < k ? pm[(j0 + lane) * sm] : kNegInf;
+    float wa = 0.f, wb = 0.f;
+    if (k - j0 > 16) {
+      constexpr int S = V == 4 ? 32 : 64;
+#pragma unroll 1
+      for (int u0 = 0; u0 < 64 && j0 + u0 < k; u0 += S) batch(std::integral_constant<int, S>{}, j0, u0, mp, wa, wb);
+    } else {
+      batch(std::integral_constant<int, 16>{}, j0, 0, mp, wa, wb);
+    }
   }
+  const float inv = 1.f / ((lane_of(l, 0) + lane_of(l, 1)) + (lane_of(l, 2) + lane_of(l, 3)));
+#pragma unroll
+  for (int e = 0; e < V; ++e) o[e] = (uint16_t)pack2(O[e] * inv, 0.f);
 }
 
 }  // namespace attn

@@ -339,36 +339,75 @@ extern "C" gdn_status gdn_attn_qk_norm_rope_bwd(const gdn_attn_shape* shape, con
 
 namespace {
 
-struct PrefillLayout {
-  size_t old_k, old_v, bad, total;
-};
-
 // work items of the append: room for every block that the tokens can touch
 int64_t touched_blocks(int32_t N, int64_t T) { return T / kBlock + 2 * (int64_t)N; }
 
-PrefillLayout prefill_layout(const gdn_attn_shape& s, int32_t N, int64_t T) {
-  const size_t tail = align_up((size_t)N * kv_heads(s) * kBlock * s.head_dim * sizeof(uint16_t));
-  const size_t bad = align_up((size_t)touched_blocks(N, T) * kv_heads(s) * sizeof(int32_t));
-  return {0, tail, 2 * tail, 2 * tail + bad};
-}
-
-struct DecodeLayout {
-  size_t base, total_word, rec_ml, rec_o, total;
-  int64_t max_parts;
+// Records of k_attn_rows: `rec_bytes` of them behind `off`.
+struct RowsLayout {
+  size_t base, total_word, rec, rec_bytes, total;
 };
 
-DecodeLayout decode_layout(const gdn_attn_shape& s, int32_t N, int32_t num_blocks) {
-  DecodeLayout L;
-  L.max_parts = (int64_t)num_blocks / kPartBlocks + N;
-  size_t off = 0;
+RowsLayout rows_layout(size_t off, int32_t N, size_t rec_bytes) {
+  RowsLayout L;
   L.base = off;
   off = align_up(off + sizeof(int32_t) * (size_t)N);
   L.total_word = off;
   off = align_up(off + sizeof(int32_t));
-  L.rec_ml = off;
-  off = align_up(off + (size_t)L.max_parts * s.num_heads * 8 * sizeof(float));
-  L.rec_o = off;
-  off = align_up(off + (size_t)L.max_parts * s.num_heads * s.head_dim * sizeof(float));
+  L.rec = off;
+  L.rec_bytes = align_up(rec_bytes);
+  L.total = off + L.rec_bytes;
+  return L;
+}
+
+// bytes of one partition's records: `rows` rows of each key/value head
+size_t record_bytes(const gdn_attn_shape& s, int rows) {
+  return (size_t)kv_heads(s) * rows * (s.head_dim + 8) * sizeof(float);
+}
+
+// A pool of num_blocks has num_blocks / 8 partitions, and one more per
+// sequence, unless sequences share blocks.
+int64_t pool_parts(int32_t N, int32_t num_blocks) { return (int64_t)num_blocks / kPartBlocks + (1 + kChunkCost) * (int64_t)N; }
+
+// Decode: a chunk is up to 16 of a key/value head's query heads.
+int decode_rows(const gdn_attn_shape& s) { return std::min(16, s.num_heads / kv_heads(s)); }
+
+RowsLayout decode_layout(const gdn_attn_shape& s, int32_t N, int32_t num_blocks) {
+  const int chunks = (s.num_heads / kv_heads(s) + 15) / 16;
+  return rows_layout(0, N, (size_t)pool_parts(N, num_blocks) * chunks * record_bytes(s, decode_rows(s)));
+}
+
+// Prefill takes k_attn_rows if no sequence has more rows than this.
+constexpr int kMaxFewRows = 256;
+// Its records, as far as this bound (beyond, sequences go to work-groups whole).
+constexpr size_t kFewRecordBytes = size_t(512) << 20;
+
+// rows of a chunk there; d = 256 has registers for one 16-row tile only
+int chunk_rows(const gdn_attn_shape& s, int64_t rows) { return s.head_dim == 256 || rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+struct PrefillLayout {
+  size_t old_k, old_v, bad, raw_k, raw_v;
+  RowsLayout rows;
+  size_t total;
+};
+
+PrefillLayout prefill_layout(const gdn_attn_shape& s, int32_t N, int64_t T, int32_t num_blocks) {
+  const size_t block = (size_t)kv_heads(s) * kBlock * s.head_dim * sizeof(uint16_t);
+  PrefillLayout L{};
+  size_t off = 0;
+  L.old_k = off;
+  off = align_up(off + N * block);
+  L.old_v = off;
+  off = align_up(off + N * block);
+  L.bad = off;
+  off = align_up(off + (size_t)touched_blocks(N, T) * kv_heads(s) * sizeof(int32_t));
+  if (T * (s.num_heads / kv_heads(s)) <= (int64_t)N * kMaxFewRows) {  // it may take k_attn_rows
+    L.raw_k = off;
+    off = align_up(off + (size_t)touched_blocks(N, T) * block);
+    L.raw_v = off;
+    off = align_up(off + (size_t)touched_blocks(N, T) * block);
+    L.rows = rows_layout(off, N, std::min(kFewRecordBytes, (size_t)pool_parts(N, num_blocks) * record_bytes(s, kMaxFewRows + 64)));
+    off = L.rows.total;
+  }
   L.total = off;
   return L;
 }
@@ -450,29 +489,43 @@ gdn_status check_workspace(const char* fn, const void* workspace, size_t bytes, 
   return GDN_OK;
 }
 
-template <int D>
-void run_append(const StepArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL(k_attn_append<D>, dim3((unsigned)touched_blocks(a.N, a.T), a.Hk), dim3(256), 0, st, a);
+void place_records(RowsArgs& a, const RowsLayout& L, char* ws, const gdn_attn_shape& s, int chunk, int rows) {
+  a.base = (int32_t*)(ws + L.base);
+  a.total = (int32_t*)(ws + L.total_word);
+  a.chunk_rows = chunk;
+  a.rec_rows = rows;
+  a.max_parts = (int)std::min<size_t>(L.rec_bytes / record_bytes(s, rows), INT32_MAX / 2);
+  a.rec_ml = (float*)(ws + L.rec);
+  a.rec_o = a.rec_ml + (size_t)a.max_parts * a.s.Hk * rows * 8;
+}
+
+// Work-groups: two on each of 256 CUs, over the key/value heads.
+template <int D, int RT, bool MULTI>
+gdn_status run_rows(const RowsArgs& a, int chunks, hipStream_t st, const char* fn) {
+  const int W = std::max(1, std::min(512 / a.s.Hk, a.max_parts));
+  hipLaunchKernelGGL((k_attn_rows<D, RT, MULTI>), dim3(W, a.s.Hk), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_attn_join<D>, dim3(a.s.N, a.s.Hk, (chunks * a.rec_rows + 3) / 4), dim3(256), 0, st, a, W);
+  return launch_status(fn);
 }
 
 template <int D>
 gdn_status run_prefill(const StepArgs& a, hipStream_t st, const char* fn) {
   typedef PrefillTile<D> P;
-  run_append<D>(a, st);
+  hipLaunchKernelGGL((k_attn_append<D, false>), dim3((unsigned)touched_blocks(a.N, a.T), a.Hk), dim3(kAppendThreads<D>), 0, st, a);
   const int64_t tiles = (int64_t)a.T * a.G / P::kRows + a.N;
   hipLaunchKernelGGL(k_attn_prefill<D>, dim3((unsigned)(tiles * a.Hk)), dim3(P::kThreads), 0, st, a);
   return launch_status(fn);
 }
 
 template <int D>
-gdn_status run_decode(const DecodeArgs& a, hipStream_t st, const char* fn) {
-  // two work-groups on each of 256 CUs, over the key/value heads and groups of 16 query heads
-  const int z = (a.s.G + 15) / 16;
-  const int W = std::max(1, std::min(512 / std::max(1, a.s.Hk * z), a.max_parts));
-  hipLaunchKernelGGL(k_attn_decode<D>, dim3(W, a.s.Hk, z), dim3(256), 0, st, a);
-  const int jz = (a.s.G * (D / 4) + 255) / 256;
-  hipLaunchKernelGGL(k_attn_join<D>, dim3(a.s.N, a.s.Hk, jz), dim3(256), 0, st, a, W);
-  return launch_status(fn);
+gdn_status run_few(const RowsArgs& a, int chunks, hipStream_t st, const char* fn) {
+  hipLaunchKernelGGL((k_attn_append<D, true>), dim3((unsigned)touched_blocks(a.s.N, a.s.T), a.s.Hk), dim3(kAppendThreads<D>), 0, st, a.s);
+  if (a.chunk_rows == 16) return run_rows<D, 1, true>(a, chunks, st, fn);
+  if constexpr (D < 256) {
+    if (a.chunk_rows == 32) return run_rows<D, 2, true>(a, chunks, st, fn);
+    return run_rows<D, 4, true>(a, chunks, st, fn);
+  }
+  return fail(GDN_ERR_UNSUPPORTED, "%s: rows", fn);
 }
 
 }  // namespace
@@ -488,12 +541,27 @@ extern "C" gdn_status gdn_attn_prefill(const gdn_attn_shape* shape, int32_t num_
   if (max_new < 0) return fail(GDN_ERR_INVALID_ARG, "%s: max_new is negative", fn);
   CHECK_PTR(cu_seqlens, "cu_seqlens");
   if (total_tokens == 0) return done();
-  const PrefillLayout L = prefill_layout(*shape, num_seqs, total_tokens);
+  const PrefillLayout L = prefill_layout(*shape, num_seqs, total_tokens, cache->num_blocks);
   CHECK(check_workspace(fn, workspace, workspace_bytes, L.total));
+  char* ws = (char*)workspace;
   a.cu = cu_seqlens;
-  a.old_k = (uint16_t*)((char*)workspace + L.old_k);
-  a.old_v = (uint16_t*)((char*)workspace + L.old_v);
-  a.bad = (int32_t*)((char*)workspace + L.bad);
+  a.old_k = (uint16_t*)(ws + L.old_k);
+  a.old_v = (uint16_t*)(ws + L.old_v);
+  a.bad = (int32_t*)(ws + L.bad);
+  const int64_t most = (int64_t)(max_new > 0 ? std::min<int64_t>(max_new, total_tokens) : total_tokens) * a.G;
+  if (most <= kMaxFewRows && L.rows.rec_bytes > 0) {
+    RowsArgs ra{};
+    a.raw_k = (uint16_t*)(ws + L.raw_k);
+    a.raw_v = (uint16_t*)(ws + L.raw_v);
+    ra.s = a;
+    const int chunk = chunk_rows(*shape, most), chunks = (int)((most + chunk - 1) / chunk);
+    place_records(ra, L.rows, ws, *shape, chunk, chunk);
+    switch (shape->head_dim) {
+      case 64: return run_few<64>(ra, chunks, (hipStream_t)stream, fn);
+      case 128: return run_few<128>(ra, chunks, (hipStream_t)stream, fn);
+      default: return run_few<256>(ra, chunks, (hipStream_t)stream, fn);
+    }
+  }
   switch (shape->head_dim) {
     case 64: return run_prefill<64>(a, (hipStream_t)stream, fn);
     case 128: return run_prefill<128>(a, (hipStream_t)stream, fn);
@@ -506,20 +574,17 @@ extern "C" gdn_status gdn_attn_decode_step(const gdn_attn_shape* shape, int32_t 
                                            const gdn_attn_step* step, const gdn_attn_cache* cache, float scale,
                                            void* o, void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "gdn_attn_decode_step";
-  DecodeArgs a{};
+  RowsArgs a{};
   CHECK(check_attention(fn, shape, num_seqs, num_seqs, q, k, v, q_stride, k_stride, v_stride, step, cache, scale, o, &a.s));
   if (num_seqs == 0) return done();
-  const DecodeLayout L = decode_layout(*shape, num_seqs, cache->num_blocks);
+  const RowsLayout L = decode_layout(*shape, num_seqs, cache->num_blocks);
   CHECK(check_workspace(fn, workspace, workspace_bytes, L.total));
-  a.base = (int32_t*)((char*)workspace + L.base);
-  a.total = (int32_t*)((char*)workspace + L.total_word);
-  a.rec_ml = (float*)((char*)workspace + L.rec_ml);
-  a.rec_o = (float*)((char*)workspace + L.rec_o);
-  a.max_parts = (int)std::min<int64_t>(L.max_parts, INT32_MAX);
+  place_records(a, L, (char*)workspace, *shape, 16, decode_rows(*shape));
+  const int chunks = (a.s.G + 15) / 16;
   switch (shape->head_dim) {
-    case 64: return run_decode<64>(a, (hipStream_t)stream, fn);
-    case 128: return run_decode<128>(a, (hipStream_t)stream, fn);
-    default: return run_decode<256>(a, (hipStream_t)stream, fn);
+    case 64: return run_rows<64, 1, false>(a, chunks, (hipStream_t)stream, fn);
+    case 128: return run_rows<128, 1, false>(a, chunks, (hipStream_t)stream, fn);
+    default: return run_rows<256, 1, false>(a, chunks, (hipStream_t)stream, fn);
   }
 }
 
@@ -560,7 +625,7 @@ extern "C" size_t gdn_attn_workspace_size(const gdn_attn_shape* shape, int32_t o
                   check_sizes("gdn_attn_workspace_size", num_seqs, total_tokens) == GDN_OK && num_blocks >= 0;
   gdn_last_error_text() = before;  // a size query is no call
   if (!ok) return 0;
-  if (op == GDN_ATTN_OP_PREFILL) return prefill_layout(*shape, num_seqs, total_tokens).total;
+  if (op == GDN_ATTN_OP_PREFILL) return prefill_layout(*shape, num_seqs, total_tokens, num_blocks).total;
   if (op == GDN_ATTN_OP_DECODE) return decode_layout(*shape, num_seqs, num_blocks).total;
   if (op == GDN_ATTN_OP_NORM_ROPE_BWD)
     return align_up((size_t)norm_bwd_groups(*shape, total_tokens) * 2 * shape->head_dim * sizeof(float));

@@ -9,11 +9,11 @@
 //            16 g + 8 h .. + 7 in slot group g of step 2 kp + h)
 //     m'   = max(m, c max(s)), c = scale * log2(e)
 //     p    = exp2(fma(s, c, -m')), alpha = exp2(m - m')
-//     l    = fma(l, alpha, sum p)   four partial sums per row, by lane group
 //     O    = alpha O + V^T p, p in bf16, two MFMA k steps
+//     l    = the same with V = 1, so numerator and denominator have the same p
 //   partitions: (m, l, O) = fold of the total and the partition, left to
 //   right: O = fma(Op, exp2(mp - m'), O exp2(m - m')).
-//   o = O (1 / l), l's partial sums added as (0 + 1) + (2 + 3).
+//   o = O (1 / l).
 // A masked tile leaves a row's state as it is (alpha = 1, p = 0), so which
 // tiles a kernel walks through for a row beyond its own does not matter,
 // and neither does which work-group does which partition.
@@ -52,27 +52,43 @@ __device__ __forceinline__ void settle(u32x4& x) { asm volatile("" : "+v"(x)); }
 // key of a sub-tile's A row x
 __device__ __forceinline__ int key_of(int a, int x) { return 16 * (x >> 2) + 4 * a + (x & 3); }
 
-// max of a lane's 16 scores
+// For inline assembly that reads MFMA results: the hardware does not wait for
+// them, the compiler puts the wait states (11 at most for these shapes) before
+// its own instructions only.  Nothing is moved over the barriers.
+__device__ __forceinline__ void mfma_done() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\ns_nop 3");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// max of a lane's 16 scores, after mfma_done().  v_max3_f32 by name: of fmaxf
+// the compiler makes one more instruction per score, to quiet NaNs that
+// v_max3_f32 passes over by itself.
 __device__ __forceinline__ float max16(const f32x4 (&s)[4]) {
-  float m = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
+  float m = fmaxf(s[3][2], s[3][3]);
 #pragma unroll
-  for (int a = 1; a < 4; ++a) m = fmaxf(m, fmaxf(fmaxf(s[a][0], s[a][1]), fmaxf(s[a][2], s[a][3])));
+  for (int i = 0; i < 14; i += 2)
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(m), "v"(s[i >> 2][i & 3]), "v"(s[(i + 1) >> 2][(i + 1) & 3]));
   return m;
 }
 
-// scores -> p: their bf16 B fragments for the two PV steps, and their sum
-__device__ __forceinline__ float probabilities(const f32x4 (&s)[4], float c, float m, u32x4 (&p)[2]) {
-  float sum[4];
+// scores -> p: their bf16 B fragments for the two PV steps
+__device__ __forceinline__ void probabilities(const f32x4 (&s)[4], float c, float m, u32x4 (&p)[2]) {
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
     float e[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) e[i] = exp2_(__builtin_fmaf(s[a][i], c, -m));
-    sum[a] = (e[0] + e[1]) + (e[2] + e[3]);
     p[a >> 1][2 * (a & 1)] = pack2(e[0], e[1]);
     p[a >> 1][2 * (a & 1) + 1] = pack2(e[2], e[3]);
   }
-  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+// l += sum p, as one more dim whose V is 1: every lane of a row gets the sum
+// over all 64 keys (in element 0; the others are not kept up).
+__device__ __forceinline__ void add_sum(const u32x4 (&p)[2], f32x4& l) {
+  const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+  l = mma(ones, p[1], mma(ones, p[0], l));
 }
 
 // the running max as a reference for exp2 (a row that has seen nothing: 0)
@@ -91,34 +107,46 @@ __device__ __forceinline__ void fold_weights(float& m, float mp, float& a, float
 
 // Rows of a (sequence, key/value head): row r is token r / G, query head
 // hk G + r % G.  A work-group takes kRows of them, a wave 16 kRT, and all of it
-// walks the keys together: a tile is converted to bf16 once per work-group
-// into LDS, in the order the MFMA operands are read (conflict-free, 16
-// bytes per lane), while the bytes of the next one are in flight from memory.
+// walks the keys together through tiles in LDS, in the order the MFMA operands
+// are read (conflict-free, 16 bytes per lane), while the bytes of the next one
+// are in flight from memory.  What bounds it is the issue of instructions: two
+// waves on a SIMD, which the accumulators' registers allow, issue one in about
+// 5 cycles.  So a tile is converted to bf16 once per work-group, before it is
+// written to LDS, at d = 64 and 128 (5 x 2,048 at d = 128: 184 us; with 8-bit tiles,
+// which every wave converts as it reads, 199).  At d = 256 the 8-bit tiles leave LDS
+// for more of the folded total, which otherwise goes to scratch memory in
+// the loop (1 x 10,240: 1,240 us; bf16 tiles 1,690).
 //
 // The 8-bit blocks come first, all in one loop (those from the work-group's
-// first own block on are masked per row), then the rows' own blocks, kRaw of
-// them staged at once, so that every wave does its own without waiting for
-// the others'.
+// first own block on are masked per row), then the rows' own blocks.
 template <int D>
 struct PrefillTile {
-  static constexpr int kRT = D == 256 ? 1 : 2;   // 16-row tiles of a wave
+  static constexpr int kRT = D == 256 ? 1 : 2;   // 16-row tiles of a wave: as the accumulators' registers allow
   static constexpr int kWaves = 8;
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int kRows = 16 * kRT * kWaves;
-  static constexpr int kFrags = 4 * (D / 32);    // 1 KiB each, K; as many for V
   static constexpr int kUnits = 4 * (D / 64);    // 1 KiB loads of an 8-bit block, K; as many for V
   static constexpr bool kSplit = kUnits < kWaves;  // d = 64: half of the waves load K, half V
   static constexpr int kPer = kSplit ? 1 : kUnits / kWaves;  // units of a wave, K and V each
-  static constexpr int kRaw = D == 64 ? 4 : 2;  // LDS buffers
+  static constexpr bool kLds8 = D == 256;          // tiles in LDS: 8 bits, or bf16
   // dim tiles of the folded total that are kept in LDS (each thread its own), for want of registers
-  static constexpr int kOtLds = D == 128 ? 4 : 0;
+  static constexpr int kOtLds = D == 64 ? 0 : D == 128 ? 5 : 8;
 };
 
 template <int D>
 struct PrefillLds {
-  u32x4 k[PrefillTile<D>::kFrags * 64];
-  u32x4 v[PrefillTile<D>::kFrags * 64];
+  static constexpr int kPart = PrefillTile<D>::kUnits * (PrefillTile<D>::kLds8 ? 1 : 2) * 64;
+  u32x4 x[2 * kPart];  // K and V of a tile in 1 KiB units or bf16 fragments
+  __device__ u32x4* k() { return x; }
+  __device__ u32x4* v() { return x + kPart; }
 };
+
+// Of the two tiles' LDS, where V of an own block lies (bf16): slots of them fit.
+template <int D>
+constexpr int kRawSlots = PrefillTile<D>::kLds8 ? 2 : 4;
+
+template <int D>
+__device__ __forceinline__ u32x4* raw_slot(PrefillLds<D>* sm, int n) { return (u32x4*)sm + n * (D / 16 * 2 * 64); }
 
 // Where V's fragment (dt, h) keeps a lane's 16 bytes: rows change places by dt in
 // groups of four, so that writing four keys of neighbouring dims (own blocks) spreads over the banks.
@@ -148,25 +176,31 @@ __device__ __forceinline__ float lane_of(float x, int lane) {
 template <int D>
 struct Bytes {  // a wave's share of an 8-bit block in flight
   u32x4 k[PrefillTile<D>::kPer], v[PrefillTile<D>::kPer];
-  float ks, vs;
 };
 
 template <int D>
-__device__ __forceinline__ void load_block(const StepArgs& a, const BlockRun& run, int hk, int b, Bytes<D>& y, int wave,
-                                           int lane) {
+__device__ __forceinline__ void load_k8(const StepArgs& a, const BlockRun& run, int hk, int b, Bytes<D>& y, int wave, int lane) {
   typedef PrefillTile<D> P;
+  if (P::kSplit && wave >= P::kUnits) return;
   const int r = lane & 15, g = lane >> 4;
   const int64_t at = (int64_t)__builtin_amdgcn_readlane(run.id, b & 63) * a.Hk + hk;
-  y.ks = lane_of(run.ks, b & 63);
-  y.vs = lane_of(run.vs, b & 63);
 #pragma unroll
   for (int n = 0; n < P::kPer; ++n) {
     const int unit = (wave + P::kWaves * n) % P::kUnits;
-    const int sub = unit & 3, kp = unit >> 2;
-    if (!P::kSplit || wave < P::kUnits)
-      y.k[n] = *(const u32x4*)(a.cache.k8 + at * (64 * D) + kp * 4096 + key_of(sub, r) * 64 + g * 16);
-    if (!P::kSplit || wave >= P::kUnits)
-      y.v[n] = *(const u32x4*)(a.cache.v8 + at * (64 * D) + (unit * 16 + r) * 64 + g * 16);
+    y.k[n] = *(const u32x4*)(a.cache.k8 + at * (64 * D) + (unit >> 2) * 4096 + key_of(unit & 3, r) * 64 + g * 16);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void load_v8(const StepArgs& a, const BlockRun& run, int hk, int b, Bytes<D>& y, int wave, int lane) {
+  typedef PrefillTile<D> P;
+  if (P::kSplit && wave < P::kUnits) return;
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t at = (int64_t)__builtin_amdgcn_readlane(run.id, b & 63) * a.Hk + hk;
+#pragma unroll
+  for (int n = 0; n < P::kPer; ++n) {
+    const int unit = (wave + P::kWaves * n) % P::kUnits;
+    y.v[n] = *(const u32x4*)(a.cache.v8 + at * (64 * D) + (unit * 16 + r) * 64 + g * 16);
   }
 }
 
@@ -192,22 +226,37 @@ __device__ __forceinline__ u32x4 drop_keys(u32x4 v, uint64_t drop, int g, int h)
 }
 
 template <int D>
-__device__ __forceinline__ void store_block(const Bytes<D>& y, PrefillLds<D>& sm, int wave, int lane) {
+__device__ __forceinline__ void put_k8(const Bytes<D>& y, float scale, PrefillLds<D>& sm, int wave, int lane) {
   typedef PrefillTile<D> P;
+  if (P::kSplit && wave >= P::kUnits) return;
+#pragma unroll
+  for (int n = 0; n < P::kPer; ++n) {
+    const int unit = (wave + P::kWaves * n) % P::kUnits, sub = unit & 3, kp = unit >> 2;
+    if constexpr (P::kLds8) {
+      sm.k()[unit * 64 + lane] = y.k[n];
+    } else {
+      u32x4 lo, hi;
+      from_e4m3(y.k[n], scale, lo, hi);
+      sm.k()[(sub * (D / 32) + 2 * kp) * 64 + lane] = lo;
+      sm.k()[(sub * (D / 32) + 2 * kp + 1) * 64 + lane] = hi;
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void put_v8(const Bytes<D>& y, float scale, PrefillLds<D>& sm, int wave, int lane) {
+  typedef PrefillTile<D> P;
+  if (P::kSplit && wave < P::kUnits) return;
 #pragma unroll
   for (int n = 0; n < P::kPer; ++n) {
     const int unit = (wave + P::kWaves * n) % P::kUnits;
-    const int sub = unit & 3, kp = unit >> 2;
-    u32x4 lo, hi;
-    if (!P::kSplit || wave < P::kUnits) {
-      from_e4m3(y.k[n], y.ks, lo, hi);
-      sm.k[(sub * (D / 32) + 2 * kp) * 64 + lane] = lo;
-      sm.k[(sub * (D / 32) + 2 * kp + 1) * 64 + lane] = hi;
-    }
-    if (!P::kSplit || wave >= P::kUnits) {
-      from_e4m3(y.v[n], y.vs, lo, hi);
-      sm.v[v_slot(unit, 0, lane)] = lo;
-      sm.v[v_slot(unit, 1, lane)] = hi;
+    if constexpr (P::kLds8) {
+      sm.v()[unit * 64 + lane] = y.v[n];
+    } else {
+      u32x4 lo, hi;
+      from_e4m3(y.v[n], scale, lo, hi);
+      sm.v()[v_slot(unit, 0, lane)] = lo;
+      sm.v()[v_slot(unit, 1, lane)] = hi;
     }
   }
 }
@@ -226,90 +275,76 @@ __device__ __forceinline__ uint64_t bad_in_block(const Bytes<D>& y, int wave) {
   return bad_keys(nan16);
 }
 
-// A block in the input type: the call's tokens, and the tail as it was for
-// the ones before.  Past the sequence's end: zeros.  K goes as it is; of V a
-// thread takes four keys of four dims and writes them turned.  Returns the
-// wave's keys with a V that is not finite.
-template <int D>
-__device__ __forceinline__ uint64_t stage_raw(const StepArgs& a, int i, int hk, int ctx, int end, int c0, int b,
-                                              PrefillLds<D>& sm, int wave, int lane) {
+// V of the own blocks b and b + 1, in the input type, into slots n and n + 1:
+// the call's tokens, and the tail as it was for the ones before.  From token
+// `end` on: zeros.  A thread takes four keys of four dims and writes them turned.
+// s_bad gets the wave's keys with a V that is not finite.
+template <int D, bool SLOW>
+__device__ __forceinline__ void stage_raw(const StepArgs& a, int i, int hk, int ctx, int end, int c0, int b, PrefillLds<D>* sm,
+                                          int n, uint64_t (*s_bad)[PrefillTile<D>::kWaves], int wave, int lane) {
   typedef PrefillTile<D> P;
-  constexpr int NK = (P::kUnits + P::kWaves - 1) / P::kWaves, NV = (64 / 4) * (D / 4) / P::kThreads;
-  const int r = lane & 15, g = lane >> 4;
+  constexpr int NV = (16 * (D / 4) + P::kThreads - 1) / P::kThreads;
   const int64_t tail = ((int64_t)i * a.Hk + hk) * (64 * D);
   const int64_t from = (int64_t)c0 - ctx;
-  u32x4 lo[NK], hi[NK];
-  u32x2 x[NV < 1 ? 1 : NV][4];
-  constexpr int NVR = NV < 1 ? 1 : NV;
+  u32x2 x[2][NV][4];
 #pragma unroll
-  for (int n = 0; n < NK; ++n) {
-    const int unit = wave + P::kWaves * n, sub = unit & 3, kp = unit >> 2, key = key_of(sub, r), p = b * 64 + key;
-    lo[n] = hi[n] = u32x4{0, 0, 0, 0};
-    if (unit < P::kUnits && p < end) {
-      const uint16_t* src = (p >= ctx ? a.k + (from + p) * a.k_stride + (int64_t)hk * D : a.old_k + tail + key * D) + kp * 64 + g * 16;
-      lo[n] = *(const u32x4*)src;
-      hi[n] = *(const u32x4*)(src + 8);
-    }
-  }
-  uint64_t bad = 0;
+  for (int z = 0; z < 2; ++z)
 #pragma unroll
-  for (int n = 0; n < NVR; ++n) {
-    const int it = wave * 64 + lane + P::kThreads * n, kq = it / (D / 4), dim = it % (D / 4) * 4;
+    for (int m = 0; m < NV; ++m) {
+      const int it = wave * 64 + lane + P::kThreads * m, kq = it / (D / 4), dim = it % (D / 4) * 4;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int key = 4 * kq + j, p = b * 64 + key;
-      x[n][j] = u32x2{0, 0};
-      if (kq < 16 && p < end) {
-        if (p >= ctx) {
-          x[n][j] = *(const u32x2*)(a.v + (from + p) * a.v_stride + (int64_t)hk * D + dim);
-        } else {
-          const uint16_t* tv = a.old_v + tail + dim * 64 + key;
-          x[n][j] = u32x2{tv[0] | (uint32_t)tv[64] << 16, tv[128] | (uint32_t)tv[192] << 16};
+      for (int j = 0; j < 4; ++j) {
+        const int key = 4 * kq + j, p = (b + z) * 64 + key;
+        x[z][m][j] = u32x2{0, 0};
+        if (kq < 16 && p < end) {
+          if (p >= ctx) {
+            x[z][m][j] = *(const u32x2*)(a.v + (from + p) * a.v_stride + (int64_t)hk * D + dim);
+          } else {
+            const uint16_t* tv = a.old_v + tail + dim * 64 + key;
+            x[z][m][j] = u32x2{tv[0] | (uint32_t)tv[64] << 16, tv[128] | (uint32_t)tv[192] << 16};
+          }
         }
       }
     }
-  }
 #pragma unroll
-  for (int n = 0; n < NK; ++n) {
-    const int unit = wave + P::kWaves * n, sub = unit & 3, kp = unit >> 2;
-    if (unit < P::kUnits) {
-      sm.k[(sub * (D / 32) + 2 * kp) * 64 + lane] = lo[n];
-      sm.k[(sub * (D / 32) + 2 * kp + 1) * 64 + lane] = hi[n];
-    }
-  }
+  for (int z = 0; z < 2; ++z) {
+    uint64_t bad = 0;
 #pragma unroll
-  for (int n = 0; n < NVR; ++n) {
-    const int it = wave * 64 + lane + P::kThreads * n, kq = it / (D / 4), dim = it % (D / 4) * 4;
-    uint32_t nan4 = 0;
+    for (int m = 0; m < NV; ++m) {
+      const int it = wave * 64 + lane + P::kThreads * m, kq = it / (D / 4), dim = it % (D / 4) * 4;
+      if (SLOW) {
+        uint32_t nan4 = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w0 = x[n][j][0] & 0x7f807f80u, w1 = x[n][j][1] & 0x7f807f80u;
-      if ((w0 & 0xffffu) == 0x7f80u || w0 >> 16 == 0x7f80u || (w1 & 0xffffu) == 0x7f80u || w1 >> 16 == 0x7f80u) nan4 |= 1u << j;
-    }
-    if (__any(nan4 != 0)) {
-      uint64_t m = kq < 16 ? (uint64_t)nan4 << (4 * kq) : 0;
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w0 = x[z][m][j][0] & 0x7f807f80u, w1 = x[z][m][j][1] & 0x7f807f80u;
+          if ((w0 & 0xffffu) == 0x7f80u || w0 >> 16 == 0x7f80u || (w1 & 0xffffu) == 0x7f80u || w1 >> 16 == 0x7f80u) nan4 |= 1u << j;
+        }
+        if (__any(nan4 != 0)) {
+          uint64_t w = kq < 16 ? (uint64_t)nan4 << (4 * kq) : 0;
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) m |= (uint64_t)__shfl_xor((long long)m, o);
-      bad |= m;
-    }
-    if (kq < 16) {
-      u32x2 turned[4];
-      transpose4(x[n], turned);
+          for (int o = 1; o < 64; o <<= 1) w |= (uint64_t)__shfl_xor((long long)w, o);
+          bad |= w;
+        }
+      }
+      if (kq < 16) {
+        u32x2 turned[4];
+        transpose4(x[z][m], turned);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {  // dim + e of the four keys
-        const int dd = dim + e;
-        ((u32x2*)&sm.v[v_slot(dd >> 4, (kq >> 1) & 1, (kq >> 2) * 16 + (dd & 15))])[kq & 1] = turned[e];
+        for (int e = 0; e < 4; ++e) {  // dim + e of the four keys
+          const int dd = dim + e;
+          ((u32x2*)&raw_slot<D>(sm, n + z)[v_slot(dd >> 4, (kq >> 1) & 1, (kq >> 2) * 16 + (dd & 15))])[kq & 1] = turned[e];
+        }
       }
     }
+    if (SLOW && lane == 0) s_bad[n + z][wave] = bad;
   }
-  return bad;
 }
 
 // A work-group's rows [row0, row0 + kRows) of sequence i.  SLOW: a block that is
 // masked for some of them holds a V that is not finite.
 template <int D, bool SLOW>
 __device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* sm, f32x4 (*s_ot)[PrefillTile<D>::kThreads],
-                                             uint64_t (*s_bad)[PrefillTile<D>::kWaves],
+                                             uint64_t (*s_bad)[PrefillTile<D>::kWaves], float (*s_scale)[2],
                                              int hk, int i, int cache_row, uint32_t row0, uint32_t rows, int c0, int ctx,
                                              int end) {
   typedef PrefillTile<D> P;
@@ -317,6 +352,22 @@ __device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* s
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const uint32_t G = (uint32_t)a.G, last_row = min(row0 + P::kRows, rows) - 1;
   const uint32_t w0 = row0 + wave * RT * 16;
+  // own blocks: of the work-group's rows
+  const int b_lo = (ctx + (int)(row0 / G)) >> 6, b_hi = (ctx + (int)(last_row / G)) >> 6;
+
+  Bytes<D> y;
+  float ks = 1.f, vs = 1.f;
+  BlockRun run;
+  const int n_tiles = b_hi;
+  auto fetch = [&](int t) __attribute__((always_inline)) {
+    if ((t & 63) == 0) run = load_run(a, cache_row, hk, t, lane);
+    load_k8<D>(a, run, hk, t, y, wave, lane);
+    load_v8<D>(a, run, hk, t, y, wave, lane);
+    ks = lane_of(run.ks, t & 63);
+    vs = lane_of(run.vs, t & 63);
+  };
+  if (n_tiles > 0) fetch(0);
+
   u32x4 q[RT][KS];
   int pos[RT];
 #pragma unroll
@@ -332,68 +383,96 @@ __device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* s
   for (int t = 0; t < RT; ++t)
 #pragma unroll
     for (int x = 0; x < KS; ++x) settle(q[t][x]);
-  // own blocks: of the work-group's rows and of this wave's
-  const int b_lo = (ctx + (int)(row0 / G)) >> 6, b_hi = (ctx + (int)(last_row / G)) >> 6;
+  // own blocks of this wave's rows
   const bool has = w0 <= last_row;
   const int w_lo = (ctx + (int)(min(w0, last_row) / G)) >> 6;
   const int w_hi = (ctx + (int)(min(w0 + RT * 16 - 1, last_row) / G)) >> 6;
 
   constexpr int OL = P::kOtLds, OR = DT - OL;
-  f32x4 O[RT][DT], Ot[RT][OR];
-  float m[RT], l[RT], mt[RT], lt[RT];
+  f32x4 O[RT][DT], Ot[RT][OR], l[RT];
+  float m[RT], mt[RT], lt[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     m[t] = mt[t] = kNegInf;
-    l[t] = lt[t] = 0.f;
+    lt[t] = 0.f;
+    l[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int x = 0; x < DT; ++x) O[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int x = 0; x < DT; ++x) (x < OR ? Ot[t][x < OR ? x : 0] : s_ot[t * OL + x - OR][threadIdx.x]) = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // one tile from LDS; MASKED: rows see keys up to upto[t] of it
-  auto tile = [&](auto masked_, int buf, const int (&upto)[RT]) {
-    constexpr bool MASKED = decltype(masked_)::value;
-    const PrefillLds<D>& s_ = sm[buf];
-    // Fragments are read from LDS a group ahead of the MFMAs that use them;
-    // the barriers keep the compiler from moving a read to its use, where
-    // its latency would show.
-    constexpr int GS = RT == 1 ? 8 : 4, NK = 4 * KS / GS, NV = 2 * DT / GS;
-    u32x4 fr[2][GS];
-    auto read_k = [&](int n) __attribute__((always_inline)) {
+  // The three parts of a tile.  LDS is read a group ahead of the MFMAs that
+  // use it; the barriers keep the compiler from moving a read to its use,
+  // where its latency would show.
+  constexpr int PF = P::kLds8 ? 2 : 1;             // fragments of 16 bytes in LDS
+  constexpr int GS = (RT == 1 ? 8 : 4) / PF;       // 16-byte reads of a group
+  f32x4 s[RT][4];
+  u32x4 p[RT][2];
+  int upto[RT];  // the last key of the tile that a row sees
+  auto scores = [&](int buf) __attribute__((always_inline)) {
+    constexpr int NG = 4 * KS / PF / GS;
+    const u32x4* s_ = sm[buf].k();
+    const float ks = P::kLds8 ? s_scale[buf][0] : 1.f;
+    u32x4 u[2][GS];
+    auto read = [&](int n) __attribute__((always_inline)) {
 #pragma unroll
       for (int e = 0; e < GS; ++e) {
         const int f = n * GS + e;  // sub-tiles inside: neighbouring MFMAs do not wait for each other
-        fr[n & 1][e] = s_.k[((f & 3) * KS + (f >> 2)) * 64 + lane];
+        u[n & 1][e] = s_[(P::kLds8 ? f : (f & 3) * KS + (f >> 2)) * 64 + lane];
       }
     };
-    auto read_v = [&](int n) __attribute__((always_inline)) {
+    read(0);
 #pragma unroll
-      for (int e = 0; e < GS; ++e) {
-        const int f = n * GS + e;
-        fr[n & 1][e] = s_.v[v_slot(f % DT, f / DT, lane)];
-      }
-    };
-    f32x4 s[RT][4];
-    read_k(0);
-#pragma unroll
-    for (int n = 0; n < NK; ++n) {
-      if (n + 1 < NK) read_k(n + 1);
+    for (int n = 0; n < NG; ++n) {
+      if (n + 1 < NG) read(n + 1);
       __builtin_amdgcn_sched_barrier(0);
+      u32x4 k[GS][PF];
 #pragma unroll
       for (int e = 0; e < GS; ++e) {
-        const int f = n * GS + e, sub = f & 3, x = f >> 2;
-#pragma unroll
-        for (int t = 0; t < RT; ++t) s[t][sub] = mma(fr[n & 1][e], q[t][x], x ? s[t][sub] : f32x4{0.f, 0.f, 0.f, 0.f});
+        if constexpr (P::kLds8)
+          from_e4m3(u[n & 1][e], ks, k[e][0], k[e][1]);
+        else
+          k[e][0] = u[n & 1][e];
       }
+#pragma unroll
+      for (int h = 0; h < PF; ++h)
+#pragma unroll
+        for (int e = 0; e < GS; ++e) {
+          const int sub = (n * GS + e) & 3, x = (n * GS + e) / 4 * PF + h;
+#pragma unroll
+          for (int t = 0; t < RT; ++t) s[t][sub] = mma(k[e][h], q[t][x], x ? s[t][sub] : f32x4{0.f, 0.f, 0.f, 0.f});
+        }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (!(MASKED && SLOW)) read_v(0);
-    __builtin_amdgcn_sched_barrier(0);
-    u32x4 p[RT][2];
+  };
+  // scores of own block b: K from memory, as it is, a sub-tile ahead
+  auto raw_scores = [&](int b) __attribute__((always_inline)) {
+    u32x4 k[2][KS];
+    auto load = [&](int sub) __attribute__((always_inline)) {
+      const int key = key_of(sub, r), pk = b * 64 + key;
+      const uint16_t* src = (pk >= ctx ? a.k + ((int64_t)c0 - ctx + min(pk, end - 1)) * a.k_stride + (int64_t)hk * D
+                                       : a.old_k + ((int64_t)i * a.Hk + hk) * (64 * D) + key * D) + g * 16;
+#pragma unroll
+      for (int x = 0; x < KS; ++x) k[sub & 1][x] = *(const u32x4*)(src + (x >> 1) * 64 + (x & 1) * 8);
+    };
+    load(0);
+#pragma unroll
+    for (int sub = 0; sub < 4; ++sub) {
+      if (sub < 3) load(sub + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int x = 0; x < KS; ++x)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) s[t][sub] = mma(k[sub & 1][x], q[t][x], x ? s[t][sub] : f32x4{0.f, 0.f, 0.f, 0.f});
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto softmax = [&](bool masked) __attribute__((always_inline)) {
+    mfma_done();
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      if (MASKED) {
+      if (masked) {
         const int lim = upto[t] - 16 * g;
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub)
@@ -403,53 +482,111 @@ __device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* s
       const float mn = fmaxf(m[t], max_over_groups(max16(s[t])) * a.c), ref = ref_of(mn);
       const float alpha = exp2_(m[t] - ref);
       m[t] = mn;
-      l[t] = __builtin_fmaf(l[t], alpha, probabilities(s[t], a.c, ref, p[t]));
+      probabilities(s[t], a.c, ref, p[t]);
       if (__any(alpha != 1.f)) {
+        l[t][0] *= alpha;
 #pragma unroll
         for (int x = 0; x < DT; ++x) O[t][x] *= alpha;
       }
     }
-    if (!(MASKED && SLOW)) {
+  };
+  // O += V^T p of a tile with keys whose V is not finite (s_bad): one product
+  // for every number n of them that a row may see, the first n as they
+  // are, the others zero; a row takes its own
+  auto slow_products = [&](int buf, auto&& fragments) __attribute__((always_inline)) {
+    uint64_t bad = 0;
 #pragma unroll
-      for (int n = 0; n < NV; ++n) {
-        if (n + 1 < NV) read_v(n + 1);
-        __builtin_amdgcn_sched_barrier(0);
+    for (int w = 0; w < P::kWaves; ++w) bad |= s_bad[buf][w];
+    int sees[RT];
 #pragma unroll
-        for (int e = 0; e < GS; ++e) {
-          const int f = n * GS + e;
+    for (int t = 0; t < RT; ++t) sees[t] = upto[t] < 0 ? 0 : __popcll(bad & (~0ull >> (63 - upto[t])));
 #pragma unroll
-          for (int t = 0; t < RT; ++t) O[t][f % DT] = mma(fr[n & 1][e], p[t][f / DT], O[t][f % DT]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    } else {
-      // keys with a V that is not finite: one product for every number n of
-      // them that a row may see, the first n as they are, the others zero; a row takes its own
-      uint64_t bad = 0;
+    for (int x = 0; x < DT; ++x) {
+      f32x4 base[RT];
 #pragma unroll
-      for (int w = 0; w < P::kWaves; ++w) bad |= s_bad[buf][w];
-      int sees[RT];
-#pragma unroll
-      for (int t = 0; t < RT; ++t) sees[t] = upto[t] < 0 ? 0 : __popcll(bad & (~0ull >> (63 - upto[t])));
-#pragma unroll
-      for (int x = 0; x < DT; ++x) {
-        f32x4 base[RT];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) base[t] = O[t][x];
-        uint64_t drop = bad;
+      for (int t = 0; t < RT; ++t) base[t] = O[t][x];
+      u32x4 f0, f1;
+      fragments(x, f0, f1);
+      uint64_t drop = bad;
 #pragma unroll 1
-        for (int n = 0; n <= __popcll(bad); ++n, drop &= drop - 1) {
-          const u32x4 v0 = drop_keys(s_.v[v_slot(x, 0, lane)], drop, g, 0);
-          const u32x4 v1 = drop_keys(s_.v[v_slot(x, 1, lane)], drop, g, 1);
+      for (int n = 0; n <= __popcll(bad); ++n, drop &= drop - 1) {
+        const u32x4 v0 = drop_keys(f0, drop, g, 0), v1 = drop_keys(f1, drop, g, 1);
 #pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            const f32x4 y_ = mma(v1, p[t][1], mma(v0, p[t][0], base[t]));
+        for (int t = 0; t < RT; ++t) {
+          const f32x4 y_ = mma(v1, p[t][1], mma(v0, p[t][0], base[t]));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) O[t][x][e] = sees[t] == n ? y_[e] : O[t][x][e];
-          }
+          for (int e = 0; e < 4; ++e) O[t][x][e] = sees[t] == n ? y_[e] : O[t][x][e];
         }
       }
     }
+  };
+  auto products = [&](int buf, bool masked) __attribute__((always_inline)) {
+    constexpr int NG = 2 * DT / PF / GS;
+    const u32x4* s_ = sm[buf].v();
+    const float vs = P::kLds8 ? s_scale[buf][1] : 1.f;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) add_sum(p[t], l[t]);
+    if (SLOW && masked) {
+      slow_products(buf, [&](int x, u32x4& f0, u32x4& f1) {
+        if constexpr (P::kLds8) {
+          from_e4m3(s_[x * 64 + lane], vs, f0, f1);
+        } else {
+          f0 = s_[v_slot(x, 0, lane)];
+          f1 = s_[v_slot(x, 1, lane)];
+        }
+      });
+      return;
+    }
+    u32x4 u[2][GS];
+    auto read = [&](int n) __attribute__((always_inline)) {
+#pragma unroll
+      for (int e = 0; e < GS; ++e) {
+        const int f = n * GS + e;
+        u[n & 1][e] = s_[P::kLds8 ? f * 64 + lane : v_slot(f % DT, f / DT, lane)];
+      }
+    };
+    read(0);
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      if (n + 1 < NG) read(n + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      u32x4 v[GS][PF];
+#pragma unroll
+      for (int e = 0; e < GS; ++e) {
+        if constexpr (P::kLds8)
+          from_e4m3(u[n & 1][e], vs, v[e][0], v[e][1]);
+        else
+          v[e][0] = u[n & 1][e];
+      }
+#pragma unroll
+      for (int h = 0; h < PF; ++h)
+#pragma unroll
+        for (int e = 0; e < GS; ++e) {
+          const int f = n * GS + e, x = f % DT, step = P::kLds8 ? h : f / DT;
+#pragma unroll
+          for (int t = 0; t < RT; ++t) O[t][x] = mma(v[e][h], p[t][step], O[t][x]);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto raw_products = [&](u32x4* s_, int slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) add_sum(p[t], l[t]);
+    if (SLOW) {
+      slow_products(slot, [&](int x, u32x4& f0, u32x4& f1) {
+        f0 = s_[v_slot(x, 0, lane)];
+        f1 = s_[v_slot(x, 1, lane)];
+      });
+      return;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int x = 0; x < DT; ++x) {
+        const u32x4 vf = s_[v_slot(x, h, lane)];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) O[t][x] = mma(vf, p[t][h], O[t][x]);
+      }
   };
   // the end of a partition; rows whose own block is in it go on (MASKED)
   auto fold = [&](auto masked_, int b) {
@@ -458,9 +595,9 @@ __device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* s
       if (decltype(masked_)::value && b >= pos[t] >> 6) continue;
       float wa, wb;
       fold_weights(mt[t], m[t], wa, wb);
-      lt[t] = __builtin_fmaf(l[t], wb, lt[t] * wa);
+      lt[t] = __builtin_fmaf(l[t][0], wb, lt[t] * wa);
       m[t] = kNegInf;
-      l[t] = 0.f;
+      l[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int x = 0; x < DT; ++x) {
         f32x4& to = x < OR ? Ot[t][x < OR ? x : 0] : s_ot[t * OL + x - OR][threadIdx.x];
@@ -473,82 +610,66 @@ __device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* s
     }
   };
 
-  // the 8-bit blocks that every row sees
-  Bytes<D> y;
-  BlockRun run;
-  auto fetch = [&](int b) {
-    if ((b & 63) == 0) run = load_run(a, cache_row, hk, b, lane);
-    load_block<D>(a, run, hk, b, y, wave, lane);
-  };
-  int upto[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) upto[t] = 63;
-  if (b_hi > 0) {
-    fetch(0);
-    store_block<D>(y, sm[0], wave, lane);
-    if (SLOW && b_lo == 0) {
-      const uint64_t bad = bad_in_block<D>(y, wave);
-      if (lane == 0) s_bad[0][wave] = bad;
+  // the 8-bit blocks, a tile ahead in LDS and another on its way
+  auto put = [&](int t) __attribute__((always_inline)) {
+    put_k8<D>(y, ks, sm[t & 1], wave, lane);
+    put_v8<D>(y, vs, sm[t & 1], wave, lane);
+    if (P::kLds8 && threadIdx.x == 0) {
+      s_scale[t & 1][0] = ks;
+      s_scale[t & 1][1] = vs;
     }
-    if (b_hi > 1) fetch(1);
+    if (SLOW && t >= b_lo) {
+      const uint64_t bad = bad_in_block<D>(y, wave);
+      if (lane == 0) s_bad[t & 1][wave] = bad;
+    }
+  };
+  if (n_tiles > 0) {
+    put(0);
+    if (n_tiles > 1) fetch(1);
   }
   __syncthreads();
 #pragma unroll 1
-  for (int b = 0; b < b_lo; ++b) {
-    if (b + 1 < b_hi) {
-      store_block<D>(y, sm[(b + 1) & 1], wave, lane);
-      if (SLOW && b + 1 == b_lo) {
-        const uint64_t bad = bad_in_block<D>(y, wave);
-        if (lane == 0) s_bad[(b + 1) & 1][wave] = bad;
-      }
-    }
-    if (b + 2 < b_hi) fetch(b + 2);
-    if (has) tile(std::false_type{}, b & 1, upto);
-    if ((b + 1) % kPartBlocks == 0) fold(std::false_type{}, b);
-    __syncthreads();
-  }
-  // those that only later rows see
-#pragma unroll 1
-  for (int b = b_lo; b < b_hi; ++b) {
-    if (b + 1 < b_hi) {
-      store_block<D>(y, sm[(b + 1) & 1], wave, lane);
-      if (SLOW) {
-        const uint64_t bad = bad_in_block<D>(y, wave);
-        if (lane == 0) s_bad[(b + 1) & 1][wave] = bad;
-      }
-    }
-    if (b + 2 < b_hi) fetch(b + 2);
+  for (int b = 0; b < n_tiles; ++b) {
+    if (b + 1 < n_tiles) put(b + 1);
+    if (b + 2 < n_tiles) fetch(b + 2);
     if (has && b < w_hi) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) upto[t] = b < pos[t] >> 6 ? 63 : -1;
-      tile(std::true_type{}, b & 1, upto);
+      // MFMAs first: a wave that has some to issue goes before one in its
+      // softmax (1 x 10,240 at d = 256: 1,165 us; all alike 1,242)
+      __builtin_amdgcn_s_setprio(1);
+      scores(b & 1);
+      __builtin_amdgcn_s_setprio(0);
+      softmax(b >= w_lo);
+      __builtin_amdgcn_s_setprio(1);
+      products(b & 1, b >= w_lo);
+      __builtin_amdgcn_s_setprio(0);
     }
     if ((b + 1) % kPartBlocks == 0) fold(std::true_type{}, b);
     __syncthreads();
   }
-  // the own blocks
+  // the own blocks, as many at once as LDS holds
+  constexpr int kSlots = kRawSlots<D>;
 #pragma unroll 1
-  for (int b0 = b_lo; b0 <= b_hi; b0 += P::kRaw) {
+  for (int b0 = b_lo; b0 <= b_hi; b0 += kSlots) {
     if (b0 > b_lo) __syncthreads();
 #pragma unroll 1
-    for (int n = 0; n < P::kRaw && b0 + n <= b_hi; ++n) {
-      const uint64_t bad = stage_raw<D>(a, i, hk, ctx, end, c0, b0 + n, sm[n], wave, lane);
-      if (SLOW && lane == 0) s_bad[n][wave] = bad;
-    }
+    for (int n = 0; n < kSlots && b0 + n <= b_hi; n += 2)
+      stage_raw<D, SLOW>(a, i, hk, ctx, min(end, (b_hi + 1) * 64), c0, b0 + n, sm, n, s_bad, wave, lane);
     __syncthreads();
 #pragma unroll 1
-    for (int n = 0; has && n < P::kRaw; ++n) {
-      const int b = b0 + n;
-      if (b < w_lo || b > w_hi) continue;
+    for (int b = max(b0, w_lo); has && b <= min(b0 + kSlots - 1, w_hi); ++b) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) upto[t] = pos[t] >> 6 == b ? pos[t] & 63 : -1;
-      tile(std::true_type{}, n, upto);
+      raw_scores(b);
+      softmax(true);
+      raw_products(raw_slot<D>(sm, b - b0), b - b0);
     }
   }
   fold(std::false_type{}, 0);
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    const float inv = 1.f / sum_over_groups(lt[t]);
+    const float inv = 1.f / lt[t];
     const uint32_t row = w0 + t * 16 + r;
     if (row >= rows) continue;
     uint16_t* o = a.o + ((int64_t)(c0 + (int)(row / G)) * a.H + hk * a.G + (int)(row % G)) * D + g * 4;
@@ -563,26 +684,20 @@ __device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* s
 template <int D>
 __global__ __launch_bounds__(PrefillTile<D>::kThreads) void k_attn_prefill(const StepArgs a) {
   typedef PrefillTile<D> P;
-  __shared__ PrefillLds<D> sm[P::kRaw];
+  __shared__ PrefillLds<D> sm[2];
   __shared__ f32x4 s_ot[P::kOtLds ? P::kRT * P::kOtLds : 1][P::kThreads];
-  __shared__ uint64_t s_bad[P::kRaw][P::kWaves];
+  __shared__ uint64_t s_bad[kRawSlots<D>][P::kWaves];
+  __shared__ float s_scale[2][2];
   // neighbouring work-groups take different heads: with 2, 4, 8 .. heads each
   // chiplet, and its L2, sees the keys of some of them only
   const int hk = blockIdx.x % a.Hk;
-  // which sequence and rows: sequence i has the row-tile slots floor(cu[i] G / kRows) + i ..
-  const int item = (int)((gridDim.x - 1 - blockIdx.x) / a.Hk);  // later rows, which see more keys, first
-  int lo = 0, hi = a.N - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((int)((int64_t)a.cu[mid] * a.G / P::kRows) + mid <= item)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  const int i = lo, c0 = a.cu[i], len = a.cu[i + 1] - c0;
-  const int64_t row0 = (int64_t)(item - ((int)((int64_t)c0 * a.G / P::kRows) + i)) * P::kRows;
+  // which sequence and rows, longest first (TileOrder)
+  const i32x2 item = a.order[blockIdx.x / a.Hk];
+  const int i = item[0];
+  if (i < 0) return;
+  const int c0 = a.cu[i], len = a.cu[i + 1] - c0;
+  const int64_t row0 = (int64_t)item[1] * P::kRows;
   const int64_t rows = (int64_t)len * a.G;
-  if (row0 >= rows) return;
   const int ctx = a.ctx_len[i], cache_row = row_of(a.slot, i, a.cache.num_slots);
   if (ctx < 0 || cache_row < 0) {  // refused: o = 0
     const int n = (int)min(rows - row0, (int64_t)P::kRows);
@@ -599,20 +714,20 @@ __global__ __launch_bounds__(PrefillTile<D>::kThreads) void k_attn_prefill(const
   int bad = 0;
   for (int b = b_lo; b <= b_hi; ++b) bad |= a.bad[(int64_t)((c0 >> 6) + 2 * i + b - (ctx >> 6)) * a.Hk + hk];
   if (bad == 0)
-    prefill_rows<D, false>(a, sm, s_ot, s_bad, hk, i, cache_row, (uint32_t)row0, (uint32_t)rows, c0, ctx, ctx + len);
+    prefill_rows<D, false>(a, sm, s_ot, s_bad, s_scale, hk, i, cache_row, (uint32_t)row0, (uint32_t)rows, c0, ctx, ctx + len);
   else
-    prefill_rows<D, true>(a, sm, s_ot, s_bad, hk, i, cache_row, (uint32_t)row0, (uint32_t)rows, c0, ctx, ctx + len);
+    prefill_rows<D, true>(a, sm, s_ot, s_bad, s_scale, hk, i, cache_row, (uint32_t)row0, (uint32_t)rows, c0, ctx, ctx + len);
 }
 
 // ---------------------------------------------------------------------------
 // few rows per sequence: the decode step, and prefill of few new tokens
 
 // Records that join work-groups' shares of a row: per partition's unit
-// and key/value head, O [rec_rows][D], and per row m and the four partial l.
+// and key/value head, O [rec_rows][D], and per row m and l.
 struct RowsArgs {
   StepArgs s;
   float* rec_o;
-  float* rec_ml;  // [..][rec_rows][8]: m, -, -, -, l of the four lane groups
+  float* rec_ml;  // [..][rec_rows][2]: m, l
   int32_t* base;  // first unit of every sequence
   int32_t* total;  // how many units there are
   int max_parts;  // records that fit
@@ -680,7 +795,7 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
   constexpr int KS = D / 32, KP = D / 64, DT = D / 64, R = 16 * RT;  // DT: dim tiles of a wave
   __shared__ u32x4 s_p[4][RT][2][64];
   __shared__ f32x4 s_raw[4][RT][64];
-  __shared__ float s_max[4][RT][16], s_sum[4][RT][64];
+  __shared__ float s_max[4][RT][16];
   __shared__ int s_scan[4], s_at[2];
   __shared__ uint32_t s_red[4];
   const int hk = blockIdx.y, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
@@ -752,12 +867,13 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
 #pragma unroll
       for (int x = 0; x < KS; ++x) q[t][x] = *(const u32x4*)(qp + (x >> 1) * 64 + g * 16 + (x & 1) * 8);
     }
-    f32x4 O[RT][DT], Ot[RT][DT];  // the partition's, the folded total
-    float m[RT], l[RT], mt[RT], lt[RT];
+    f32x4 O[RT][DT], Ot[RT][DT], l[RT];  // the partition's, the folded total
+    float m[RT], mt[RT], lt[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       m[t] = mt[t] = kNegInf;
-      l[t] = lt[t] = 0.f;
+      lt[t] = 0.f;
+      l[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int x = 0; x < DT; ++x) O[t][x] = Ot[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
@@ -769,27 +885,32 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
         float* to = ra.rec_o + rec * D + wave * DT * 16 + g * 4;
 #pragma unroll
         for (int x = 0; x < DT; ++x) *(f32x4*)(to + x * 16) = o[t][x];
-        if (wave == 0) {
-          if (g == 0) ra.rec_ml[rec * 8] = mr[t];
-          ra.rec_ml[rec * 8 + 4 + g] = lr[t];
+        if (wave == 0 && g == 0) {
+          ra.rec_ml[rec * 2] = mr[t];
+          ra.rec_ml[rec * 2 + 1] = lr[t];
         }
       }
     };
     auto end_partition = [&](int p) __attribute__((always_inline)) {
-      if (p_lo > 0) record(p, O, m, l);
+      if (p_lo > 0) {
+        float l0[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) l0[t] = l[t][0];
+        record(p, O, m, l0);
+      }
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         if (p_lo == 0) {
           float wa, wb;
           fold_weights(mt[t], m[t], wa, wb);
-          lt[t] = __builtin_fmaf(l[t], wb, lt[t] * wa);
+          lt[t] = __builtin_fmaf(l[t][0], wb, lt[t] * wa);
 #pragma unroll
           for (int x = 0; x < DT; ++x)
 #pragma unroll
             for (int e = 0; e < 4; ++e) Ot[t][x][e] = __builtin_fmaf(O[t][x][e], wb, Ot[t][x][e] * wa);
         }
         m[t] = kNegInf;
-        l[t] = 0.f;
+        l[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int x = 0; x < DT; ++x) O[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
@@ -896,7 +1017,9 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
         const float mn = fmaxf(m[t], max_over_groups(max16(s)) * a.c), ref = ref_of(mn);
         alpha[t] = exp2_(m[t] - ref);
         m[t] = mn;
-        l[t] = __builtin_fmaf(l[t], alpha[t], probabilities(s, a.c, ref, p[t]));
+        probabilities(s, a.c, ref, p[t]);
+        l[t][0] *= alpha[t];
+        add_sum(p[t], l[t]);
       }
       // V: keys past the sequence's end are not there yet (whatever the tail
       // holds); decode's new one comes from the call
@@ -963,6 +1086,7 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
         fetch_raw(b_hi);
       }
       const bool mytile = more || b0 + wave < b_end;
+      mfma_done();
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         if (MULTI && b0 + wave >= b_lo) {  // only rows whose own block comes later see it
@@ -985,7 +1109,7 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
         if (mytile) {
           u32x4 pf[2];
           const float mine_ = wave == 0 ? mm[t][1] : wave == 1 ? mm[t][2] : wave == 2 ? mm[t][3] : mm[t][4];
-          s_sum[wave][t][lane] = probabilities(s[t], a.c, ref_of(mine_), pf);
+          probabilities(s[t], a.c, ref_of(mine_), pf);
           s_p[wave][t][0][lane] = pf[0];
           s_p[wave][t][1][lane] = pf[1];
         }
@@ -998,9 +1122,10 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           const float alpha = exp2_(mm[t][n] - ref_of(mm[t][n + 1]));
-          l[t] = __builtin_fmaf(l[t], alpha, s_sum[n][t][lane]);
           p[t][0] = s_p[n][t][0][lane];
           p[t][1] = s_p[n][t][1][lane];
+          l[t][0] *= alpha;
+          add_sum(p[t], l[t]);
 #pragma unroll
           for (int x = 0; x < DT; ++x) O[t][x] *= alpha;
         }
@@ -1092,7 +1217,7 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
     if (p_lo == 0 && p_hi == np) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        const float inv = 1.f / sum_over_groups(lt[t]);
+        const float inv = 1.f / lt[t];
         const uint32_t row = row0 + t * 16 + r;
         if (row > last_row) continue;
         uint16_t* o = a.o + ((int64_t)(c0 + (int)(row / (uint32_t)a.G)) * a.H + hk * a.G + (int)(row % (uint32_t)a.G)) * D +
@@ -1151,12 +1276,12 @@ __global__ __launch_bounds__(256) void k_attn_join(const RowsArgs ra, int W) {
   const int64_t step = (int64_t)a.Hk * ra.rec_rows, at = (int64_t)hk * ra.rec_rows + rr;
   const int64_t rec0 = base * step + at;
   fv O = *(const fv*)(ra.rec_o + rec0 * D + lane * V);
-  float m = ra.rec_ml[rec0 * 8], l = ra.rec_ml[rec0 * 8 + 4 + (lane & 3)];  // lanes 0 .. 3: the four partial sums
+  float m = ra.rec_ml[rec0 * 2], l = ra.rec_ml[rec0 * 2 + 1];
   // the others follow each other
   const int k = n - 1;
   const float* po = ra.rec_o + (cut * step + at) * D;
-  const float* pm = ra.rec_ml + (cut * step + at) * 8;
-  const int64_t so = step * D, sm = step * 8;
+  const float* pm = ra.rec_ml + (cut * step + at) * 2;
+  const int64_t so = step * D, sm = step * 2;
   auto batch = [&](auto size_, int j0, int u0, float mp, float& wa, float& wb) __attribute__((always_inline)) {
     constexpr int S = decltype(size_)::value;  // records asked for at once
     fv Op[S];
@@ -1165,7 +1290,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const RowsArgs ra, int W) {
 #pragma unroll
     for (int u = 0; u < S; ++u) {
       Op[u] = *(const fv*)(to + lane * V);
-      lp[u] = tm[4 + (lane & 3)];
+      lp[u] = tm[1];
       if (j0 + u0 + u + 1 < k) {  // past the last: the last again
         to += so;
         tm += sm;
@@ -1204,7 +1329,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const RowsArgs ra, int W) {
       batch(std::integral_constant<int, 16>{}, j0, 0, mp, wa, wb);
     }
   }
-  const float inv = 1.f / ((lane_of(l, 0) + lane_of(l, 1)) + (lane_of(l, 2) + lane_of(l, 3)));
+  const float inv = 1.f / l;
 #pragma unroll
   for (int e = 0; e < V; ++e) o[e] = (uint16_t)pack2(O[e] * inv, 0.f);
 }

@@ -354,14 +354,14 @@ RowsLayout rows_layout(size_t off, int32_t N, size_t rec_bytes) {
   L.total_word = off;
   off = align_up(off + sizeof(int32_t));
   L.rec = off;
-  L.rec_bytes = align_up(rec_bytes);
+  L.rec_bytes = align_up(rec_bytes) + 256;
   L.total = off + L.rec_bytes;
   return L;
 }
 
 // bytes of one partition's records: `rows` rows of each key/value head
 size_t record_bytes(const gdn_attn_shape& s, int rows) {
-  return (size_t)kv_heads(s) * rows * (s.head_dim + 8) * sizeof(float);
+  return (size_t)kv_heads(s) * rows * (s.head_dim + 2) * sizeof(float);
 }
 
 // A pool of num_blocks has num_blocks / 8 partitions, and one more per
@@ -384,8 +384,15 @@ constexpr size_t kFewRecordBytes = size_t(512) << 20;
 // rows of a chunk there; d = 256 has registers for one 16-row tile only
 int chunk_rows(const gdn_attn_shape& s, int64_t rows) { return s.head_dim == 256 || rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
+int tile_rows(const gdn_attn_shape& s) {
+  return s.head_dim == 64 ? PrefillTile<64>::kRows : s.head_dim == 128 ? PrefillTile<128>::kRows : PrefillTile<256>::kRows;
+}
+
+// k_attn_prefill's row tiles of a key/value head: every sequence's last may be short, and one in excess
+int64_t row_tiles(const gdn_attn_shape& s, int32_t N, int64_t T) { return T * (s.num_heads / kv_heads(s)) / tile_rows(s) + N; }
+
 struct PrefillLayout {
-  size_t old_k, old_v, bad, raw_k, raw_v;
+  size_t old_k, old_v, bad, order, raw_k, raw_v;
   RowsLayout rows;
   size_t total;
 };
@@ -400,6 +407,8 @@ PrefillLayout prefill_layout(const gdn_attn_shape& s, int32_t N, int64_t T, int3
   off = align_up(off + N * block);
   L.bad = off;
   off = align_up(off + (size_t)touched_blocks(N, T) * kv_heads(s) * sizeof(int32_t));
+  L.order = off;
+  off = align_up(off + sizeof(i32x2) * (size_t)row_tiles(s, N, T));
   if (T * (s.num_heads / kv_heads(s)) <= (int64_t)N * kMaxFewRows) {  // it may take k_attn_rows
     L.raw_k = off;
     off = align_up(off + (size_t)touched_blocks(N, T) * block);
@@ -494,9 +503,10 @@ void place_records(RowsArgs& a, const RowsLayout& L, char* ws, const gdn_attn_sh
   a.total = (int32_t*)(ws + L.total_word);
   a.chunk_rows = chunk;
   a.rec_rows = rows;
-  a.max_parts = (int)std::min<size_t>(L.rec_bytes / record_bytes(s, rows), INT32_MAX / 2);
+  // 256 bytes for aligning the second array
+  a.max_parts = (int)std::min<size_t>((L.rec_bytes - 256) / record_bytes(s, rows), INT32_MAX / 2);
   a.rec_ml = (float*)(ws + L.rec);
-  a.rec_o = a.rec_ml + (size_t)a.max_parts * a.s.Hk * rows * 8;
+  a.rec_o = a.rec_ml + align_up((size_t)a.max_parts * a.s.Hk * rows * 2 * sizeof(float)) / sizeof(float);
 }
 
 // Work-groups: two on each of 256 CUs, over the key/value heads.
@@ -509,10 +519,9 @@ gdn_status run_rows(const RowsArgs& a, int chunks, hipStream_t st, const char* f
 }
 
 template <int D>
-gdn_status run_prefill(const StepArgs& a, hipStream_t st, const char* fn) {
+gdn_status run_prefill(const StepArgs& a, int64_t tiles, hipStream_t st, const char* fn) {
   typedef PrefillTile<D> P;
-  hipLaunchKernelGGL((k_attn_append<D, false>), dim3((unsigned)touched_blocks(a.N, a.T), a.Hk), dim3(kAppendThreads<D>), 0, st, a);
-  const int64_t tiles = (int64_t)a.T * a.G / P::kRows + a.N;
+  hipLaunchKernelGGL((k_attn_append<D, false>), dim3((unsigned)touched_blocks(a.N, a.T) + 1, a.Hk), dim3(kAppendThreads<D>), 0, st, a);
   hipLaunchKernelGGL(k_attn_prefill<D>, dim3((unsigned)(tiles * a.Hk)), dim3(P::kThreads), 0, st, a);
   return launch_status(fn);
 }
@@ -562,10 +571,13 @@ extern "C" gdn_status gdn_attn_prefill(const gdn_attn_shape* shape, int32_t num_
       default: return run_few<256>(ra, chunks, (hipStream_t)stream, fn);
     }
   }
+  a.order = (i32x2*)(ws + L.order);
+  a.tile_rows = tile_rows(*shape);
+  const int64_t tiles = row_tiles(*shape, num_seqs, total_tokens);
   switch (shape->head_dim) {
-    case 64: return run_prefill<64>(a, (hipStream_t)stream, fn);
-    case 128: return run_prefill<128>(a, (hipStream_t)stream, fn);
-    default: return run_prefill<256>(a, (hipStream_t)stream, fn);
+    case 64: return run_prefill<64>(a, tiles, (hipStream_t)stream, fn);
+    case 128: return run_prefill<128>(a, tiles, (hipStream_t)stream, fn);
+    default: return run_prefill<256>(a, tiles, (hipStream_t)stream, fn);
   }
 }
 

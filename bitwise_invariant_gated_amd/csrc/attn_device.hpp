@@ -55,14 +55,6 @@ __device__ __forceinline__ float max_over_groups(float x) {
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
-// sum over the same four lanes, (l + l^16) + (l^32 + l^48)
-__device__ __forceinline__ float sum_over_groups(float x) {
-  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
 // Sum over aligned groups of L lanes (8, 16 or 32); every lane gets it, the
 // same bits in each (a butterfly of commutative adds).
 template <int L>

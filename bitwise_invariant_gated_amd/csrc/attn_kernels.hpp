@@ -7,13 +7,18 @@
 //   tokens up to the row in the input type.  A block of 64 keys is one tile:
 //     s    = K q, v_mfma_f32_16x16x32_bf16, k steps ascending (dims 64 kp +
 //            16 g + 8 h .. + 7 in slot group g of step 2 kp + h)
-//     m'   = max(m, c max(s)), c = scale * log2(e)
+//     m'   = c max(s) if that is more than m + 8, m if not; c = scale * log2(e)
 //     p    = exp2(fma(s, c, -m')), alpha = exp2(m - m')
 //     O    = alpha O + V^T p, p in bf16, two MFMA k steps
 //     l    = the same with V = 1, so numerator and denominator have the same p
 //   partitions: (m, l, O) = fold of the total and the partition, left to
 //   right: O = fma(Op, exp2(mp - m'), O exp2(m - m')).
 //   o = O (1 / l).
+// m is a reference for the exponents, not the maximum itself: it moves, and O
+// and l are scaled, only when p would pass 2^8, which bf16 and the 32-bit sums hold
+// as exactly as 1.  Of random scores a partition's first tile sets it for the rest,
+// where a true running maximum moves for some row of 16 in nearly every tile
+// (prefill, 5 x 2,048 at d = 128: 163 us a call; with the maximum 170).
 // A masked tile leaves a row's state as it is (alpha = 1, p = 0), so which
 // tiles a kernel walks through for a row beyond its own does not matter,
 // and neither does which work-group does which partition.
@@ -64,12 +69,16 @@ __device__ __forceinline__ void mfma_done() {
 // max of a lane's 16 scores, after mfma_done().  v_max3_f32 by name: of fmaxf
 // the compiler makes one more instruction per score, to quiet NaNs that
 // v_max3_f32 passes over by itself.
-__device__ __forceinline__ float max16(const f32x4 (&s)[4]) {
-  float m = fmaxf(s[3][2], s[3][3]);
-#pragma unroll
-  for (int i = 0; i < 14; i += 2)
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(m), "v"(s[i >> 2][i & 3]), "v"(s[(i + 1) >> 2][(i + 1) & 3]));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(c));
   return m;
+}
+
+__device__ __forceinline__ float max16(const f32x4 (&s)[4]) {
+  const float a = max3(s[0][0], s[0][1], s[0][2]), b = max3(s[0][3], s[1][0], s[1][1]), c = max3(s[1][2], s[1][3], s[2][0]);
+  const float d = max3(s[2][1], s[2][2], s[2][3]), e = max3(s[3][0], s[3][1], s[3][2]);
+  return max3(max3(a, b, c), max3(d, e, s[3][3]), s[3][3]);
 }
 
 // scores -> p: their bf16 B fragments for the two PV steps
@@ -91,7 +100,10 @@ __device__ __forceinline__ void add_sum(const u32x4 (&p)[2], f32x4& l) {
   l = mma(ones, p[1], mma(ones, p[0], l));
 }
 
-// the running max as a reference for exp2 (a row that has seen nothing: 0)
+// the reference after a tile whose scores have the maximum x / c
+__device__ __forceinline__ float move_ref(float m, float x) { return x > m + 8.f ? x : m; }
+
+// as an exponent's reference (a row that has seen nothing: 0)
 __device__ __forceinline__ float ref_of(float m) { return m == kNegInf ? 0.f : m; }
 
 // Weights of the total and of a partition in their fold, and the new max.
@@ -470,25 +482,35 @@ __device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* s
   };
   auto softmax = [&](bool masked) __attribute__((always_inline)) {
     mfma_done();
+    if (masked) {
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      if (masked) {
+      for (int t = 0; t < RT; ++t) {
         const int lim = upto[t] - 16 * g;
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[t][sub][e] = 4 * sub + e <= lim ? s[t][sub][e] : kNegInf;
       }
-      const float mn = fmaxf(m[t], max_over_groups(max16(s[t])) * a.c), ref = ref_of(mn);
-      const float alpha = exp2_(m[t] - ref);
-      m[t] = mn;
-      probabilities(s[t], a.c, ref, p[t]);
-      if (__any(alpha != 1.f)) {
-        l[t][0] *= alpha;
+    }
+    float alpha[RT];
+    bool moved = false;
 #pragma unroll
-        for (int x = 0; x < DT; ++x) O[t][x] *= alpha;
+    for (int t = 0; t < RT; ++t) {
+      const float mn = move_ref(m[t], max_over_groups(max16(s[t])) * a.c);
+      moved |= mn != m[t];
+      alpha[t] = exp2_(m[t] - ref_of(mn));
+      m[t] = mn;
+    }
+    if (__any(moved)) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        l[t][0] *= alpha[t];
+#pragma unroll
+        for (int x = 0; x < DT; ++x) O[t][x] *= alpha[t];
       }
     }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) probabilities(s[t], a.c, ref_of(m[t]), p[t]);
   };
   // O += V^T p of a tile with keys whose V is not finite (s_bad): one product
   // for every number n of them that a row may see, the first n as they
@@ -1014,7 +1036,7 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[sub][e] = 16 * g + 4 * sub + e <= upto[t] ? s[sub][e] : kNegInf;
         }
-        const float mn = fmaxf(m[t], max_over_groups(max16(s)) * a.c), ref = ref_of(mn);
+        const float mn = move_ref(m[t], max_over_groups(max16(s)) * a.c), ref = ref_of(mn);
         alpha[t] = exp2_(m[t] - ref);
         m[t] = mn;
         probabilities(s, a.c, ref, p[t]);
@@ -1100,12 +1122,12 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
         if (g == 0) s_max[wave][t][r] = smax;
       }
       __syncthreads();
-      float mm[RT][5];  // the running max before and after every tile
+      float mm[RT][5];  // the reference before and after every tile
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         mm[t][0] = m[t];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) mm[t][n + 1] = more || b0 + n < b_end ? fmaxf(mm[t][n], s_max[n][t][r] * a.c) : mm[t][n];
+        for (int n = 0; n < 4; ++n) mm[t][n + 1] = more || b0 + n < b_end ? move_ref(mm[t][n], s_max[n][t][r] * a.c) : mm[t][n];
         if (mytile) {
           u32x4 pf[2];
           const float mine_ = wave == 0 ? mm[t][1] : wave == 1 ? mm[t][2] : wave == 2 ? mm[t][3] : mm[t][4];

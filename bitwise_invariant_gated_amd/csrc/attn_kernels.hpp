@@ -797,10 +797,11 @@ __device__ __forceinline__ int run_of(int total, int W, int x) {
 // All units of the batch in a row, sequence by sequence and chunk by chunk,
 // are dealt out in equal runs to the W work-groups of a key/value head
 // (blockIdx.x of gridDim.x): a batch of any lengths is balanced to one
-// partition.  A chunk's first units are its partitions.  A run that begins a chunk folds its partitions as it goes; one
-// that begins inside a chunk must leave each partition by itself, because
-// the fold goes left to right.  If the batch has more partitions than there
-// is room for records (sequences that share blocks), sequences are dealt out whole.
+// partition.  A chunk's first units are its partitions.  A run that begins a
+// chunk folds its partitions as it goes; one that begins inside a chunk must
+// leave each partition by itself, because the fold goes left to right.  If the
+// batch has more units than there is room for records, chunks (decode:
+// sequences) are dealt out whole.
 //
 // In a work-group the four waves share a partition, four tiles at a time: wave
 // w computes the scores and p of tile w; p goes through LDS and every wave
@@ -812,7 +813,7 @@ __device__ __forceinline__ int run_of(int total, int W, int x) {
 // (last block) or raw_k, raw_v (blocks that they filled).  Otherwise one each,
 // which this kernel appends itself.
 template <int D, int RT, bool MULTI>
-__global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(const RowsArgs ra) {
+__global__ __launch_bounds__(256, D == 256 || RT == 2 ? 2 : 3) void k_attn_rows(const RowsArgs ra) {
   const StepArgs& a = ra.s;
   constexpr int KS = D / 32, KP = D / 64, DT = D / 64, R = 16 * RT;  // DT: dim tiles of a wave
   __shared__ u32x4 s_p[4][RT][2][64];
@@ -837,10 +838,10 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
   __syncthreads();
   const int total = s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
   for (int w = 0; w < wave; ++w) upto_ += s_scan[w];
-  const bool whole_seqs = total > ra.max_parts;
+  const bool whole = total > ra.max_parts;
   const int g0 = run_begin(total, W, blockIdx.x), g1 = run_begin(total, W, blockIdx.x + 1);
   if (blockIdx.x == 0 && hk == 0 && tid == 0) *ra.total = total;
-  if (g0 >= g1 && !whole_seqs) return;
+  if (g0 >= g1 && !whole) return;
   if (g0 >= upto_ - mine && g0 < upto_) {
     int at = upto_ - mine, n = n0;
     for (; n < n1 - 1; ++n) {
@@ -852,27 +853,34 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
     s_at[1] = at;
   }
   __syncthreads();
-  int i = whole_seqs ? blockIdx.x : s_at[0], base = whole_seqs ? 0 : s_at[1], c = 0;
+  int i = whole ? (MULTI ? 0 : blockIdx.x) : s_at[0], base = whole ? 0 : s_at[1], c = 0;
+  auto skip = [&](int n) {  // n chunks further
+    c += n;
+    for (int k; i < a.N && c >= (k = max(1, chunks_of(ra, len_of(ra, i)))); ++i) c -= k;
+  };
+  if (MULTI && whole) skip(blockIdx.x);
 
-  for (int f = g0; whole_seqs ? i < a.N : f < g1;) {
+  for (int f = g0; whole ? i < a.N : f < g1;) {
     const int ctx = a.ctx_len[i], len = MULTI ? len_of(ra, i) : 1;
     const int np = ctx < 0 || len <= 0 ? 0 : parts_of(ra, ctx, len, c);
-    if (c == 0 && np > 0 && !whole_seqs && hk == 0 && tid == 0 && f == base) ra.base[i] = base;
-    if (np == 0 || (!whole_seqs && f >= base + np)) {  // nothing there, or behind it
+    if (c == 0 && np > 0 && !whole && hk == 0 && tid == 0 && f == base) ra.base[i] = base;
+    if (np == 0 || (!whole && f >= base + np)) {  // nothing there, or behind it
       if (np) base += np + kChunkCost;
       f = max(f, base);
-      if (np && c + 1 < chunks_of(ra, len)) {
+      if (MULTI && whole) {
+        skip(W);
+      } else if (np && c + 1 < chunks_of(ra, len)) {
         ++c;
       } else {
         c = 0;
-        i += whole_seqs ? W : 1;
+        i += !MULTI && whole ? W : 1;
       }
       continue;
     }
     const int c0 = MULTI ? a.cu[i] : i, end = ctx + len;
     const uint32_t rows = (uint32_t)len * (uint32_t)a.G, row0 = (uint32_t)c * R;
     const uint32_t last_row = min(row0 + R, rows) - 1;
-    const int p_lo = whole_seqs ? 0 : f - base, p_hi = whole_seqs ? np : min(np, g1 - base);
+    const int p_lo = whole ? 0 : f - base, p_hi = whole ? np : min(np, g1 - base);
     const int cache_row = max(row_of(a.slot, i, a.cache.num_slots), 0);
     // own blocks of the chunk's rows (there are two at most)
     const int b_lo = (ctx + (int)(row0 / (uint32_t)a.G)) >> 6, b_hi = (ctx + (int)(last_row / (uint32_t)a.G)) >> 6;
@@ -1250,15 +1258,19 @@ __global__ __launch_bounds__(256, D == 256 || RT > 1 ? 2 : 3) void k_attn_rows(c
       }
     }
     __syncthreads();  // LDS is used again by the next chunk
-    f = whole_seqs ? 0 : base + p_hi;
-    if (whole_seqs || p_hi == np) {
+    if (MULTI && whole) {
+      skip(W);
+      continue;
+    }
+    f = whole ? 0 : base + p_hi;
+    if (whole || p_hi == np) {
       base += np + kChunkCost;
       f = max(f, base);
       if (c + 1 < chunks_of(ra, len)) {
         ++c;
       } else {
         c = 0;
-        i += whole_seqs ? W : 1;
+        i += whole ? W : 1;
       }
     }
   }

@@ -376,13 +376,31 @@ RowsLayout decode_layout(const gdn_attn_shape& s, int32_t N, int32_t num_blocks)
   return rows_layout(0, N, (size_t)pool_parts(N, num_blocks) * chunks * record_bytes(s, decode_rows(s)));
 }
 
-// Prefill takes k_attn_rows if no sequence has more rows than this.
-constexpr int kMaxFewRows = 256;
-// Its records, as far as this bound (beyond, sequences go to work-groups whole).
-constexpr size_t kFewRecordBytes = size_t(512) << 20;
+// Prefill by k_attn_rows: rows of a chunk.  d = 256 has registers for one
+// 16-row tile; with 64 rows, four tiles, the others spill (16 x 37 new tokens
+// after 5,000, 4 query heads to each of 8: 130 us instead of 116 at d = 64, 291 instead of 177 at 128).
+int chunk_rows(const gdn_attn_shape& s, int64_t rows) { return s.head_dim == 256 || rows <= 16 ? 16 : 32; }
 
-// rows of a chunk there; d = 256 has registers for one 16-row tile only
-int chunk_rows(const gdn_attn_shape& s, int64_t rows) { return s.head_dim == 256 || rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Work-groups of k_attn_rows: two on each of 256 CUs, over the key/value heads.
+constexpr int kRowsGroups = 512;
+
+// Prefill takes k_attn_rows, which splits the keys and reads them once per
+// chunk, if the batch has no more chunks than this, each sequence counted with the
+// most rows of any, or a sequence one only; else k_attn_prefill, which splits rows
+// only, 256 to a work-group.  Turns after 5,000, 4 query heads to each of 8,
+// k_attn_rows / k_attn_prefill in us, d = 64 and d = 128: 512 chunks 81 / 100 and 131 / 153,
+// 640 chunks 116 / 129 and 177 / 171, 1,024 chunks 151 / 134 and 239 / 180; d = 256, 8 to each of
+// 2, 256 chunks 141 / 212, 512 chunks 225 / 215, 1,024 chunks 476 / 224.
+constexpr int kMostChunks = 640;
+
+bool takes_rows(const gdn_attn_shape& s, int32_t N, int64_t rows) {
+  const int chunk = chunk_rows(s, rows);
+  const int64_t chunks = (rows + chunk - 1) / chunk;
+  return chunks <= 1 || N * (int64_t)kv_heads(s) * chunks <= kMostChunks;
+}
+
+// Its records, as far as this bound (beyond, chunks go to work-groups whole).
+constexpr size_t kFewRecordBytes = size_t(512) << 20;
 
 int tile_rows(const gdn_attn_shape& s) {
   return s.head_dim == 64 ? PrefillTile<64>::kRows : s.head_dim == 128 ? PrefillTile<128>::kRows : PrefillTile<256>::kRows;
@@ -409,12 +427,16 @@ PrefillLayout prefill_layout(const gdn_attn_shape& s, int32_t N, int64_t T, int3
   off = align_up(off + (size_t)touched_blocks(N, T) * kv_heads(s) * sizeof(int32_t));
   L.order = off;
   off = align_up(off + sizeof(i32x2) * (size_t)row_tiles(s, N, T));
-  if (T * (s.num_heads / kv_heads(s)) <= (int64_t)N * kMaxFewRows) {  // it may take k_attn_rows
+  const int64_t G = s.num_heads / kv_heads(s);
+  if (N > 0 && takes_rows(s, N, (T * G + N - 1) / N)) {  // it may, if no sequence has many more than the others
+    const int chunk = chunk_rows(s, 32);
+    const int64_t most = std::max<int64_t>(1, kMostChunks / (N * (int64_t)kv_heads(s)));
+    const size_t chunks = (size_t)std::min(most, (T * G + chunk - 1) / chunk);
     L.raw_k = off;
     off = align_up(off + (size_t)touched_blocks(N, T) * block);
     L.raw_v = off;
     off = align_up(off + (size_t)touched_blocks(N, T) * block);
-    L.rows = rows_layout(off, N, std::min(kFewRecordBytes, (size_t)pool_parts(N, num_blocks) * record_bytes(s, kMaxFewRows + 64)));
+    L.rows = rows_layout(off, N, std::min(kFewRecordBytes, (size_t)pool_parts(N, num_blocks) * chunks * record_bytes(s, chunk)));
     off = L.rows.total;
   }
   L.total = off;
@@ -509,10 +531,9 @@ void place_records(RowsArgs& a, const RowsLayout& L, char* ws, const gdn_attn_sh
   a.rec_o = a.rec_ml + align_up((size_t)a.max_parts * a.s.Hk * rows * 2 * sizeof(float)) / sizeof(float);
 }
 
-// Work-groups: two on each of 256 CUs, over the key/value heads.
 template <int D, int RT, bool MULTI>
 gdn_status run_rows(const RowsArgs& a, int chunks, hipStream_t st, const char* fn) {
-  const int W = std::max(1, std::min(512 / a.s.Hk, a.max_parts));
+  const int W = std::max(1, std::min(kRowsGroups / a.s.Hk, a.max_parts));
   hipLaunchKernelGGL((k_attn_rows<D, RT, MULTI>), dim3(W, a.s.Hk), dim3(256), 0, st, a);
   hipLaunchKernelGGL(k_attn_join<D>, dim3(a.s.N, a.s.Hk, (chunks * a.rec_rows + 3) / 4), dim3(256), 0, st, a, W);
   return launch_status(fn);
@@ -532,7 +553,6 @@ gdn_status run_few(const RowsArgs& a, int chunks, hipStream_t st, const char* fn
   if (a.chunk_rows == 16) return run_rows<D, 1, true>(a, chunks, st, fn);
   if constexpr (D < 256) {
     if (a.chunk_rows == 32) return run_rows<D, 2, true>(a, chunks, st, fn);
-    return run_rows<D, 4, true>(a, chunks, st, fn);
   }
   return fail(GDN_ERR_UNSUPPORTED, "%s: rows", fn);
 }
@@ -558,7 +578,7 @@ extern "C" gdn_status gdn_attn_prefill(const gdn_attn_shape* shape, int32_t num_
   a.old_v = (uint16_t*)(ws + L.old_v);
   a.bad = (int32_t*)(ws + L.bad);
   const int64_t most = (int64_t)(max_new > 0 ? std::min<int64_t>(max_new, total_tokens) : total_tokens) * a.G;
-  if (most <= kMaxFewRows && L.rows.rec_bytes > 0) {
+  if (L.rows.rec_bytes > 0 && takes_rows(*shape, num_seqs, most)) {
     RowsArgs ra{};
     a.raw_k = (uint16_t*)(ws + L.raw_k);
     a.raw_v = (uint16_t*)(ws + L.raw_v);

@@ -771,7 +771,9 @@ __device__ __forceinline__ int parts_of(const RowsArgs& a, int ctx, int len, int
 __device__ __forceinline__ int len_of(const RowsArgs& a, int i) { return a.s.cu ? a.s.cu[i + 1] - a.s.cu[i] : 1; }
 
 // What a chunk costs, in units of a partition: its partitions, and its own
-// block, first loads and outputs, which took about as long as two (d = 128).
+// block, first loads and outputs, which take about as long as two (with one, 16 x 16
+// tokens of 8 heads each to 2 at d = 256 took 169 us instead of 143; with none, decode
+// of 256 x 4,096 203 instead of 197).
 constexpr int kChunkCost = 2;
 
 // units of all chunks of sequence i
@@ -794,6 +796,15 @@ __device__ __forceinline__ int run_of(int total, int W, int x) {
   return x < first ? x / (per + 1) : more + (x - first) / per;
 }
 
+// Work-groups of k_attn_rows that share a CU.  With one its waves have all
+// registers, and what hides the memory's latency are the loads that a wave has in
+// flight (decode, 256 x 4,096 at d = 128: 175 us; with two, whose loop spilled, 198;
+// 16 x 16 new tokens at d = 256: 114 us; two 143); fewer runs also leave fewer records.
+// Several new tokens at d = 64 and 128 keep the MFMAs busier with two (16 x 37 tokens at d = 64:
+// 118 us; one 144, three 131).
+template <int D, bool MULTI>
+constexpr int kRowsPerCu = MULTI && D < 256 ? 2 : 1;
+
 // All units of the batch in a row, sequence by sequence and chunk by chunk,
 // are dealt out in equal runs to the W work-groups of a key/value head
 // (blockIdx.x of gridDim.x): a batch of any lengths is balanced to one
@@ -813,7 +824,7 @@ __device__ __forceinline__ int run_of(int total, int W, int x) {
 // (last block) or raw_k, raw_v (blocks that they filled).  Otherwise one each,
 // which this kernel appends itself.
 template <int D, int RT, bool MULTI>
-__global__ __launch_bounds__(256, D == 256 || RT == 2 ? 2 : 3) void k_attn_rows(const RowsArgs ra) {
+__global__ __launch_bounds__(256, (kRowsPerCu<D, MULTI>)) void k_attn_rows(const RowsArgs ra) {
   const StepArgs& a = ra.s;
   constexpr int KS = D / 32, KP = D / 64, DT = D / 64, R = 16 * RT;  // DT: dim tiles of a wave
   __shared__ u32x4 s_p[4][RT][2][64];

@@ -6,8 +6,10 @@
 //   plan           k_attn_plan (and k_attn_plan_tokens for many tokens)
 //   norm + rope    k_attn_norm_rope; its gradient k_attn_norm_rope_bwd and
 //                  k_attn_norm_rope_dw
-//   prefill        k_attn_append (tails, full blocks), k_attn_prefill
-//   decode step    k_attn_decode (attention and append), k_attn_join
+//   prefill        k_attn_append (tails, full blocks), then k_attn_prefill, or
+//                  k_attn_rows and k_attn_join (takes_rows)
+//   decode step    k_attn_rows (attention and append), k_attn_join
+//   cache read     k_attn_cache_read
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -381,9 +383,6 @@ RowsLayout decode_layout(const gdn_attn_shape& s, int32_t N, int32_t num_blocks)
 // after 5,000, 4 query heads to each of 8: 130 us instead of 116 at d = 64, 291 instead of 177 at 128).
 int chunk_rows(const gdn_attn_shape& s, int64_t rows) { return s.head_dim == 256 || rows <= 16 ? 16 : 32; }
 
-// Work-groups of k_attn_rows: two on each of 256 CUs, over the key/value heads.
-constexpr int kRowsGroups = 512;
-
 // Prefill takes k_attn_rows, which splits the keys and reads them once per
 // chunk, if the batch has no more chunks than this, each sequence counted with the
 // most rows of any, or a sequence one only; else k_attn_prefill, which splits rows
@@ -533,7 +532,7 @@ void place_records(RowsArgs& a, const RowsLayout& L, char* ws, const gdn_attn_sh
 
 template <int D, int RT, bool MULTI>
 gdn_status run_rows(const RowsArgs& a, int chunks, hipStream_t st, const char* fn) {
-  const int W = std::max(1, std::min(kRowsGroups / a.s.Hk, a.max_parts));
+  const int W = std::max(1, std::min(256 * kRowsPerCu<D, MULTI> / a.s.Hk, a.max_parts));  // 256 CUs
   hipLaunchKernelGGL((k_attn_rows<D, RT, MULTI>), dim3(W, a.s.Hk), dim3(256), 0, st, a);
   hipLaunchKernelGGL(k_attn_join<D>, dim3(a.s.N, a.s.Hk, (chunks * a.rec_rows + 3) / 4), dim3(256), 0, st, a, W);
   return launch_status(fn);

@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .api import _DTYPES, _ptr, _stream
+from .api import _DTYPES, _ptr
 
 BLOCK = _lib.GDN_ATTN_BLOCK
 
@@ -29,12 +29,12 @@ class AttnShape:
     def __post_init__(self):
         if self.dtype not in _DTYPES:
             raise ValueError(f"unsupported dtype {self.dtype}")
-        object.__setattr__(self, "_c", _lib.AttnShapeC(self.num_heads, self.num_kv_heads, self.head_dim,
-                                                       _DTYPES[self.dtype]))
+        object.__setattr__(self, "kv_heads", self.num_kv_heads or self.num_heads)
+        object.__setattr__(self, "_ref", ctypes.byref(_lib.AttnShapeC(self.num_heads, self.num_kv_heads, self.head_dim,
+                                                                      _DTYPES[self.dtype])))
 
-    @property
-    def kv_heads(self) -> int:
-        return self.num_kv_heads or self.num_heads
+    def __reduce__(self):
+        return AttnShape, (self.num_heads, self.num_kv_heads, self.head_dim, self.dtype)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -61,7 +61,7 @@ class AttnPool:
         slots, width = self.block_table.shape
         if self.blocks_held.numel() != slots or self.seq_len.numel() != slots or self.free_count.numel() != 1:
             raise ValueError("pool arrays do not match the block table")
-        object.__setattr__(self, "_c", _lib.AttnPoolC(*map(_ptr, t), slots, width, self.free_blocks.numel()))
+        object.__setattr__(self, "_ref", ctypes.byref(_lib.AttnPoolC(*map(_ptr, t), slots, width, self.free_blocks.numel())))
 
 
 def alloc_attn_pool(num_slots: int, max_blocks: int, num_blocks: int, device="cuda") -> AttnPool:
@@ -91,9 +91,9 @@ class AttnPlan:
             if self.slot_index.numel() != self.ctx_len.numel():
                 raise ValueError("slot_index and ctx_len differ in length")
         slots, width = self.block_table.shape
-        object.__setattr__(self, "_c", _lib.AttnStepC(
+        object.__setattr__(self, "_ref", ctypes.byref(_lib.AttnStepC(
             _ptr(self.ctx_len), _ptr(self.positions), _ptr(self.slot_map), _ptr(self.status), _ptr(self.block_table),
-            _ptr(self.slot_index), width, slots))
+            _ptr(self.slot_index), width, slots)))
 
 
 def alloc_attn_plan(pool: AttnPool, num_seqs: int, total_tokens: int,
@@ -127,9 +127,9 @@ class AttnCache:
         _check_types((self.k8, self.v8), torch.uint8)
         _check_types((self.k_scale, self.v_scale), torch.float32)
         _check_types((self.tail_k, self.tail_v), torch.bfloat16)
-        object.__setattr__(self, "_c", _lib.AttnCacheC(
+        object.__setattr__(self, "_ref", ctypes.byref(_lib.AttnCacheC(
             _ptr(self.k8), _ptr(self.v8), _ptr(self.k_scale), _ptr(self.v_scale), _ptr(self.tail_k),
-            _ptr(self.tail_v), blocks, slots))
+            _ptr(self.tail_v), blocks, slots)))
 
     def check(self, shape: AttnShape) -> None:
         if self.tail_k.shape[1] != shape.kv_heads or self.tail_k.shape[3] != shape.head_dim:
@@ -149,13 +149,21 @@ def alloc_attn_cache(shape: AttnShape, num_blocks: int, num_slots: int, device="
 
 def gdn_attn_workspace_size(shape: AttnShape, op: int, total_tokens: int, num_seqs: int = 0,
                             num_blocks: int = 0) -> int:
-    return int(_lib.load().gdn_attn_workspace_size(ctypes.byref(shape._c), op, total_tokens, num_seqs, num_blocks))
+    return int(_lib.load().gdn_attn_workspace_size(shape._ref, op, total_tokens, num_seqs, num_blocks))
 
 
 def alloc_attn_workspace(shape: AttnShape, op: int, total_tokens: int, num_seqs: int = 0, num_blocks: int = 0,
                          device="cuda") -> torch.Tensor:
     n = gdn_attn_workspace_size(shape, op, total_tokens, num_seqs, num_blocks)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _stream(stream) -> int:
+    """The stream's handle, or that of the current one, without making a torch.cuda.Stream
+    of it (2.5 us, where a call of one token takes 7 in all)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check_types(tensors, dtype) -> None:
@@ -165,18 +173,19 @@ def _check_types(tensors, dtype) -> None:
 
 
 def _rows(t: torch.Tensor, heads: int, d: int, dtype, name: str):
-    """(pointer, token stride) of a [T, heads, d] tensor whose heads and dims are contiguous."""
+    """(tokens, pointer, token stride) of a [T, heads, d] tensor whose heads and dims are contiguous."""
     shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.dtype != dtype:
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.dtype is not dtype:
         raise ValueError(f"{name}: [T, {heads}, {d}] of {dtype} expected, {tuple(shape)} of {t.dtype} given")
+    n = shape[0]
     s0, s1, s2 = t.stride()
-    if shape[0] and (s2 != 1 or (heads > 1 and s1 != d)):
+    if n and (s2 != 1 or (heads > 1 and s1 != d)):
         raise ValueError(f"{name}: heads and dims must be contiguous")
-    if shape[0] <= 1:
+    if n <= 1:
         s0 = 0  # a single token's stride is not used
     elif s0 < heads * d:
         raise ValueError(f"{name}: tokens overlap")
-    return t.data_ptr(), s0
+    return n, t.data_ptr(), s0
 
 
 def gdn_attn_plan(pool: AttnPool, cu_seqlens, plan: AttnPlan, advance: bool = True, stream=None) -> None:
@@ -184,30 +193,30 @@ def gdn_attn_plan(pool: AttnPool, cu_seqlens, plan: AttnPlan, advance: bool = Tr
     n = plan.ctx_len.numel()
     if cu_seqlens.numel() != n + 1 or cu_seqlens.dtype != torch.int32:
         raise ValueError(f"cu_seqlens: int32 of {n + 1} expected")
-    _lib.check(_lib.load().gdn_attn_plan(ctypes.byref(pool._c), n, plan.positions.numel(), _ptr(cu_seqlens),
-                                         int(advance), ctypes.byref(plan._c), _stream(stream)))
+    _lib.check(_lib.load().gdn_attn_plan(pool._ref, n, plan.positions.numel(), _ptr(cu_seqlens),
+                                         int(advance), plan._ref, _stream(stream)))
 
 
 def gdn_attn_release(pool: AttnPool, slot_index, stream=None) -> None:
     """The blocks of the given cache rows go back to the pool."""
     _check_types((slot_index,), torch.int32)
-    _lib.check(_lib.load().gdn_attn_release(ctypes.byref(pool._c), slot_index.numel(), _ptr(slot_index),
+    _lib.check(_lib.load().gdn_attn_release(pool._ref, slot_index.numel(), _ptr(slot_index),
                                             _stream(stream)))
 
 
 def _rope_c(rope: AttnRope, cos_sin, positions, tokens: int):
     n_pos = 0
     if rope.rotary_dim:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != rope.rotary_dim:
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != rope.rotary_dim:
             raise ValueError(f"cos_sin: float32 [positions, {rope.rotary_dim}] expected")
-        if positions.dtype != torch.int32 or positions.numel() < tokens:
+        if positions.dtype is not torch.int32 or positions.numel() < tokens:
             raise ValueError("positions: int32 of every token expected")
         n_pos = cos_sin.shape[0]
-    return _lib.AttnRopeC(rope.rotary_dim, int(rope.interleaved), int(rope.zero_centered), n_pos, rope.eps)
+    return ctypes.byref(_lib.AttnRopeC(rope.rotary_dim, rope.interleaved, rope.zero_centered, n_pos, rope.eps))
 
 
 def _weight(w, d: int, name: str):
-    if w.dtype != torch.float32 or w.numel() != d:
+    if w.dtype is not torch.float32 or w.numel() != d:
         raise ValueError(f"{name}: float32 of {d} expected")
     return _ptr(w)
 
@@ -216,35 +225,31 @@ def gdn_attn_qk_norm_rope(shape: AttnShape, rope: AttnRope, q, k, w_q, w_k, cos_
                           stream=None) -> None:
     """RMS norm of every head of q and k and the rotation; q_out, k_out may be q, k."""
     h, hk, d, dt = shape.num_heads, shape.kv_heads, shape.head_dim, shape.dtype
-    t = q.shape[0]
-    if k.shape[0] != t or q_out.shape[0] != t or k_out.shape[0] != t:
+    t, qp, qs = qrows = _rows(q, h, d, dt, "q")
+    tk, kp, ks = krows = _rows(k, hk, d, dt, "k")
+    tqo, qo, qos = qrows if q_out is q else _rows(q_out, h, d, dt, "q_out")
+    tko, ko, kos = krows if k_out is k else _rows(k_out, hk, d, dt, "k_out")
+    if not t == tk == tqo == tko:
         raise ValueError("q, k and their outputs differ in tokens")
-    qp, qs = _rows(q, h, d, dt, "q")
-    kp, ks = _rows(k, hk, d, dt, "k")
-    qo, qos = _rows(q_out, h, d, dt, "q_out")
-    ko, kos = _rows(k_out, hk, d, dt, "k_out")
-    rc = _rope_c(rope, cos_sin, positions, t)
     _lib.check(_lib.load().gdn_attn_qk_norm_rope(
-        ctypes.byref(shape._c), ctypes.byref(rc), t, qp, kp, qs, ks, _weight(w_q, d, "w_q"), _weight(w_k, d, "w_k"),
-        _ptr(cos_sin), _ptr(positions), qo, ko, qos, kos, _stream(stream)))
+        shape._ref, _rope_c(rope, cos_sin, positions, t), t, qp, kp, qs, ks, _weight(w_q, d, "w_q"),
+        _weight(w_k, d, "w_k"), _ptr(cos_sin), _ptr(positions), qo, ko, qos, kos, _stream(stream)))
 
 
 def gdn_attn_qk_norm_rope_bwd(shape: AttnShape, rope: AttnRope, q, k, w_q, w_k, cos_sin, positions, d_q_out, d_k_out,
                               dq, dk, dw_q, dw_k, workspace, stream=None) -> None:
     """Gradients of gdn_attn_qk_norm_rope: dq, dk in the input type, dw_q, dw_k in fp32."""
     h, hk, d, dt = shape.num_heads, shape.kv_heads, shape.head_dim, shape.dtype
-    t = q.shape[0]
-    if any(x.shape[0] != t for x in (k, d_q_out, d_k_out, dq, dk)):
+    t, qp, qs = _rows(q, h, d, dt, "q")
+    tk, kp, ks = _rows(k, hk, d, dt, "k")
+    tgq, gq, gqs = _rows(d_q_out, h, d, dt, "d_q_out")
+    tgk, gk, gks = _rows(d_k_out, hk, d, dt, "d_k_out")
+    toq, oq, oqs = _rows(dq, h, d, dt, "dq")
+    tok, ok, oks = _rows(dk, hk, d, dt, "dk")
+    if not t == tk == tgq == tgk == toq == tok:
         raise ValueError("q, k and their gradients differ in tokens")
-    qp, qs = _rows(q, h, d, dt, "q")
-    kp, ks = _rows(k, hk, d, dt, "k")
-    gq, gqs = _rows(d_q_out, h, d, dt, "d_q_out")
-    gk, gks = _rows(d_k_out, hk, d, dt, "d_k_out")
-    oq, oqs = _rows(dq, h, d, dt, "dq")
-    ok, oks = _rows(dk, hk, d, dt, "dk")
-    rc = _rope_c(rope, cos_sin, positions, t)
     _lib.check(_lib.load().gdn_attn_qk_norm_rope_bwd(
-        ctypes.byref(shape._c), ctypes.byref(rc), t, qp, kp, qs, ks, _weight(w_q, d, "w_q"), _weight(w_k, d, "w_k"),
+        shape._ref, _rope_c(rope, cos_sin, positions, t), t, qp, kp, qs, ks, _weight(w_q, d, "w_q"), _weight(w_k, d, "w_k"),
         _ptr(cos_sin), _ptr(positions), gq, gk, gqs, gks, oq, ok, oqs, oks, _weight(dw_q, d, "dw_q"),
         _weight(dw_k, d, "dw_k"), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
@@ -252,11 +257,10 @@ def gdn_attn_qk_norm_rope_bwd(shape: AttnShape, rope: AttnRope, q, k, w_q, w_k, 
 def _attention_args(shape: AttnShape, q, k, v, cache: AttnCache, o, scale):
     h, hk, d, dt = shape.num_heads, shape.kv_heads, shape.head_dim, shape.dtype
     cache.check(shape)
-    qp, qs = _rows(q, h, d, dt, "q")
-    kp, ks = _rows(k, hk, d, dt, "k")
-    vp, vs = _rows(v, hk, d, dt, "v")
-    t = q.shape[0]
-    if k.shape[0] != t or v.shape[0] != t or tuple(o.shape) != (t, h, d) or o.dtype != dt:
+    t, qp, qs = _rows(q, h, d, dt, "q")
+    tk, kp, ks = _rows(k, hk, d, dt, "k")
+    tv, vp, vs = _rows(v, hk, d, dt, "v")
+    if tk != t or tv != t or tuple(o.shape) != (t, h, d) or o.dtype != dt:
         raise ValueError("q, k, v and o differ in tokens, shape or type")
     return (qp, kp, vp, qs, ks, vs), d ** -0.5 if scale is None else scale
 
@@ -271,8 +275,8 @@ def gdn_attn_prefill(shape: AttnShape, q, k, v, cu_seqlens, plan: AttnPlan, cach
     if cu_seqlens.dtype != torch.int32 or plan.ctx_len.numel() != n:
         raise ValueError("cu_seqlens: int32 of one more than the plan's sequences expected")
     _lib.check(_lib.load().gdn_attn_prefill(
-        ctypes.byref(shape._c), n, q.shape[0], max_new, *args, _ptr(cu_seqlens), ctypes.byref(plan._c),
-        ctypes.byref(cache._c), scale, _ptr(o), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        shape._ref, n, q.shape[0], max_new, *args, _ptr(cu_seqlens), plan._ref,
+        cache._ref, scale, _ptr(o), _ptr(workspace), workspace.numel() * workspace.element_size(),
         _stream(stream)))
 
 
@@ -284,7 +288,7 @@ def gdn_attn_decode_step(shape: AttnShape, q, k, v, plan: AttnPlan, cache: AttnC
     if plan.ctx_len.numel() != n:
         raise ValueError("one token for each of the plan's sequences expected")
     _lib.check(_lib.load().gdn_attn_decode_step(
-        ctypes.byref(shape._c), n, *args, ctypes.byref(plan._c), ctypes.byref(cache._c), scale, _ptr(o),
+        shape._ref, n, *args, plan._ref, cache._ref, scale, _ptr(o),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
@@ -304,6 +308,6 @@ def gdn_attn_cache_read(shape: AttnShape, cu_seqlens, total_tokens: int, plan: A
     if cu_seqlens.dtype != torch.int32:
         raise ValueError("cu_seqlens: int32 expected")
     _lib.check(_lib.load().gdn_attn_cache_read(
-        ctypes.byref(shape._c), cu_seqlens.numel() - 1, total_tokens, _ptr(cu_seqlens), ctypes.byref(plan._c),
-        ctypes.byref(cache._c), _ptr(k_out), _ptr(v_out), _stream(stream)))
+        shape._ref, cu_seqlens.numel() - 1, total_tokens, _ptr(cu_seqlens), plan._ref,
+        cache._ref, _ptr(k_out), _ptr(v_out), _stream(stream)))
     return k_out, v_out

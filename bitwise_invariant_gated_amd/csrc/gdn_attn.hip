@@ -189,6 +189,7 @@ namespace {
 
 // work-groups of the gradient's row pass, each with a partial dw: enough to
 // fill the card (4 on each of 256 CUs), few enough that adding them up is short
+// (20,000 tokens of 20 heads, d = 128: 68 us; with half as many 93, twice 78)
 constexpr int kNormBwdGroups = 1024;
 
 int norm_bwd_groups(const gdn_attn_shape& s, int64_t T) {
@@ -245,7 +246,8 @@ void launch_norm(NormRopeArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((k_attn_norm_rope<E, D, U>), dim3(a.groups[0] + a.groups[1]), dim3(kNormThreads), 0, st, a);
 }
 
-// Four rows per lane group once that still leaves 8 work-groups per CU.
+// Four rows per lane group once that still leaves 8 work-groups per CU (20
+// heads, d = 128: 20,000 tokens 41.3 us with four, 43.5 with one; 6,400 tokens 15.9 and 15.2).
 template <class E, int D>
 void run_norm(NormRopeArgs& a, hipStream_t st) {
   const int64_t per = kNormThreads / (D / 8);

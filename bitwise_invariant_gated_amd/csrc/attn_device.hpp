@@ -22,6 +22,23 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, p);
 }
 
+// STREAM: not to be kept in the caches
+template <bool STREAM, class V>
+__device__ __forceinline__ void store(V* p, V x) {
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(x, p);
+  else
+    *p = x;
+}
+
+template <bool STREAM, class V>
+__device__ __forceinline__ V load(const V* p) {
+  if constexpr (STREAM)
+    return __builtin_nontemporal_load(p);
+  else
+    return *p;
+}
+
 // four consecutive elements of the input type as floats, and back
 struct ElemBf16 {
   typedef uint16_t T;
@@ -30,15 +47,17 @@ struct ElemBf16 {
     return f32x4{__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u), __uint_as_float(r[1] << 16),
                  __uint_as_float(r[1] & 0xffff0000u)};
   }
+  template <bool STREAM>
   static __device__ __forceinline__ void store4(T* p, f32x4 x) {
-    *(u32x2*)p = u32x2{pack2(x[0], x[1]), pack2(x[2], x[3])};
+    store<STREAM>((u32x2*)p, u32x2{pack2(x[0], x[1]), pack2(x[2], x[3])});
   }
 };
 
 struct ElemF32 {
   typedef float T;
   static __device__ __forceinline__ f32x4 load4(const T* p) { return *(const f32x4*)p; }
-  static __device__ __forceinline__ void store4(T* p, f32x4 x) { *(f32x4*)p = x; }
+  template <bool STREAM>
+  static __device__ __forceinline__ void store4(T* p, f32x4 x) { store<STREAM>((f32x4*)p, x); }
 };
 
 template <int CTRL>

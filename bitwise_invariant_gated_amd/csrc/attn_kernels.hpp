@@ -803,13 +803,13 @@ __device__ __forceinline__ int run_of(int total, int W, int x) {
 
 // Work-groups of k_attn_rows that share a CU.  With one its waves have all
 // registers, and what hides the memory's latency are the loads that a wave has in
-// flight (decode, 256 x 4,096 at d = 128: 175 us; with two, whose loop spilled, 198;
+// flight (decode, 256 x 4,096 at d = 128: 176 us; with two, whose loop spilled, 198;
 // 16 x 16 new tokens at d = 256: 114 us; two 143); fewer runs also leave fewer records.
 // Several new tokens at d = 64 and 128 keep the MFMAs busier with two (16 x 37 tokens at d = 64:
 // 118 us; one 144, three 131).
 //
-// Bound by memory in decode: 256 x 4,096, 823 MB, 168 us, 4.9 TB/s, where a
-// copy moves 4.65 and a kernel that only reads 6.1; 3 x 100,003, 307 MB, 62 us.
+// Bound by memory in decode: 256 x 4,096, 823 MB, 154 us, 5.3 TB/s, where a
+// copy moves 4.65 and a kernel that only reads 6.1; 3 x 100,003, 307 MB, 58 us.
 template <int D, bool MULTI>
 constexpr int kRowsPerCu = MULTI && D < 256 ? 2 : 1;
 
@@ -831,7 +831,11 @@ constexpr int kRowsPerCu = MULTI && D < 256 ? 2 : 1;
 // MULTI: any number of new tokens, which k_attn_append has put into the tail
 // (last block) or raw_k, raw_v (blocks that they filled).  Otherwise one each,
 // which this kernel appends itself.
-template <int D, int RT, bool MULTI>
+//
+// STREAM: no other chunk reads the keys, and the caches need not keep them (decode,
+// 256 x 4,096 at d = 128: 160 us instead of 176; 64 x 4 new tokens after 3,000: 96 instead of 111; but 5
+// chunks a sequence, 16 x 37 tokens after 3,000: 150 instead of 129).
+template <int D, int RT, bool MULTI, bool STREAM>
 __global__ __launch_bounds__(256, (kRowsPerCu<D, MULTI>)) void k_attn_rows(const RowsArgs ra) {
   const StepArgs& a = ra.s;
   constexpr int KS = D / 32, KP = D / 64, DT = D / 64, R = 16 * RT;  // DT: dim tiles of a wave
@@ -1008,7 +1012,7 @@ __global__ __launch_bounds__(256, (kRowsPerCu<D, MULTI>)) void k_attn_rows(const
 #pragma unroll
       for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
-        for (int x = 0; x < KP; ++x) kb[sub][x] = *(const u32x4*)(kp_ + x * 4096 + key_of(sub, r) * 64);
+        for (int x = 0; x < KP; ++x) kb[sub][x] = load<STREAM>((const u32x4*)(kp_ + x * 4096 + key_of(sub, r) * 64));
     };
     auto fetch_v = [&](int b0) __attribute__((always_inline)) {  // of all four, this wave's dims
 #pragma unroll
@@ -1016,7 +1020,7 @@ __global__ __launch_bounds__(256, (kRowsPerCu<D, MULTI>)) void k_attn_rows(const
         const int64_t at = (int64_t)__builtin_amdgcn_readlane(run.id, min(b0 + t, b_end - 1) & 63) * a.Hk + hk;
         const uint8_t* vp = a.cache.v8 + at * (64 * D) + (wave * DT * 16 + r) * 64 + g * 16;
 #pragma unroll
-        for (int x = 0; x < DT; ++x) vb[t][x] = *(const u32x4*)(vp + x * 1024);
+        for (int x = 0; x < DT; ++x) vb[t][x] = load<STREAM>((const u32x4*)(vp + x * 1024));
       }
     };
     // ---- an own block in the input type: this wave's 16 keys and its dims of V

@@ -13,8 +13,8 @@
 // crosses lanes; the runs are 8 bytes (bf16) and neighbouring lanes'
 // runs are contiguous.  Dims past rd, and adjacent pairs, take 8 dims in a row.
 //
-// Measured, 10,240 tokens, 32 heads in all, d = 128, bf16: 34.5 us, 173 MB, 5.0 TB/s; the gradient
-// 47 + 4.5 us, 257 MB, 5.0 TB/s (a copy moves 4.65).
+// Measured with inputs that no cache holds, 10,240 tokens, 32 heads in all, d = 128, bf16: 37 us,
+// 173 MB, 4.7 TB/s; the gradient 59 us in two launches, 257 MB, 4.3 TB/s (a copy moves 4.65).
 #pragma once
 
 #include "attn_device.hpp"
@@ -104,7 +104,7 @@ __device__ __forceinline__ float dot8(f32x4 a, f32x4 b, f32x4 c, f32x4 d) {
 }
 
 // U rows per lane group: their loads are all issued before the first is used.
-template <class E, int D, int U>
+template <class E, int D, int U, bool STREAM>
 __global__ __launch_bounds__(kNormThreads) void k_attn_norm_rope(const NormRopeArgs a) {
   typedef typename E::T T;
   constexpr int L = D / 8, R = kNormThreads / L;
@@ -138,15 +138,15 @@ __global__ __launch_bounds__(kNormThreads) void k_attn_norm_rope(const NormRopeA
     x1[u] = x1[u] * r * w1;
     x2[u] = x2[u] * r * w2;
     rotate(p, x1[u], x2[u], c[u], s[u], false);
-    E::store4(out + at[u] + p.o1, x1[u]);
-    E::store4(out + at[u] + p.o2, x2[u]);
+    E::template store4<STREAM>(out + at[u] + p.o1, x1[u]);
+    E::template store4<STREAM>(out + at[u] + p.o2, x2[u]);
   }
 }
 
 // Gradient.  Work-groups go over the rows of q, then over those of k, in
 // steps of the grid; a lane keeps dw of its eight dims in registers for all
 // of its rows, so dw costs one partial sum of 2 d floats per work-group.
-template <class E, int D>
+template <class E, int D, bool STREAM>
 __global__ __launch_bounds__(kNormThreads) void k_attn_norm_rope_bwd(const NormRopeArgs a) {
   typedef typename E::T T;
   constexpr int L = D / 8, R = kNormThreads / L;
@@ -172,8 +172,8 @@ __global__ __launch_bounds__(kNormThreads) void k_attn_norm_rope_bwd(const NormR
       const float r = 1.f / __builtin_sqrtf(ss * (1.f / D) + a.eps);
       const float m = hx * r * r * (1.f / D);
       T* o = (T*)a.out[which] + token * a.out_stride[which] + head * D;
-      E::store4(o + p.o1, r * (h1 - x1 * m));
-      E::store4(o + p.o2, r * (h2 - x2 * m));
+      E::template store4<STREAM>(o + p.o1, r * (h1 - x1 * m));
+      E::template store4<STREAM>(o + p.o2, r * (h2 - x2 * m));
       g1 += y1 * (x1 * r);
       g2 += y2 * (x2 * r);
     }

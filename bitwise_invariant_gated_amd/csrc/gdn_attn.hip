@@ -239,11 +239,20 @@ gdn_status check_norm(const char* fn, const gdn_attn_shape* shape, const gdn_att
   return GDN_OK;
 }
 
-template <class E, int D, int U>
+// Outputs that the caches could not hold for long are stored past them: from
+// 64 MB on (d = 128, forward and gradient in us, past / into the caches: 33 MB 16.4 / 15.3 and
+// 26.6 / 25.4; 84 MB 37 / 43 and 59 / 61; 102 MB 40.6 / 41.5 and 61 / 68).  What reads them next is no
+// slower for it (with the prefill of 5 x 2,048 behind it 207 us either way, of 4 x 1,700 with 28 MB 104 / 106).
+template <class E, int D>
+bool streams(const NormRopeArgs& a) {
+  return (a.rows[0] + a.rows[1]) * (int64_t)(D * sizeof(typename E::T)) >= (int64_t(64) << 20);
+}
+
+template <class E, int D, int U, bool STREAM>
 void launch_norm(NormRopeArgs& a, hipStream_t st) {
   const int64_t per = (int64_t)(kNormThreads / (D / 8)) * U;
   for (int i = 0; i < 2; ++i) a.groups[i] = (int)((a.rows[i] + per - 1) / per);
-  hipLaunchKernelGGL((k_attn_norm_rope<E, D, U>), dim3(a.groups[0] + a.groups[1]), dim3(kNormThreads), 0, st, a);
+  hipLaunchKernelGGL((k_attn_norm_rope<E, D, U, STREAM>), dim3(a.groups[0] + a.groups[1]), dim3(kNormThreads), 0, st, a);
 }
 
 // Four rows per lane group once that still leaves 8 work-groups per CU (20
@@ -251,15 +260,20 @@ void launch_norm(NormRopeArgs& a, hipStream_t st) {
 template <class E, int D>
 void run_norm(NormRopeArgs& a, hipStream_t st) {
   const int64_t per = kNormThreads / (D / 8);
-  if (a.rows[0] + a.rows[1] >= per * 4 * 2048)
-    launch_norm<E, D, 4>(a, st);
+  if (streams<E, D>(a))
+    launch_norm<E, D, 4, true>(a, st);
+  else if (a.rows[0] + a.rows[1] >= per * 4 * 2048)
+    launch_norm<E, D, 4, false>(a, st);
   else
-    launch_norm<E, D, 1>(a, st);
+    launch_norm<E, D, 1, false>(a, st);
 }
 
 template <class E, int D>
 void run_norm_bwd(const NormRopeArgs& a, int groups, float* dw_q, float* dw_k, hipStream_t st) {
-  hipLaunchKernelGGL((k_attn_norm_rope_bwd<E, D>), dim3(groups), dim3(kNormThreads), 0, st, a);
+  if (streams<E, D>(a))
+    hipLaunchKernelGGL((k_attn_norm_rope_bwd<E, D, true>), dim3(groups), dim3(kNormThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_attn_norm_rope_bwd<E, D, false>), dim3(groups), dim3(kNormThreads), 0, st, a);
   hipLaunchKernelGGL(k_attn_norm_rope_dw, dim3(2 * D / 32), dim3(1024), 0, st, a.partial, groups, D, dw_q, dw_k);
 }
 
@@ -532,12 +546,17 @@ void place_records(RowsArgs& a, const RowsLayout& L, char* ws, const gdn_attn_sh
   a.rec_o = a.rec_ml + align_up((size_t)a.max_parts * a.s.Hk * rows * 2 * sizeof(float)) / sizeof(float);
 }
 
-template <int D, int RT, bool MULTI>
+template <int D, int RT, bool MULTI, bool STREAM>
 gdn_status run_rows(const RowsArgs& a, int chunks, hipStream_t st, const char* fn) {
   const int W = std::max(1, std::min(256 * kRowsPerCu<D, MULTI> / a.s.Hk, a.max_parts));  // 256 CUs
-  hipLaunchKernelGGL((k_attn_rows<D, RT, MULTI>), dim3(W, a.s.Hk), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((k_attn_rows<D, RT, MULTI, STREAM>), dim3(W, a.s.Hk), dim3(256), 0, st, a);
   hipLaunchKernelGGL(k_attn_join<D>, dim3(a.s.N, a.s.Hk, (chunks * a.rec_rows + 3) / 4), dim3(256), 0, st, a, W);
   return launch_status(fn);
+}
+
+template <int D>
+gdn_status run_decode(const RowsArgs& a, int chunks, hipStream_t st, const char* fn) {
+  return chunks == 1 ? run_rows<D, 1, false, true>(a, chunks, st, fn) : run_rows<D, 1, false, false>(a, chunks, st, fn);
 }
 
 template <int D>
@@ -551,11 +570,12 @@ gdn_status run_prefill(const StepArgs& a, int64_t tiles, hipStream_t st, const c
 template <int D>
 gdn_status run_few(const RowsArgs& a, int chunks, hipStream_t st, const char* fn) {
   hipLaunchKernelGGL((k_attn_append<D, true>), dim3((unsigned)touched_blocks(a.s.N, a.s.T), a.s.Hk), dim3(kAppendThreads<D>), 0, st, a.s);
-  if (a.chunk_rows == 16) return run_rows<D, 1, true>(a, chunks, st, fn);
-  if constexpr (D < 256) {
-    if (a.chunk_rows == 32) return run_rows<D, 2, true>(a, chunks, st, fn);
+  if constexpr (D == 256) {
+    return chunks == 1 ? run_rows<D, 1, true, true>(a, chunks, st, fn) : run_rows<D, 1, true, false>(a, chunks, st, fn);
+  } else {
+    if (a.chunk_rows == 16) return run_rows<D, 1, true, true>(a, chunks, st, fn);  // one chunk, or it would be 32
+    return chunks == 1 ? run_rows<D, 2, true, true>(a, chunks, st, fn) : run_rows<D, 2, true, false>(a, chunks, st, fn);
   }
-  return fail(GDN_ERR_UNSUPPORTED, "%s: rows", fn);
 }
 
 }  // namespace
@@ -615,9 +635,9 @@ extern "C" gdn_status gdn_attn_decode_step(const gdn_attn_shape* shape, int32_t 
   place_records(a, L, (char*)workspace, *shape, 16, decode_rows(*shape));
   const int chunks = (a.s.G + 15) / 16;
   switch (shape->head_dim) {
-    case 64: return run_rows<64, 1, false>(a, chunks, (hipStream_t)stream, fn);
-    case 128: return run_rows<128, 1, false>(a, chunks, (hipStream_t)stream, fn);
-    default: return run_rows<256, 1, false>(a, chunks, (hipStream_t)stream, fn);
+    case 64: return run_decode<64>(a, chunks, (hipStream_t)stream, fn);
+    case 128: return run_decode<128>(a, chunks, (hipStream_t)stream, fn);
+    default: return run_decode<256>(a, chunks, (hipStream_t)stream, fn);
   }
 }
 

@@ -1368,20 +1368,26 @@ __global__ __launch_bounds__(256) void k_attn_join(const RowsArgs ra, int W) {
       fold_weights(before, mp, wa, wb);
       m = fmaxf(m, __shfl(up, 63));
     }
+    auto folds = [&](auto all_) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < S; ++u) {
-      const bool there = j0 + u0 + u < k;
-      const float ya = lane_of(wa, u0 + u), yb = lane_of(wb, u0 + u);
-      l = there ? __builtin_fmaf(lp[u], yb, l * ya) : l;
+      for (int u = 0; u < S; ++u) {
+        const bool there = decltype(all_)::value || j0 + u0 + u < k;
+        const float ya = lane_of(wa, u0 + u), yb = lane_of(wb, u0 + u);
+        l = there ? __builtin_fmaf(lp[u], yb, l * ya) : l;
 #pragma unroll
-      for (int e = 0; e < V; ++e) O[e] = there ? __builtin_fmaf(Op[u][e], yb, O[e] * ya) : O[e];
-    }
+        for (int e = 0; e < V; ++e) O[e] = there ? __builtin_fmaf(Op[u][e], yb, O[e] * ya) : O[e];
+      }
+    };
+    if (j0 + u0 + S <= k)
+      folds(std::true_type{});
+    else
+      folds(std::false_type{});
   };
   for (int j0 = 0; j0 < k; j0 += 64) {
     const float mp = j0 + lane < k ? pm[(j0 + lane) * sm] : kNegInf;
     float wa = 0.f, wb = 0.f;
     if (k - j0 > 16) {
-      constexpr int S = V == 4 ? 32 : 64;
+      constexpr int S = 32;  // with 64 more of the last batch is in vain (3 x 100,003: 81 us a call, with 32 76)
 #pragma unroll 1
       for (int u0 = 0; u0 < 64 && j0 + u0 < k; u0 += S) batch(std::integral_constant<int, S>{}, j0, u0, mp, wa, wb);
     } else {

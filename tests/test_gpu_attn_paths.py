@@ -173,3 +173,30 @@ def test_one_and_no_tokens():
     k, v = L.read()
     for i in range(3):
         assert same_bits(k[i], seqs[i][1].to(DEV)) and same_bits(v[i], seqs[i][2].to(DEV))
+
+
+@pytest.mark.parametrize("h,hk,n", [(4, 2, 2), (16, 8, 20)])  # keys split; rows split
+def test_prefill_in_a_graph(h, hk, n):
+    """Plan and prefill captured once; each replay appends the next tokens as the eager call does."""
+    d, new = 64, 70
+    note(f"attn prefill graph h={h} hk={hk} n={n}")
+    seqs = random_seqs(38, [4 * new] * n, h, hk, d)
+    E = Layer(h, hk, d, seqs)
+    eager = [E.prefill([new] * n, max_new=new) for _ in range(4)]
+    L = Layer(h, hk, d, seqs)
+    (q, k, v), cu = L.pack([new] * n)
+    plan = gdn.alloc_attn_plan(L.pool, n, n * new, L.slot_index)
+    ws = gdn.alloc_attn_workspace(L.shape, gdn.GDN_ATTN_OP_PREFILL, n * new, n, L.cache.k8.shape[0], DEV)
+    o = torch.empty_like(q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        gdn.gdn_attn_plan(L.pool, cu, plan)
+        gdn.gdn_attn_prefill(L.shape, q, k, v, cu, plan, L.cache, o, ws, max_new=new)
+    for step in range(4):
+        for to, x in zip((q, k, v), L.pack([new] * n)[0]):
+            to.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        L.done = [x + new for x in L.done]
+        assert same_bits(o, torch.cat(eager[step])), step

@@ -86,7 +86,9 @@ def check_dpp_hazards(asm_text: str) -> list:
 
 # kernels on the bf16 hot paths (prefill, decode, continuation, fwd_bwd), by
 # mangled-name fragment; register spills there cost a scratch set-up per
-# launch and memory traffic per spill, so the build rejects them
+# launch and memory traffic per spill, so the build rejects them.  k_attn_prefill
+# and k_attn_rows of two row tiles are not among them: they fill the registers and
+# spill what their main loops do not touch
 HOT_KERNELS = ("k_scanIN3cpr4Bf16", "k_chain_scan_bf16", "k_decodeIN3cpr4Bf16", "k_resync_bf16",
                "k_cont_headIN3cpr4Bf16", "k_chunk_local_prefill_bf16", "k_chain_prefill_bf16", "k_bwd_local_bf16",
                "k_bwd_chain_bf16", "k_bwd_state_grads_bf16", "k_plan", "k_attn_join",

@@ -35,6 +35,23 @@ struct StepArgs {
   int tile_rows;
 };
 
+// Batch entry i: its packed tokens [c0, c0 + len), the tokens in its cache and its
+// cache row.  An entry without a request (context -1, or a row that the cache
+// does not have) has ctx = row = -1 in every kernel: o = 0, nothing is written.
+struct Entry {
+  int c0, len, ctx, row;
+};
+
+__device__ __forceinline__ Entry entry_of(const StepArgs& a, int i) {
+  Entry e;
+  e.c0 = a.cu ? a.cu[i] : i;
+  e.len = a.cu ? a.cu[i + 1] - e.c0 : 1;
+  e.ctx = a.ctx_len[i];
+  e.row = row_of(a.slot, i, a.cache.num_slots);
+  if (e.ctx < 0 || e.row < 0) e.ctx = e.row = -1;
+  return e;
+}
+
 // the pool block of a row's block b, held to the pool
 __device__ __forceinline__ int pool_block(const StepArgs& a, int row, int b) {
   const int id = a.table[(size_t)row * a.max_blocks + min(b, a.max_blocks - 1)];
@@ -256,13 +273,12 @@ __global__ __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4) void k_attn_ap
     return;
   }
   const int i = seq_of_item(a.cu, a.N, at_block);
-  const int ctx = a.ctx_len[i], c0 = a.cu[i], len = a.cu[i + 1] - c0;
+  const Entry e_ = entry_of(a, i);
+  const int c0 = e_.c0, len = e_.len, ctx = e_.ctx, row = e_.row;
   if (ctx < 0 || len <= 0) return;
   const int first = ctx >> 6, last = (ctx + len - 1) >> 6;
   const int b = first + at_block - ((c0 >> 6) + 2 * i);
   if (b > last) return;
-  const int row = row_of(a.slot, i, a.cache.num_slots);
-  if (row < 0) return;
   uint16_t* tk = a.cache.tail_k + ((int64_t)row * a.Hk + hk) * (64 * D);
   uint16_t* tv = a.cache.tail_v + ((int64_t)row * a.Hk + hk) * (64 * D);
   const uint16_t* nk = a.k + (int64_t)hk * D;

@@ -722,11 +722,11 @@ __global__ __launch_bounds__(PrefillTile<D>::kThreads) void k_attn_prefill(const
   const i32x2 item = a.order[blockIdx.x / a.Hk];
   const int i = item[0];
   if (i < 0) return;
-  const int c0 = a.cu[i], len = a.cu[i + 1] - c0;
+  const Entry e_ = entry_of(a, i);
+  const int c0 = e_.c0, len = e_.len, ctx = e_.ctx, cache_row = e_.row;
   const int64_t row0 = (int64_t)item[1] * P::kRows;
   const int64_t rows = (int64_t)len * a.G;
-  const int ctx = a.ctx_len[i], cache_row = row_of(a.slot, i, a.cache.num_slots);
-  if (ctx < 0 || cache_row < 0) {  // refused: o = 0
+  if (ctx < 0) {  // no request: o = 0
     const int n = (int)min(rows - row0, (int64_t)P::kRows);
     for (int x = threadIdx.x; x < n * (D / 8); x += P::kThreads) {
       const uint32_t row = (uint32_t)row0 + x / (D / 8);
@@ -783,7 +783,8 @@ constexpr int kChunkCost = 2;
 
 // units of all chunks of sequence i
 __device__ __forceinline__ int all_units_of(const RowsArgs& a, int i) {
-  const int ctx = a.s.ctx_len[i], len = len_of(a, i);
+  const Entry e_ = entry_of(a.s, i);
+  const int ctx = e_.ctx, len = e_.len;
   if (ctx < 0 || len <= 0) return 0;
   const int n = chunks_of(a, len);
   if ((ctx >> 9) == (ctx + len - 1) >> 9) return n * ((ctx >> 9) + 1 + kChunkCost);
@@ -884,7 +885,8 @@ __global__ __launch_bounds__(256, (kRowsPerCu<D, MULTI>)) void k_attn_rows(const
   if (MULTI && whole) skip(blockIdx.x);
 
   for (int f = g0; whole ? i < a.N : f < g1;) {
-    const int ctx = a.ctx_len[i], len = MULTI ? len_of(ra, i) : 1;
+    const Entry e_ = entry_of(a, i);
+    const int c0 = MULTI ? e_.c0 : i, len = MULTI ? e_.len : 1, ctx = e_.ctx, cache_row = e_.row;
     const int np = ctx < 0 || len <= 0 ? 0 : parts_of(ra, ctx, len, c);
     if (c == 0 && np > 0 && !whole && hk == 0 && tid == 0 && f == base) ra.base[i] = base;
     if (np == 0 || (!whole && f >= base + np)) {  // nothing there, or behind it
@@ -900,11 +902,10 @@ __global__ __launch_bounds__(256, (kRowsPerCu<D, MULTI>)) void k_attn_rows(const
       }
       continue;
     }
-    const int c0 = MULTI ? a.cu[i] : i, end = ctx + len;
+    const int end = ctx + len;
     const uint32_t rows = (uint32_t)len * (uint32_t)a.G, row0 = (uint32_t)c * R;
     const uint32_t last_row = min(row0 + R, rows) - 1;
     const int p_lo = whole ? 0 : f - base, p_hi = whole ? np : min(np, g1 - base);
-    const int cache_row = max(row_of(a.slot, i, a.cache.num_slots), 0);
     // own blocks of the chunk's rows (there are two at most)
     const int b_lo = (ctx + (int)(row0 / (uint32_t)a.G)) >> 6, b_hi = (ctx + (int)(last_row / (uint32_t)a.G)) >> 6;
     const int b_end = min(p_hi * kPartBlocks, b_hi);  // the 8-bit blocks end here
@@ -1300,7 +1301,7 @@ __global__ __launch_bounds__(256, (kRowsPerCu<D, MULTI>)) void k_attn_rows(const
 }
 
 // Joins what several work-groups did of a chunk, left to right; chunks that
-// one work-group did alone are finished, refused requests' rows get o = 0.
+// one work-group did alone are finished, rows of entries without a request get o = 0.
 // A wave takes a row, a lane D / 64 of its dims.  The fold is a chain over the
 // records, but what it needs of each is not: the weights of 64 folds come
 // from prefix maxima (exact in any order), a lane each, and many records are
@@ -1313,12 +1314,13 @@ __global__ __launch_bounds__(256) void k_attn_join(const RowsArgs ra, int W) {
   typedef float fv __attribute__((ext_vector_type(V)));
   const StepArgs& a = ra.s;
   const int i = blockIdx.x, hk = blockIdx.y, lane = threadIdx.x & 63;
-  const int ctx = a.ctx_len[i], len = len_of(ra, i);
+  const Entry e_ = entry_of(a, i);
+  const int c0 = e_.c0, len = e_.len, ctx = e_.ctx;
   const int x_ = __builtin_amdgcn_readfirstlane(blockIdx.z * 4 + (threadIdx.x >> 6));
   const int c = x_ / ra.rec_rows, rr = x_ % ra.rec_rows;
   const uint32_t row = (uint32_t)c * ra.chunk_rows + rr, G = (uint32_t)a.G;
   if (len <= 0 || row >= (uint32_t)len * G) return;
-  uint16_t* o = a.o + ((int64_t)((a.cu ? a.cu[i] : i) + (int)(row / G)) * a.H + hk * a.G + (int)(row % G)) * D + lane * V;
+  uint16_t* o = a.o + ((int64_t)(c0 + (int)(row / G)) * a.H + hk * a.G + (int)(row % G)) * D + lane * V;
   if (ctx < 0) {
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = 0;

@@ -218,8 +218,9 @@ gdn_status gdn_attn_qk_norm_rope_bwd(const gdn_attn_shape* shape, const gdn_attn
  * (causal), appending them: o = softmax(scale q k^T) v by the cache's rule.
  *   q [T, H, d], k, v [T, Hk, d]  with token strides; o [T, H, d] contiguous
  *   step      the plan's; every request's blocks up to its last token are in
- *             its table.  Tokens of a request with ctx_len -1 get o = 0 and
- *             leave the cache alone.
+ *             its table.  Tokens of an entry with ctx_len -1, or with a
+ *             slot_index that is no row of the cache (whatever its ctx_len),
+ *             get o = 0 and leave the cache alone.
  *   max_new   an upper bound of any sequence's new tokens (0: T); it chooses
  *             between kernels and changes no bits
  *   scale     positive and finite

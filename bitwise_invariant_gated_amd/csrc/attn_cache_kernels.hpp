@@ -42,10 +42,13 @@ struct Entry {
   int c0, len, ctx, row;
 };
 
+// cu[i], held to the call's tokens
+__device__ __forceinline__ int cu_at(const StepArgs& a, int i) { return min(max(a.cu[i], 0), a.T); }
+
 __device__ __forceinline__ Entry entry_of(const StepArgs& a, int i) {
   Entry e;
-  e.c0 = a.cu ? a.cu[i] : i;
-  e.len = a.cu ? a.cu[i + 1] - e.c0 : 1;
+  e.c0 = a.cu ? cu_at(a, i) : i;
+  e.len = a.cu ? max(cu_at(a, i + 1) - e.c0, 0) : 1;
   e.ctx = a.ctx_len[i];
   e.row = row_of(a.slot, i, a.cache.num_slots);
   if (e.ctx < 0 || e.row < 0) e.ctx = e.row = -1;
@@ -154,12 +157,12 @@ __device__ __forceinline__ void quantise_block(const CacheArgs& c, int64_t at, F
 }
 
 // The i with slots(i) <= x < slots(i + 1), slots(i) = cu[i] / 64 + per * i: room for every block that
-// sequence i's tokens can touch, found without a prefix sum over the batch.
-__device__ __forceinline__ int seq_of_item(const int32_t* cu, int N, int x) {
-  int lo = 0, hi = N - 1;
+// sequence i's tokens can touch, found without a prefix sum over the batch.  0 if x lies before slots(0).
+__device__ __forceinline__ int seq_of_item(const StepArgs& a, int x) {
+  int lo = 0, hi = a.N - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if ((cu[mid] >> 6) + 2 * mid <= x)
+    if ((cu_at(a, mid) >> 6) + 2 * mid <= x)
       lo = mid;
     else
       hi = mid - 1;
@@ -192,7 +195,10 @@ __device__ void order_tiles(const StepArgs& a, int* hist /* [kClasses] */, int* 
   if (tid == 0) *most = 0;
   __syncthreads();
   int m = 0;
-  for (int i = tid; i < a.N; i += TH) m = max(m, (a.ctx_len[i] + a.cu[i + 1] - a.cu[i]) >> 6);
+  for (int i = tid; i < a.N; i += TH) {
+    const Entry e = entry_of(a, i);
+    m = max(m, (e.ctx + e.len) >> 6);
+  }
   atomicMax(most, m);
   __syncthreads();
   const int shift = max(0, 32 - __builtin_clz(*most + 1) - 9);  // (most + 1) >> shift < kClasses
@@ -200,16 +206,17 @@ __device__ void order_tiles(const StepArgs& a, int* hist /* [kClasses] */, int* 
     int lo = 0, hi = a.N - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((int)((int64_t)a.cu[mid] * a.G / a.tile_rows) + mid <= x)
+      if ((int)((int64_t)cu_at(a, mid) * a.G / a.tile_rows) + mid <= x)
         lo = mid;
       else
         hi = mid - 1;
     }
-    const int c0 = a.cu[lo], tile = x - ((int)((int64_t)c0 * a.G / a.tile_rows) + lo);
-    const int64_t rows = (int64_t)(a.cu[lo + 1] - c0) * a.G, row0 = (int64_t)tile * a.tile_rows;
-    const bool none = row0 >= rows;
+    const Entry e = entry_of(a, lo);
+    const int tile = x - ((int)((int64_t)e.c0 * a.G / a.tile_rows) + lo);
+    const int64_t rows = (int64_t)e.len * a.G, row0 = (int64_t)tile * a.tile_rows;
+    const bool none = tile < 0 || row0 >= rows;
     to = none ? i32x2{-1, 0} : i32x2{lo, tile};
-    const int keys = a.ctx_len[lo] + (int)((min(row0 + a.tile_rows, rows) - 1) / a.G);  // -1 in a refused sequence at least
+    const int keys = e.ctx + (int)((min(row0 + a.tile_rows, rows) - 1) / a.G);  // -1 in a refused sequence at least
     return kClasses - 1 - (none ? 0 : min(((max(keys, 0) >> 6) + 1) >> shift, kClasses - 1));
   };
   i32x2 it;
@@ -272,13 +279,13 @@ __global__ __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4) void k_attn_ap
     if (hk == 0) order_tiles<TH>(a, (int*)vt, (int*)red);
     return;
   }
-  const int i = seq_of_item(a.cu, a.N, at_block);
+  const int i = seq_of_item(a, at_block);
   const Entry e_ = entry_of(a, i);
   const int c0 = e_.c0, len = e_.len, ctx = e_.ctx, row = e_.row;
   if (ctx < 0 || len <= 0) return;
   const int first = ctx >> 6, last = (ctx + len - 1) >> 6;
   const int b = first + at_block - ((c0 >> 6) + 2 * i);
-  if (b > last) return;
+  if (b < first || b > last) return;
   uint16_t* tk = a.cache.tail_k + ((int64_t)row * a.Hk + hk) * (64 * D);
   uint16_t* tv = a.cache.tail_v + ((int64_t)row * a.Hk + hk) * (64 * D);
   const uint16_t* nk = a.k + (int64_t)hk * D;
@@ -436,10 +443,10 @@ __global__ __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4) void k_attn_ap
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_cache_read(const StepArgs a, uint16_t* k_out, uint16_t* v_out) {
   const int hk = blockIdx.y;
-  const int i = seq_of_item(a.cu, a.N, blockIdx.x);
-  const int c0 = a.cu[i], len = a.cu[i + 1] - c0;
+  const int i = seq_of_item(a, blockIdx.x);
+  const int c0 = cu_at(a, i), len = cu_at(a, i + 1) - c0;
   const int b = (int)blockIdx.x - ((c0 >> 6) + 2 * i);
-  if (len <= 0 || b > ((len - 1) >> 6)) return;
+  if (len <= 0 || b < 0 || b > ((len - 1) >> 6)) return;
   const int row = row_of(a.slot, i, a.cache.num_slots);
   const bool full = (int64_t)(b + 1) * 64 <= len;
   const int64_t at = row < 0 ? 0 : (int64_t)(full ? pool_block(a, row, b) : row) * a.Hk + hk;

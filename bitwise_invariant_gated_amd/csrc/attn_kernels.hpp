@@ -773,7 +773,7 @@ __device__ __forceinline__ int parts_of(const RowsArgs& a, int ctx, int len, int
   return ((ctx + (int)(last / (uint32_t)a.s.G)) >> 9) + 1;
 }
 
-__device__ __forceinline__ int len_of(const RowsArgs& a, int i) { return a.s.cu ? a.s.cu[i + 1] - a.s.cu[i] : 1; }
+__device__ __forceinline__ int len_of(const RowsArgs& a, int i) { return entry_of(a.s, i).len; }
 
 // What a chunk costs, in units of a partition: its partitions, and its own
 // block, first loads and outputs, which take about as long as two (with one, 16 x 16

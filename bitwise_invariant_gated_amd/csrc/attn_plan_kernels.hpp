@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const PlanArgs a) {
     }
     if (a.tokens_here) {
       __syncthreads();
-      for (int t = s_cu[0] + tid; t < min(s_cu[n], a.T); t += kPlanThreads) {
+      for (int t = max(s_cu[0], 0) + tid; t < min(s_cu[n], a.T); t += kPlanThreads) {
         const int r = seq_of(s_cu, n, t);
         const bool on = s_ctx[r] >= 0;
         const int from = on ? s_ctx[r] : -1 - s_ctx[r];
@@ -145,10 +145,10 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const PlanArgs a) {
   }
 }
 
-// Tokens of a large plan: a thread each.
+// Tokens of a large plan: a thread each.  Those outside every request are left alone, as above.
 __global__ __launch_bounds__(256) void k_attn_plan_tokens(const PlanArgs a) {
   const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t >= a.T) return;
+  if (t >= a.T || t < a.cu[0] || t >= a.cu[a.N]) return;
   const int i = seq_of(a.cu, a.N, t);
   const int row = row_of(a.slot, i, a.num_slots);
   const int ctx = a.ctx_len[i];

@@ -43,8 +43,10 @@
  *     a multiple of 8 and at least heads * head_dim, so q, k and v may be read
  *     in place out of a projection that makes them in one row.
  *   - Device data (lengths, tables, positions) is the caller's to get right;
- *     the kernels keep their accesses inside the arrays where it is not
- *     (block ids are held to the pool, positions to the rotation table).
+ *     the kernels keep their accesses inside the arrays where it is not:
+ *     cu_seqlens are held to 0 .. T, block ids to the pool, positions to the
+ *     rotation table.  Tokens outside [cu_seqlens[0], cu_seqlens[N]) belong
+ *     to no sequence; nothing is read or written for them.
  */
 #ifndef GDN_ATTN_H
 #define GDN_ATTN_H

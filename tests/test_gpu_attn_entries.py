@@ -66,3 +66,103 @@ def test_no_cache_row_beside_a_context(h, hk, d, row, how, new):
         assert torch.equal(after[x][rest], full[x][rest])
     for x in (4, 5):
         assert torch.equal(after[x][0], before[x][0]) and torch.equal(after[x][1:], full[x][1:])
+
+
+def window(t, pad=128, fill=float("nan")):
+    """A copy of t inside a larger array whose rows before and behind it hold `fill`: (view, whole)."""
+    whole = torch.full((t.shape[0] + 2 * pad, *t.shape[1:]), fill, dtype=t.dtype, device=DEV)
+    whole[pad:-pad] = t
+    return whole[pad:-pad], whole
+
+
+def around(whole, pad=128):
+    return torch.cat([whole[:pad], whole[-pad:]])
+
+
+# how the batch's first and last limits are wrong: before the tokens, and past them
+@pytest.mark.parametrize("first,past", [(-5, 36), (-100, 100), (0, 1), (-1, 0)])
+@pytest.mark.parametrize("how", [50, 0])
+@pytest.mark.parametrize("h,hk,d", [(7, 7, 64), (16, 4, 128), (8, 2, 256)])
+def test_limits_outside_the_tokens(h, hk, d, how, first, past):
+    """cu_seqlens that begins before token 0 and ends behind token T: the call does what it
+    does for limits held to 0 and T, and touches nothing around its arrays."""
+    note(f"attn limits h={h} hk={hk} d={d} how={how} {first} {past}")
+    lens = [40, 50, 13, 24] * 4
+    n = len(lens)
+    seqs = random_seqs(62, [70 + n for n in lens], h, hk, d)
+
+    def step(wrong):
+        L = Layer(h, hk, d, seqs)
+        L.prefill([70] * n)
+        (q, k, v), cu = L.pack(lens)
+        plan = L.plan(lens, cu)
+        if wrong:
+            cu = cu.clone()
+            cu[0] += first
+            cu[-1] += past
+        (q, qw), (k, kw), (v, vw) = window(q), window(k), window(v)
+        o, ow = window(torch.full_like(q, float("nan")))
+        ws = gdn.alloc_attn_workspace(L.shape, gdn.GDN_ATTN_OP_PREFILL, sum(lens), n, L.cache.k8.shape[0], DEV)
+        gdn.gdn_attn_prefill(L.shape, q, k, v, cu, plan, L.cache, o, ws, max_new=how)
+        assert around(ow).isnan().all()
+        return o, contents(L), L, cu
+
+    want, full, _, _ = step(False)
+    got, after, L, cu = step(True)
+    assert same_bits(got, want) and all(torch.equal(a, b) for a, b in zip(after, full))
+    # the read-out of the new tokens' number of tokens, by the same wrong limits
+    out = [window(torch.full((sum(lens), hk, d), float("nan"), dtype=torch.bfloat16, device=DEV)) for _ in range(4)]
+    plan = gdn.alloc_attn_plan(L.pool, n, 0, L.slot_index)
+    right = cu.clone()
+    right[0], right[-1] = 0, sum(lens)
+    for limits, (k, v) in ((cu, out[:2]), (right, out[2:])):
+        gdn.gdn_attn_cache_read(L.shape, limits, sum(lens), plan, L.cache, k[0], v[0])
+    for a, b in zip(out[:2], out[2:]):
+        assert around(a[1]).isnan().all() and torch.equal(a[0].view(torch.int16), b[0].view(torch.int16))
+
+
+def test_limits_that_leave_tokens_out():
+    """Tokens before the first limit and behind the last belong to nobody: nothing of theirs is written."""
+    h, hk, d, lens = 8, 2, 128, [40, 50, 70] * 4
+    note("attn limits inside")
+    seqs = random_seqs(63, lens, h, hk, d)
+    for how in (70, 0):
+        L = Layer(h, hk, d, seqs)
+        want = torch.cat(L.prefill(lens))
+        L = Layer(h, hk, d, seqs)
+        (q, k, v), cu = L.pack(lens)
+        (_, q), (_, k), (_, v) = window(q), window(k), window(v)
+        cu += 128
+        plan = gdn.alloc_attn_plan(L.pool, len(lens), q.shape[0], L.slot_index)
+        plan.positions.fill_(-7)
+        plan.slot_map.fill_(-7)
+        gdn.gdn_attn_plan(L.pool, cu, plan)
+        assert (around(plan.positions) == -7).all() and (around(plan.slot_map) == -7).all()
+        assert plan.positions[128:-128].tolist() == [p for n in lens for p in range(n)]
+        o = torch.full_like(q, float("nan"))
+        ws = gdn.alloc_attn_workspace(L.shape, gdn.GDN_ATTN_OP_PREFILL, q.shape[0], len(lens), L.cache.k8.shape[0], DEV)
+        gdn.gdn_attn_prefill(L.shape, q, k, v, cu, plan, L.cache, o, ws, max_new=how)
+        assert same_bits(o[128:-128], want) and around(o).isnan().all()
+
+
+@pytest.mark.parametrize("lens", [[40, 50, 13, 24], [1500, 2, 3000, 700]])  # tokens in the plan's launch, or in a second
+@pytest.mark.parametrize("first,past", [(-5, 36), (-100, 100), (3, -4)])
+def test_plan_with_limits_outside_the_tokens(lens, first, past):
+    note(f"plan limits {lens} {first} {past}")
+    pool = gdn.alloc_attn_pool(4, 60, 200, DEV)
+    t = sum(lens)
+    pos, pos_all = window(torch.full((t,), -7, **I32), fill=-7)
+    place, place_all = window(torch.full((t,), -7, dtype=torch.int64, device=DEV), fill=-7)
+    plan = gdn.AttnPlan(torch.empty(4, **I32), pos, place, torch.empty(1, **I32), pool.block_table)
+    cu = torch.tensor([sum(lens[:i]) for i in range(5)], **I32)
+    cu[0] += first
+    cu[-1] += past
+    gdn.gdn_attn_plan(pool, cu, plan)
+    assert int(plan.status) == 0 and plan.ctx_len.tolist() == [0] * 4
+    assert (around(pos_all) == -7).all() and (around(place_all) == -7).all()
+    lo, hi = max(first, 0), t + min(past, 0)
+    seq = torch.bucketize(torch.arange(lo, hi), torch.tensor(cu.tolist()[1:]), right=True)
+    want = torch.arange(lo, hi) - cu.cpu()[seq]
+    assert pos[lo:hi].tolist() == want.tolist()
+    assert (pos[:lo] == -7).all() and (pos[hi:] == -7).all() and (place[:lo] == -7).all() and (place[hi:] == -7).all()
+    assert place[lo:hi].tolist() == (pool.block_table.cpu()[seq, want // 64].long() * 64 + want % 64).tolist()

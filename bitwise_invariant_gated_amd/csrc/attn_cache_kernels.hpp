@@ -61,6 +61,13 @@ __device__ __forceinline__ int pool_block(const StepArgs& a, int row, int b) {
   return min(max(id, 0), a.cache.num_blocks - 1);
 }
 
+// whether the table has a block of the pool there: one that is missing is not written
+__device__ __forceinline__ bool has_block(const StepArgs& a, int row, int b) {
+  if (b >= a.max_blocks) return false;
+  const int id = a.table[(size_t)row * a.max_blocks + b];
+  return id >= 0 && id < a.cache.num_blocks;
+}
+
 // largest finite magnitude among eight bf16, as its bits (ordered like the values)
 __device__ __forceinline__ uint32_t amax8(u32x4 x, uint32_t m) {
 #pragma unroll
@@ -361,15 +368,16 @@ __global__ __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4) void k_attn_ap
 
   if (keys == 64) {  // full now
     const int64_t at = (int64_t)pool_block(a, row, b) * a.Hk + hk;
+    const bool there = has_block(a, row, b);
     const int ek = scale_exponent(km), ev = scale_exponent(vm);
-    if (tid == 0) {
+    if (there && tid == 0) {
       a.cache.k_scale[at] = pow2(ek);
       a.cache.v_scale[at] = pow2(ev);
     }
 #pragma unroll
     for (int j = 0; j < n; ++j) {
       const int x = tid + TH * j, key = x / (D / 8), dim = x % (D / 8) * 8;
-      *(u32x2*)(a.cache.k8 + at * (64 * D) + (dim >> 6) * 4096 + key * 64 + (dim & 63)) = to_e4m3(kx[j], pow2(-ek));
+      if (there) *(u32x2*)(a.cache.k8 + at * (64 * D) + (dim >> 6) * 4096 + key * 64 + (dim & 63)) = to_e4m3(kx[j], pow2(-ek));
       if (RAW && b != last) ((u32x4*)(a.raw_k + ((int64_t)at_block * a.Hk + hk) * (64 * D)))[x] = kx[j];
     }
 #pragma unroll
@@ -390,7 +398,7 @@ __global__ __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4) void k_attn_ap
       }
     }
     __syncthreads();
-    for (int x = tid; x < D * 4; x += TH) {
+    for (int x = tid; there && x < D * 4; x += TH) {
       const uint32_t* w = vt + x / 4 * kLd + x % 4 * 4;
       *(u32x4*)(a.cache.v8 + at * (64 * D) + x * 16) = u32x4{w[0], w[1], w[2], w[3]};
     }

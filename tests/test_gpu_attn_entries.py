@@ -166,3 +166,35 @@ def test_plan_with_limits_outside_the_tokens(lens, first, past):
     assert pos[lo:hi].tolist() == want.tolist()
     assert (pos[:lo] == -7).all() and (pos[hi:] == -7).all() and (place[:lo] == -7).all() and (place[hi:] == -7).all()
     assert place[lo:hi].tolist() == (pool.block_table.cpu()[seq, want // 64].long() * 64 + want % 64).tolist()
+
+
+@pytest.mark.parametrize("how,new", [("decode", 1), (2, 2), (0, 70)])
+@pytest.mark.parametrize("entry", [-1, 1 << 20])
+@pytest.mark.parametrize("h,hk,d", [(7, 7, 64), (16, 4, 128), (8, 2, 256)])
+def test_missing_block_is_not_written(h, hk, d, entry, how, new):
+    """The table has no block of the pool where a row's block fills: nobody's block is written for it."""
+    note(f"attn missing block h={h} hk={hk} d={d} entry={entry} how={how}")
+    n, ctx, row = 8, 127, 3
+    seqs = random_seqs(64, [ctx + new] * n, h, hk, d)
+
+    def step(missing):
+        L = Layer(h, hk, d, seqs)
+        L.prefill([ctx] * n)
+        (q, k, v), cu = L.pack([new] * n)
+        plan = L.plan([new] * n, cu)
+        gone = int(L.pool.block_table[row, 1])
+        if missing:
+            L.pool.block_table[row, 1] = entry
+        before = contents(L)
+        return call(L, q, k, v, cu, plan, how).view(n, new, h, d), before, contents(L), gone
+
+    want, _, full, _ = step(False)
+    got, before, after, gone = step(True)
+    assert all(same_bits(got[i], want[i]) for i in range(n) if i != row)
+    assert same_bits(got[row, 0], want[row, 0])  # its own block comes from the tail
+    for x in range(4):
+        assert torch.equal(after[x][gone], before[x][gone])
+        rest = torch.arange(len(after[x]), device=DEV) != gone
+        assert torch.equal(after[x][rest], full[x][rest])
+    for x in (4, 5):
+        assert torch.equal(after[x], full[x])

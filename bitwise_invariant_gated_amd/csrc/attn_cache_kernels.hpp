@@ -364,11 +364,12 @@ __global__ __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4) void k_attn_ap
     vm = max(vm, red[w][1]);
     bad |= red[w][2];
   }
-  if (tid == 0) a.bad[(int64_t)at_block * a.Hk + hk] = bad;
+  // a missing block is read as some other one, whatever that holds
+  const bool there = keys == 64 && has_block(a, row, b);
+  if (tid == 0) a.bad[(int64_t)at_block * a.Hk + hk] = bad | (keys == 64 && !there);
 
   if (keys == 64) {  // full now
     const int64_t at = (int64_t)pool_block(a, row, b) * a.Hk + hk;
-    const bool there = has_block(a, row, b);
     const int ek = scale_exponent(km), ev = scale_exponent(vm);
     if (there && tid == 0) {
       a.cache.k_scale[at] = pow2(ek);

@@ -36,8 +36,10 @@ struct StepArgs {
 };
 
 // Batch entry i: its packed tokens [c0, c0 + len), the tokens in its cache and its
-// cache row.  An entry without a request (context -1, or a row that the cache
-// does not have) has ctx = row = -1 in every kernel: o = 0, nothing is written.
+// cache row.  An entry without a request (context -1, a row that the cache does not
+// have, or more full blocks than a row of the table is wide) has ctx = row = -1
+// in every kernel: o = 0, nothing is written.  So positions fit 32 bits, and the
+// work that a wrong context can ask for is held to the table's width.
 struct Entry {
   int c0, len, ctx, row;
 };
@@ -51,7 +53,8 @@ __device__ __forceinline__ Entry entry_of(const StepArgs& a, int i) {
   e.len = a.cu ? max(cu_at(a, i + 1) - e.c0, 0) : 1;
   e.ctx = a.ctx_len[i];
   e.row = row_of(a.slot, i, a.cache.num_slots);
-  if (e.ctx < 0 || e.row < 0) e.ctx = e.row = -1;
+  const bool fits = e.ctx <= 0x7fffffff - kBlock - e.len && (e.ctx + e.len) >> 6 <= a.max_blocks;
+  if (e.ctx < 0 || e.row < 0 || !fits) e.ctx = e.row = -1;
   return e;
 }
 

@@ -198,3 +198,61 @@ def test_missing_block_is_not_written(h, hk, d, entry, how, new):
         assert torch.equal(after[x][rest], full[x][rest])
     for x in (4, 5):
         assert torch.equal(after[x], full[x])
+
+
+@pytest.mark.parametrize("how,new", [("decode", 1), (2, 2), (0, 70)])
+@pytest.mark.parametrize("h,hk,d", [(7, 7, 64), (16, 4, 128), (8, 2, 256)])
+def test_contexts_that_the_table_cannot_hold(h, hk, d, how, new):
+    """ctx_len up to the end of 32 bits, in some entries: zeros, nothing of theirs written, the others as
+    without them."""
+    note(f"attn contexts past the table h={h} hk={hk} d={d} how={how}")
+    n, ctx = 8, 127
+    seqs = random_seqs(65, [ctx + new] * n, h, hk, d)
+
+    def step(wrong):
+        L = Layer(h, hk, d, seqs)
+        L.prefill([ctx] * n)
+        (q, k, v), cu = L.pack([new] * n)
+        plan = L.plan([new] * n, cu)
+        for i, x in wrong.items():
+            plan.ctx_len[i] = x
+        before = contents(L)
+        return call(L, q, k, v, cu, plan, how).view(n, new, h, d), before, contents(L), L.pool.block_table
+
+    want, _, full, table = step({})
+    width = table.shape[1]
+    wrong = {0: 2 ** 31 - 1, 3: 2 ** 31 - 100, 4: 1 << 30, 7: 64 * (width + 1) - new}
+    got, before, after, _ = step(wrong)
+    mine = torch.cat([table[i][table[i] >= 0] for i in wrong]).long()
+    for i in range(n):
+        if i in wrong:
+            assert torch.count_nonzero(got[i]) == 0 and not got[i].isnan().any()
+        else:
+            assert same_bits(got[i], want[i])
+    for x in range(4):
+        assert torch.equal(after[x][mine], before[x][mine])
+        rest = torch.ones(len(after[x]), dtype=torch.bool, device=DEV)
+        rest[mine] = False
+        assert torch.equal(after[x][rest], full[x][rest])
+    for x in (4, 5):
+        for i in range(n):
+            assert torch.equal(after[x][i], (before if i in wrong else full)[x][i])
+
+
+@pytest.mark.parametrize("how,new", [("decode", 1), (2, 2), (0, 30)])
+def test_open_block_past_a_full_table(how, new):
+    """Every full block is in the table and the open one has no entry yet: the answer is that of a wider table."""
+    h, hk, d, n, ctx = 8, 8, 64, 8, 130
+    note(f"attn open block past the table how={how}")
+    seqs = random_seqs(66, [ctx + new] * n, h, hk, d)
+    got = []
+    for width in (None, 2):
+        L = Layer(h, hk, d, seqs)
+        L.prefill([ctx] * n)
+        (q, k, v), cu = L.pack([new] * n)
+        plan = L.plan([new] * n, cu)
+        table = plan.block_table if width is None else plan.block_table[:, :width].contiguous()
+        hand = gdn.AttnPlan(plan.ctx_len, plan.positions, plan.slot_map, plan.status, table, plan.slot_index)
+        got.append((call(L, q, k, v, cu, hand, how), contents(L)))
+    assert same_bits(got[0][0], got[1][0])
+    assert all(torch.equal(a, b) for a, b in zip(got[0][1], got[1][1]))

@@ -98,9 +98,11 @@ __device__ __forceinline__ bool not_finite8(u32x4 x) {
   return bad;
 }
 
-// eight bf16 times inv (a power of two) -> eight e4m3, nearest even; what is
-// not finite becomes NaN
-__device__ __forceinline__ u32x2 to_e4m3(u32x4 x, float inv) {
+// eight bf16 divided by 2^e -> eight e4m3, nearest even; what is not finite
+// becomes NaN.  At the largest exponent, 120, e4m3 reaches past bf16: what would
+// round to 256 * 2^120, which is infinite there, is held to 240 * 2^120.
+__device__ __forceinline__ u32x2 to_e4m3(u32x4 x, int e) {
+  const float inv = pow2(-e), most = e == 120 ? 240.f : 448.f;
   u32x2 r;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -111,7 +113,8 @@ __device__ __forceinline__ u32x2 to_e4m3(u32x4 x, float inv) {
       f[2 * j + 1] = __uint_as_float(x[2 * i + j] & 0xffff0000u) * inv;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = __builtin_isinf(f[j]) ? __uint_as_float(0x7fc00000u) : f[j];
+    for (int j = 0; j < 4; ++j)
+      f[j] = __builtin_isfinite(f[j]) ? __builtin_amdgcn_fmed3f(f[j], -most, most) : __uint_as_float(0x7fc00000u);
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
     w = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
     r[i] = (uint32_t)w;
@@ -153,7 +156,7 @@ __device__ __forceinline__ void quantise_block(const CacheArgs& c, int64_t at, F
 #pragma unroll
   for (int i = 0; i < n; ++i) {
     const int ch = threadIdx.x + 256 * i, key = ch / (D / 8), dim = ch % (D / 8) * 8;
-    *(u32x2*)(c.k8 + at * (64 * D) + (dim >> 6) * 4096 + key * 64 + (dim & 63)) = to_e4m3(x[i], pow2(-e));
+    *(u32x2*)(c.k8 + at * (64 * D) + (dim >> 6) * 4096 + key * 64 + (dim & 63)) = to_e4m3(x[i], e);
   }
   if (threadIdx.x == 0) c.k_scale[at] = pow2(e);
   m = 0;
@@ -162,7 +165,7 @@ __device__ __forceinline__ void quantise_block(const CacheArgs& c, int64_t at, F
   e = scale_exponent(block_max256(m, red));
 #pragma unroll
   for (int i = 0; i < n; ++i)
-    *(u32x2*)(c.v8 + at * (64 * D) + (int64_t)(threadIdx.x + 256 * i) * 8) = to_e4m3(x[i], pow2(-e));
+    *(u32x2*)(c.v8 + at * (64 * D) + (int64_t)(threadIdx.x + 256 * i) * 8) = to_e4m3(x[i], e);
   if (threadIdx.x == 0) c.v_scale[at] = pow2(e);
 }
 
@@ -381,7 +384,7 @@ __global__ __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4) void k_attn_ap
 #pragma unroll
     for (int j = 0; j < n; ++j) {
       const int x = tid + TH * j, key = x / (D / 8), dim = x % (D / 8) * 8;
-      if (there) *(u32x2*)(a.cache.k8 + at * (64 * D) + (dim >> 6) * 4096 + key * 64 + (dim & 63)) = to_e4m3(kx[j], pow2(-ek));
+      if (there) *(u32x2*)(a.cache.k8 + at * (64 * D) + (dim >> 6) * 4096 + key * 64 + (dim & 63)) = to_e4m3(kx[j], ek);
       if (RAW && b != last) ((u32x4*)(a.raw_k + ((int64_t)at_block * a.Hk + hk) * (64 * D)))[x] = kx[j];
     }
 #pragma unroll
@@ -391,7 +394,7 @@ __global__ __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4) void k_attn_ap
       transpose4(vx[j], t);
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
-        const u32x2 w = to_e4m3(u32x4{t[e][0], t[e][1], t[e + 1][0], t[e + 1][1]}, pow2(-ev));
+        const u32x2 w = to_e4m3(u32x4{t[e][0], t[e][1], t[e + 1][0], t[e + 1][1]}, ev);
         vt[(dim + e) * kLd + kq] = w[0];
         vt[(dim + e + 1) * kLd + kq] = w[1];
       }

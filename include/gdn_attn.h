@@ -31,7 +31,9 @@
  * scale is exact, so an element is rounded once, and its cached value is a
  * bf16 number.  e4m3 keeps its relative precision over 15 binades, so a
  * power of two instead of amax / 448 gives up at most one binade at the
- * bottom.  A NaN or infinity is cached as NaN.
+ * bottom.  A finite magnitude past 240 * 2^120 (3.2e38; bf16 ends at 3.4e38)
+ * is cached as that, since the next e4m3 value, 256, would be 2^128.  A NaN
+ * or infinity is cached as NaN.
  *
  * Conventions: those of gdn_cpr.h (device pointers, 16-byte aligned; calls
  * only enqueue on `stream`; nothing is allocated; host-detectable errors

@@ -7,6 +7,7 @@ from __future__ import annotations
 import numpy as np
 
 BLOCK = 64
+TOP = 240 * 2.0 ** 120  # the largest cached magnitude
 
 
 def e4m3_values() -> np.ndarray:
@@ -45,7 +46,9 @@ def cached(x: np.ndarray) -> np.ndarray:
         for h in range(x.shape[1]):
             blk = out[b * BLOCK:(b + 1) * BLOCK, h]
             s = block_scale(blk)
-            out[b * BLOCK:(b + 1) * BLOCK, h] = to_e4m3(blk / s) * s
+            # 256 * 2^120 is no bf16 number
+            most = np.where(np.isfinite(blk), TOP, np.inf)
+            out[b * BLOCK:(b + 1) * BLOCK, h] = to_e4m3(np.clip(blk, -most, most) / s) * s
     return out
 
 

@@ -64,11 +64,10 @@ __device__ __forceinline__ int pool_block(const StepArgs& a, int row, int b) {
   return min(max(id, 0), a.cache.num_blocks - 1);
 }
 
-// whether the table has a block of the pool there: one that is missing is not written
-__device__ __forceinline__ bool has_block(const StepArgs& a, int row, int b) {
-  if (b >= a.max_blocks) return false;
-  const int id = a.table[(size_t)row * a.max_blocks + b];
-  return id >= 0 && id < a.cache.num_blocks;
+// the same for writing: -1 where the table has no block of the pool
+__device__ __forceinline__ int block_to_write(const StepArgs& a, int row, int b) {
+  const int id = b < a.max_blocks ? a.table[(size_t)row * a.max_blocks + b] : -1;
+  return id < a.cache.num_blocks ? max(id, -1) : -1;
 }
 
 // largest finite magnitude among eight bf16, as its bits (ordered like the values)
@@ -306,6 +305,7 @@ __global__ __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4) void k_attn_ap
   const int old = b == first ? ctx & 63 : 0;  // tokens of this block that were there
   const int64_t from = (int64_t)c0 + (int64_t)b * 64 - ctx;  // packed row of the block's key 0
   const int keys = min(64, ctx + len - b * 64);
+  const int block = keys == 64 ? block_to_write(a, row, b) : -1;
 
   // run i: key x / (D / 8), dims 8 (x % (D / 8)) ..; square i: keys 4 (x / (D / 4)) .., dims 4 (x % (D / 4)) ..,
   // x = thread + TH i
@@ -370,21 +370,20 @@ __global__ __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4) void k_attn_ap
     vm = max(vm, red[w][1]);
     bad |= red[w][2];
   }
-  // a missing block is read as some other one, whatever that holds
-  const bool there = keys == 64 && has_block(a, row, b);
-  if (tid == 0) a.bad[(int64_t)at_block * a.Hk + hk] = bad | (keys == 64 && !there);
+  const bool missing = keys == 64 && block < 0;  // it is read as some other one, whatever that holds
+  if (tid == 0) a.bad[(int64_t)at_block * a.Hk + hk] = bad | missing;
 
   if (keys == 64) {  // full now
-    const int64_t at = (int64_t)pool_block(a, row, b) * a.Hk + hk;
+    const int64_t at = (int64_t)block * a.Hk + hk;
     const int ek = scale_exponent(km), ev = scale_exponent(vm);
-    if (there && tid == 0) {
+    if (!missing && tid == 0) {
       a.cache.k_scale[at] = pow2(ek);
       a.cache.v_scale[at] = pow2(ev);
     }
 #pragma unroll
     for (int j = 0; j < n; ++j) {
       const int x = tid + TH * j, key = x / (D / 8), dim = x % (D / 8) * 8;
-      if (there) *(u32x2*)(a.cache.k8 + at * (64 * D) + (dim >> 6) * 4096 + key * 64 + (dim & 63)) = to_e4m3(kx[j], ek);
+      if (!missing) *(u32x2*)(a.cache.k8 + at * (64 * D) + (dim >> 6) * 4096 + key * 64 + (dim & 63)) = to_e4m3(kx[j], ek);
       if (RAW && b != last) ((u32x4*)(a.raw_k + ((int64_t)at_block * a.Hk + hk) * (64 * D)))[x] = kx[j];
     }
 #pragma unroll
@@ -405,7 +404,7 @@ __global__ __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4) void k_attn_ap
       }
     }
     __syncthreads();
-    for (int x = tid; there && x < D * 4; x += TH) {
+    for (int x = tid; !missing && x < D * 4; x += TH) {
       const uint32_t* w = vt + x / 4 * kLd + x % 4 * 4;
       *(u32x4*)(a.cache.v8 + at * (64 * D) + x * 16) = u32x4{w[0], w[1], w[2], w[3]};
     }

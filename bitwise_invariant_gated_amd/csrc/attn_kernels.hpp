@@ -1257,11 +1257,12 @@ __global__ __launch_bounds__(256, (kRowsPerCu<D, MULTI>)) void k_attn_rows(const
         const uint16_t* nv = a.v + (int64_t)i * a.v_stride + (int64_t)hk * D;
         if (tid < D / 8) *(u32x4*)(wk + at * D + tid * 8) = *(const u32x4*)(nk + tid * 8);
         for (int x = tid; x < D; x += 256) wv[x * 64 + at] = nv[x];
-        if (at == 63 && has_block(a, cache_row, b_hi)) {
+        const int block = at == 63 ? block_to_write(a, cache_row, b_hi) : -1;
+        if (block >= 0) {
           __threadfence_block();
           __syncthreads();
           quantise_block<D>(
-              a.cache, (int64_t)pool_block(a, cache_row, b_hi) * a.Hk + hk,
+              a.cache, (int64_t)block * a.Hk + hk,
               [&](int x) { return ((const u32x4*)wk)[x]; }, [&](int x) { return ((const u32x4*)wv)[x]; }, s_red);
         }
       }

@@ -172,14 +172,12 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_release(const ReleaseArgs
     int row = -1, held = 0, total;
     if (tid < n) {
       row = row_of(a.slot, i, a.num_slots);
-      if (row >= 0) held = min(max(a.held[row], 0), a.max_blocks);
+      // exchanged, so that a row named twice gives its blocks back once
+      if (row >= 0) held = min(max(atomicExch(&a.held[row], 0), 0), a.max_blocks);
     }
     s_upto[tid] = block_scan(held, s_sums, &total);
     s_row[tid] = row;
-    if (row >= 0) {
-      a.held[row] = 0;
-      a.seq_len[row] = 0;
-    }
+    if (row >= 0) a.seq_len[row] = 0;
     __syncthreads();
     for (int j = tid; j < total; j += kPlanThreads) {
       const int r = first_above(s_upto, n, j);

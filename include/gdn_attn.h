@@ -174,7 +174,8 @@ gdn_status gdn_attn_plan(const gdn_attn_pool* pool, int32_t num_seqs, int64_t to
  * Requests leave: the blocks of the N rows slot_index[i] (NULL: row i) go
  * back on the free stack, last request and last block first, so that a plan
  * right after gives them out in the same order; the rows are emptied (table
- * -1, blocks_held 0, seq_len 0).  Entries that are -1 are skipped.
+ * -1, blocks_held 0, seq_len 0).  Entries that are -1 are skipped, and so is
+ * a row's second entry (which of the two counts is not defined).
  */
 gdn_status gdn_attn_release(const gdn_attn_pool* pool, int32_t num_seqs, const int32_t* slot_index,
                             void* stream);

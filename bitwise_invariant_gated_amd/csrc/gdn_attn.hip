@@ -128,6 +128,8 @@ extern "C" gdn_status gdn_attn_plan(const gdn_attn_pool* pool, int32_t num_seqs,
   if (!step) return fail(GDN_ERR_INVALID_ARG, "%s: step is NULL", fn);
   CHECK_PTR(cu_seqlens, "cu_seqlens");
   CHECK_PTR(step->status, "step.status");
+  if (step->block_table != pool->block_table || step->max_blocks != pool->max_blocks || step->num_slots != pool->num_slots)
+    return fail(GDN_ERR_INVALID_ARG, "%s: step.block_table, max_blocks and num_slots are not the pool's", fn);
   CHECK_OPT_PTR(step->slot_index, "step.slot_index");
   if (num_seqs > 0) CHECK_PTR(step->ctx_len, "step.ctx_len");
   if (total_tokens > 0) {

@@ -106,7 +106,7 @@ typedef struct {
  *   slot_map    [T] int64   every new token's place in the pool, block *
  *               GDN_ATTN_BLOCK + offset; -1 in a request that has ctx_len -1
  *   status      [1] int32   requests refused for want of blocks
- *   block_table, max_blocks, num_slots   the pool's
+ *   block_table, max_blocks, num_slots   the pool's (the plan refuses others)
  *   slot_index  [N] int32 cache row of every batch entry, or NULL for row i.
  *               Rows are distinct within a call; -1 marks an entry that is
  *               only there to fill the batch.

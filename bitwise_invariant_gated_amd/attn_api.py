@@ -63,6 +63,9 @@ class AttnPool:
             raise ValueError("pool arrays do not match the block table")
         object.__setattr__(self, "_ref", ctypes.byref(_lib.AttnPoolC(*map(_ptr, t), slots, width, self.free_blocks.numel())))
 
+    def __reduce__(self):
+        return AttnPool, _fields(self)
+
 
 def alloc_attn_pool(num_slots: int, max_blocks: int, num_blocks: int, device="cuda") -> AttnPool:
     """An empty pool: every block free, the lowest id to be given out first."""
@@ -94,6 +97,9 @@ class AttnPlan:
         object.__setattr__(self, "_ref", ctypes.byref(_lib.AttnStepC(
             _ptr(self.ctx_len), _ptr(self.positions), _ptr(self.slot_map), _ptr(self.status), _ptr(self.block_table),
             _ptr(self.slot_index), width, slots)))
+
+    def __reduce__(self):
+        return AttnPlan, _fields(self)
 
 
 def alloc_attn_plan(pool: AttnPool, num_seqs: int, total_tokens: int,
@@ -131,6 +137,9 @@ class AttnCache:
             _ptr(self.k8), _ptr(self.v8), _ptr(self.k_scale), _ptr(self.v_scale), _ptr(self.tail_k),
             _ptr(self.tail_v), blocks, slots)))
 
+    def __reduce__(self):
+        return AttnCache, _fields(self)
+
     def check(self, shape: AttnShape) -> None:
         if self.tail_k.shape[1] != shape.kv_heads or self.tail_k.shape[3] != shape.head_dim:
             raise ValueError("the cache is of another shape")
@@ -164,6 +173,11 @@ def _stream(stream) -> int:
     if stream is not None:
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _fields(x) -> tuple:
+    """What a copy is made from: the arrays; the C handle (_ref) is made anew over the copy's."""
+    return tuple(getattr(x, f.name) for f in dataclasses.fields(x))
 
 
 def _check_types(tensors, dtype) -> None:

@@ -84,33 +84,37 @@ def check_dpp_hazards(asm_text: str) -> list:
     return bad
 
 
-# kernels on the bf16 hot paths (prefill, decode, continuation, fwd_bwd), by
-# mangled-name fragment; register spills there cost a scratch set-up per
-# launch and memory traffic per spill, so the build rejects them.  k_attn_prefill
-# and k_attn_rows of two row tiles are not among them: they fill the registers and
-# spill what their main loops do not touch
+# kernels on the bf16 hot paths (prefill, decode, continuation, fwd_bwd, and the
+# attention layer), by mangled-name fragment; register spills there cost a
+# scratch set-up per launch and memory traffic per spill, so the build rejects them
 HOT_KERNELS = ("k_scanIN3cpr4Bf16", "k_chain_scan_bf16", "k_decodeIN3cpr4Bf16", "k_resync_bf16",
                "k_cont_headIN3cpr4Bf16", "k_chunk_local_prefill_bf16", "k_chain_prefill_bf16", "k_bwd_local_bf16",
-               "k_bwd_chain_bf16", "k_bwd_state_grads_bf16", "k_plan", "k_attn_join",
-               "k_attn_norm_rope", "k_attn_plan", "k_attn_append")
+               "k_bwd_chain_bf16", "k_bwd_state_grads_bf16", "k_plan", "k_attn_")
+
+# three of them fill the registers, and spill: up to this many.  k_attn_prefill
+# reloads one value beside the score MFMAs of a tile, and its fold at the end of a partition
+# stores and reloads 14 (d = 128) or one (256); k_attn_rows of two row tiles at d = 128
+# reloads one or two in each part of its loop
+MAY_SPILL = {"k_attn_prefillILi128E": 76, "k_attn_prefillILi256E": 21, "k_attn_rowsILi128ELi2E": 14}
 
 
-def check_spills(asm_text: str, hot=HOT_KERNELS) -> list:
+def check_spills(asm_text: str, hot=HOT_KERNELS, may=MAY_SPILL) -> list:
     """(kernel, spilled VGPRs) for every hot kernel whose metadata records
-    VGPR spills."""
+    more VGPR spills than it may have."""
     import re
     bad = []
     for m in re.finditer(r"\.name:\s+(\S+)\n(.*?)\.wavefront_size", asm_text, re.S):
         name, body = m.group(1), m.group(2)
         sp = re.search(r"\.vgpr_spill_count:\s+(\d+)", body)
-        if sp and int(sp.group(1)) > 0 and any(h in name for h in hot):
+        most = next((n for frag, n in may.items() if frag in name), 0)
+        if sp and int(sp.group(1)) > most and any(h in name for h in hot):
             bad.append((name, int(sp.group(1))))
     return bad
 
 
 def check_isa(texts: list, verbose: bool = True) -> None:
     """Check the sources' device assembly: the DPP hazard rule, and that no
-    hot kernel spills."""
+    hot kernel spills (or more than it may)."""
     n_dpp = sum(t.count("v_fmac_f32_dpp") for t in texts)
     bad = [v for t in texts for v in check_dpp_hazards(t)]
     if bad:
@@ -121,7 +125,7 @@ def check_isa(texts: list, verbose: bool = True) -> None:
         raise RuntimeError("register spills in hot kernels: " + "; ".join(f"{n} ({k})" for n, k in spills))
     if verbose:
         print(f"ISA check: {n_dpp} v_fmac_f32_dpp instructions, no VALU-write -> DPP-read hazard, "
-              "no spills in the hot kernels")
+              "no spills in the hot kernels beyond those listed")
 
 
 def _run(cmds: list) -> str:

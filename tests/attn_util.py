@@ -98,3 +98,45 @@ def tolerance(v) -> float:
     2^-8 max|v| in the weighted mean) and so is o (2^-8 |o| <= 2^-8 max|v|);
     scores, exp2 and the fp32 sums add a few 2^-20 of max|v|, covered by the 5%."""
     return 1.05 * 2.0 ** -7 * float(np.abs(v[np.isfinite(v)]).max())
+
+
+# long contexts of the tests on marked_seqs: heads, key/value heads, head dim, tokens
+LONG = [(8, 2, 128, [9000, 2, 5200]), (2, 1, 128, [70000]), (2, 1, 64, [33087, 9000]), (4, 2, 256, [20000, 300])]
+SHARED = (1, 1, 64, 20050)
+
+
+def marked_seqs(seed, lens, h, hk, d):
+    """Sequences in which every block shows in the output: V is zero but in dim
+    (block mod d), where it is positive and of a size of its own, and the scores are
+    even enough that no block's share of its dim is small.  The scales of K and V
+    change from block to block."""
+    rng = np.random.default_rng(seed)
+    out = []
+    for n in lens:
+        block = np.arange(n) // 64
+        k = rng.standard_normal((n, hk, d)) * 2.0 ** (block % 3 - 1)[:, None, None]
+        v = np.zeros((n, hk, d))
+        v[np.arange(n), :, block % d] = rng.uniform(0.5, 1.0, (n, hk)) * 2.0 ** (block % d % 5)[:, None]
+        to = lambda x: torch.from_numpy(x.astype(np.float32)).bfloat16()  # noqa: E731
+        out.append((bf16(rng, n, h, d, std=0.5), to(k), to(v)))
+    return out
+
+
+def error_bound(o, spread):
+    """Largest |result - o|, element by element; spread: the same mean of |v|.  p is
+    rounded to bf16, by 2^-8 = u of itself at most, in numerator and denominator alike:
+    |sum p (1 + e) v / sum p (1 + e) - o| <= u / (1 - u) (spread + |o|).  The output's
+    rounding: u of it.  Scores (d products in fp32, |terms| of some tens at most), exp2
+    and the sums in fp32 change p by less than 2^-10."""
+    u = 2.0 ** -8
+    return (u / (1 - u) * (1 + u) + 2.0 ** -10) * (spread + np.abs(o)) + u * np.abs(o)
+
+
+def expect_within(q, k, v, scale, first=0):
+    """The oracle's o of the positions from `first` on, and error_bound."""
+    from oracle import attention as ref
+
+    q, k, v = (f64(x) for x in (q, k, v))
+    o = ref.attention(q[first:], k, v, scale, first)
+    spread = o if (v >= 0).all() else ref.attention(q[first:], k, np.abs(v), scale, first)
+    return o, error_bound(o, spread)

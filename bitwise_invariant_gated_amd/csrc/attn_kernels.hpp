@@ -14,11 +14,15 @@
 //   partitions: (m, l, O) = fold of the total and the partition, left to
 //   right: O = fma(Op, exp2(mp - m'), O exp2(m - m')).
 //   o = O (1 / l).
+// p is rounded to bf16 because the second product takes bf16 operands; that is the
+// largest error of o beside its own rounding (5 x 2,048: 0.0020 of its size against 64
+// bits, where 32 bits throughout and one rounding at the end give 0.0016).
 // m is a reference for the exponents, not the maximum itself: it moves, and O
 // and l are scaled, only when p would pass 2^8, which bf16 and the 32-bit sums hold
 // as exactly as 1.  Of random scores a partition's first tile sets it for the rest,
 // where a true running maximum moves for some row of 16 in nearly every tile
-// (prefill, 5 x 2,048 at d = 128: 163 us a call; with the maximum 170).
+// (prefill, 5 x 2,048 at d = 128: 172 us a call, with the maximum 179; 1 x 10,240 at
+// d = 256: 1,109 and 1,167).
 // A masked tile leaves a row's state as it is (alpha = 1, p = 0), so which
 // tiles a kernel walks through for a row beyond its own does not matter,
 // and neither does which work-group does which partition.
@@ -121,19 +125,21 @@ __device__ __forceinline__ void fold_weights(float& m, float mp, float& a, float
 // hk G + r % G.  A work-group takes kRows of them, a wave 16 kRT, and all of it
 // walks the keys together through tiles in LDS, in the order the MFMA operands
 // are read (conflict-free, 16 bytes per lane), while the bytes of the next one
-// are in flight from memory.  What bounds it is the issue of instructions: two
-// waves on a SIMD, which the accumulators' registers allow, issue one in about
-// 5 cycles.  So a tile is converted to bf16 once per work-group, before it is
-// written to LDS, at d = 64 and 128 (5 x 2,048 at d = 128: 184 us; with 8-bit tiles,
-// which every wave converts as it reads, 199).  At d = 256 the 8-bit tiles leave LDS
-// for more of the folded total, which otherwise goes to scratch memory in
-// the loop (1 x 10,240: 1,240 us; bf16 tiles 1,690).
+// are in flight from memory.  The accumulators' registers allow two waves on a
+// SIMD.  Of a long prompt what bounds it is their issue of instructions, one a SIMD in
+// 6 to 7 cycles at d = 256 with the MFMAs busy a third of the time; of 2,048
+// tokens at d = 128 it is one in 11, MFMAs busy for a quarter, and the start, the masked
+// tiles and the own blocks count for as much.  So a tile is converted to bf16 once per work-group,
+// before it is written to LDS, at d = 64 and 128 (5 x 2,048 at d = 128: 172 us a call;
+// with 8-bit tiles, which every wave converts as it reads, 185).  At d = 256 the 8-bit
+// tiles leave LDS for more of the folded total, which otherwise goes to scratch memory in
+// the loop (1 x 10,240: 1,109 us a call; bf16 tiles 1,616).
 //
 // The 8-bit blocks come first, all in one loop (those from the work-group's
 // first own block on are masked per row), then the rows' own blocks.
 //
-// Measured: 5 x 2,048, 16 heads, d = 128: 143 us, 85.9 GFLOP, 600 TFLOP/s; 1 x 10,240, 16 heads over 2,
-// d = 256: 1,090 us, 859 GFLOP, 790 TFLOP/s; a library product of two 8,192 x 8,192
+// Measured: 5 x 2,048, 16 heads, d = 128: 145 us, 85.9 GFLOP, 590 TFLOP/s; 1 x 10,240, 16 heads over 2,
+// d = 256: 1,076 us, 859 GFLOP, 800 TFLOP/s; a library product of two 8,192 x 8,192
 // matrices reaches 1,210.  Two more tries at the issue of instructions changed nothing: half of the
 // waves half a tile behind the others, and half of the exponentials between the MFMAs.
 template <int D>
@@ -663,7 +669,7 @@ __device__ __forceinline__ void prefill_rows(const StepArgs& a, PrefillLds<D>* s
 #pragma unroll
       for (int t = 0; t < RT; ++t) upto[t] = b < pos[t] >> 6 ? 63 : -1;
       // MFMAs first: a wave that has some to issue goes before one in its
-      // softmax (1 x 10,240 at d = 256: 1,165 us; all alike 1,242)
+      // softmax (1 x 10,240 at d = 256: 1,109 us a call; all alike 1,156)
       __builtin_amdgcn_s_setprio(1);
       scores(b & 1);
       __builtin_amdgcn_s_setprio(0);
@@ -779,9 +785,10 @@ __device__ __forceinline__ int parts_of(const RowsArgs& a, int ctx, int len, int
 __device__ __forceinline__ int len_of(const RowsArgs& a, int i) { return entry_of(a.s, i).len; }
 
 // What a chunk costs, in units of a partition: its partitions, and its own
-// block, first loads and outputs, which take about as long as two (with one, 16 x 16
-// tokens of 8 heads each to 2 at d = 256 took 169 us instead of 143; with none, decode
-// of 256 x 4,096 203 instead of 197).
+// block, first loads and outputs, which take about as long as two (two, one, none:
+// 16 x 37 new tokens, 4 query heads to each of 8, d = 64 after 5,000 tokens 110, 115 and
+// 118 us, d = 128 after 3,000 127, 134 and 134; decode of 256 x 4,096 161.7, 162.2 and
+// 162.6; ragged turns after 4,000 to 8,000, whose contexts weigh more, 118, 112 and 113).
 constexpr int kChunkCost = 2;
 
 // units of all chunks of sequence i
@@ -807,13 +814,17 @@ __device__ __forceinline__ int run_of(int total, int W, int x) {
 
 // Work-groups of k_attn_rows that share a CU.  With one its waves have all
 // registers, and what hides the memory's latency are the loads that a wave has in
-// flight (decode, 256 x 4,096 at d = 128: 176 us; with two, whose loop spilled, 198;
-// 16 x 16 new tokens at d = 256: 114 us; two 143); fewer runs also leave fewer records.
-// Several new tokens at d = 64 and 128 keep the MFMAs busier with two (16 x 37 tokens at d = 64:
-// 118 us; one 144, three 131).
+// flight (decode, 256 x 4,096 at d = 128: 162 us a call, with two 166; 16 x 16 new tokens,
+// 8 query heads to each of 2, d = 256, after 5,000: 116, with two 149); fewer runs also leave
+// fewer records.  Several new tokens at d = 64 and 128 keep the MFMAs busier with two (16 x 37
+// tokens, 4 query heads to each of 8, d = 64, after 5,000: 110 us; one 171, three 116;
+// d = 128, after 3,000: 127 and one 163).
 //
-// Bound by memory in decode: 256 x 4,096, 823 MB, 154 us, 5.3 TB/s, where a
-// copy moves 4.65 and a kernel that only reads 6.1; 3 x 100,003, 307 MB, 58 us.
+// Bound by memory in decode: 256 x 4,096, 823 MB, 155 us, 5.3 TB/s, where a
+// copy moves 4.65 and a kernel that only reads 6.1; 3 x 100,003, 307 MB, 58 us.  Few new
+// tokens are bound by neither: 88 us of the ragged turns at d = 64 are 9.4 VALU instructions to
+// an MFMA, one instruction a SIMD in 10 cycles and MFMAs busy a sixth of the time, so
+// the two barriers and the dependent parts of a step count beside the issue.
 template <int D, bool MULTI>
 constexpr int kRowsPerCu = MULTI && D < 256 ? 2 : 1;
 
@@ -837,8 +848,8 @@ constexpr int kRowsPerCu = MULTI && D < 256 ? 2 : 1;
 // which this kernel appends itself.
 //
 // STREAM: no other chunk reads the keys, and the caches need not keep them (decode,
-// 256 x 4,096 at d = 128: 160 us instead of 176; 64 x 4 new tokens after 3,000: 96 instead of 111; but 5
-// chunks a sequence, 16 x 37 tokens after 3,000: 150 instead of 129).
+// 256 x 4,096 at d = 128: 162 us instead of 178; 64 x 4 new tokens after 3,000: 98 instead of 119; but 5
+// chunks a sequence, 16 x 37 tokens after 3,000: 151 instead of 127).
 template <int D, int RT, bool MULTI, bool STREAM>
 __global__ __launch_bounds__(256, (kRowsPerCu<D, MULTI>)) void k_attn_rows(const RowsArgs ra) {
   const StepArgs& a = ra.s;
@@ -1310,8 +1321,8 @@ __global__ __launch_bounds__(256, (kRowsPerCu<D, MULTI>)) void k_attn_rows(const
 // records, but what it needs of each is not: the weights of 64 folds come
 // from prefix maxima (exact in any order), a lane each, and many records are
 // asked for before the first is used, so the chain is two operations a record
-// (195 records a row, 3 x 100,003 at d = 128: 20 us).  Two batches in turn, the next asked
-// for during the fold, took 26 us, weights through LDS and a wave to a work-group 59.
+// (195 records a row, 3 x 100,003 at d = 128: 18 us; where it was 20, two batches in turn, the
+// next asked for during the fold, took 26, weights through LDS and a wave to a work-group 59).
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_join(const RowsArgs ra, int W) {
   constexpr int V = D / 64;
@@ -1393,7 +1404,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const RowsArgs ra, int W) {
     const float mp = j0 + lane < k ? pm[(j0 + lane) * sm] : kNegInf;
     float wa = 0.f, wb = 0.f;
     if (k - j0 > 16) {
-      constexpr int S = 32;  // with 64 more of the last batch is in vain (3 x 100,003: 81 us a call, with 32 76)
+      constexpr int S = 32;  // with 64 more of the last batch is in vain (3 x 100,003: 82 us a call, with 32 77)
 #pragma unroll 1
       for (int u0 = 0; u0 < 64 && j0 + u0 < k; u0 += S) batch(std::integral_constant<int, S>{}, j0, u0, mp, wa, wb);
     } else {

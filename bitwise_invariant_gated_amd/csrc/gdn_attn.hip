@@ -397,17 +397,23 @@ RowsLayout decode_layout(const gdn_attn_shape& s, int32_t N, int32_t num_blocks)
 }
 
 // Prefill by k_attn_rows: rows of a chunk.  d = 256 has registers for one
-// 16-row tile; with 64 rows, four tiles, the others spill (16 x 37 new tokens
+// 16-row tile; with 64 rows, four tiles, the others spilled (16 x 37 new tokens
 // after 5,000, 4 query heads to each of 8: 130 us instead of 116 at d = 64, 291 instead of 177 at 128).
 int chunk_rows(const gdn_attn_shape& s, int64_t rows) { return s.head_dim == 256 || rows <= 16 ? 16 : 32; }
 
 // Prefill takes k_attn_rows, which splits the keys and reads them once per
 // chunk, if the batch has no more chunks than this, each sequence counted with the
 // most rows of any, or a sequence one only; else k_attn_prefill, which splits rows
-// only, 256 to a work-group.  Turns after 5,000, 4 query heads to each of 8,
-// k_attn_rows / k_attn_prefill in us, d = 64 and d = 128: 512 chunks 81 / 100 and 131 / 153,
-// 640 chunks 116 / 129 and 177 / 171, 1,024 chunks 151 / 134 and 239 / 180; d = 256, 8 to each of
-// 2, 256 chunks 141 / 212, 512 chunks 225 / 215, 1,024 chunks 476 / 224.
+// only, 256 to a work-group.  Turns of 64 tokens (d = 256: 32) after 5,000, k_attn_rows /
+// k_attn_prefill in us, by chunks:
+//                                     256        512        640        768       1,024
+//   d = 64,  4 query heads to each of 8   67 / 132   86 / 133  118 / 133  132 / 135  153 / 135
+//   d = 128, the same                     85 / 178  137 / 178  175 / 177  193 / 181  241 / 181
+//   d = 256, 8 to each of 2              108 / 215  210 / 215  264 / 215  302 / 217  393 / 220
+// One bound for all: the two are even at about 780 chunks at d = 64, 650 at 128 and 530 at
+// 256, so batches of 530 to 640 at d = 256 take the slower one (by up to 23 %).  How full the
+// chunks and tiles are moves these by some per cent (37 tokens, 640 chunks: d = 64
+// 116 / 129, d = 128 174 / 171).
 constexpr int kMostChunks = 640;
 
 bool takes_rows(const gdn_attn_shape& s, int32_t N, int64_t rows) {

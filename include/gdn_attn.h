@@ -46,7 +46,8 @@
  *     in place out of a projection that makes them in one row.
  *   - Device data (lengths, tables, positions) is the caller's to get right;
  *     the kernels keep their accesses inside the arrays where it is not:
- *     cu_seqlens are held to 0 .. T, block ids to the pool, positions to the
+ *     cu_seqlens are held to 0 .. T (the plan counts blocks by the lengths as
+ *     they are, and holds what it writes per token), block ids to the pool, positions to the
  *     rotation table; a block that the table does not have is not written;
  *     an entry with more full blocks than max_blocks counts as refused.
  *     Tokens outside [cu_seqlens[0], cu_seqlens[N]) belong to no sequence;
@@ -182,7 +183,9 @@ gdn_status gdn_attn_release(const gdn_attn_pool* pool, int32_t num_seqs, const i
 
 /* Bytes of workspace (host only; 0 for an invalid shape or op, or where the
  * op needs none).  num_blocks is the cache's; norm_rope_bwd reads only the
- * shape and total_tokens. */
+ * shape and total_tokens.  Decode has a record for every 512 tokens that the
+ * pool can hold, 6 % of one layer's cache with 16 query heads to a key head;
+ * one workspace serves all layers. */
 size_t gdn_attn_workspace_size(const gdn_attn_shape* shape, int32_t op, int64_t total_tokens,
                                int32_t num_seqs, int32_t num_blocks);
 
@@ -231,6 +234,8 @@ gdn_status gdn_attn_qk_norm_rope_bwd(const gdn_attn_shape* shape, const gdn_attn
  *   max_new   an upper bound of any sequence's new tokens (0: T); it chooses
  *             between kernels and changes no bits
  *   scale     positive and finite
+ * Sums are fp32, of p v with p up to 2^8: where a weighted sum of |v| passes
+ * 2^119 or so, o may be infinite though the exact mean is not.
  */
 gdn_status gdn_attn_prefill(const gdn_attn_shape* shape, int32_t num_seqs, int64_t total_tokens, int32_t max_new,
                             const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,

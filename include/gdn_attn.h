@@ -47,11 +47,11 @@
  *   - Device data (lengths, tables, positions) is the caller's to get right;
  *     the kernels keep their accesses inside the arrays where it is not:
  *     cu_seqlens are held to 0 .. T (the plan counts blocks by the lengths as
- *     they are, and holds what it writes per token), block ids to the pool, positions to the
- *     rotation table; a block that the table does not have is not written;
- *     an entry with more full blocks than max_blocks counts as refused.
- *     Tokens outside [cu_seqlens[0], cu_seqlens[N]) belong to no sequence;
- *     nothing is read or written for them.
+ *     they are, and holds what it writes per token), block ids to the pool,
+ *     positions to the rotation table; a block that the table does not have
+ *     is not written; an entry with more full blocks than max_blocks counts
+ *     as refused.  Tokens outside [cu_seqlens[0], cu_seqlens[N]) belong to no
+ *     sequence; nothing is read or written for them.
  */
 #ifndef GDN_ATTN_H
 #define GDN_ATTN_H

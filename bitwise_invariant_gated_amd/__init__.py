@@ -1,8 +1,9 @@
 """CPR Gated DeltaNet layer for MI355X (gfx950): HIP kernels behind a C ABI.
 
 The C ABI lives in include/gdn_cpr.h, that of the softmax-attention layer
-beside it in include/gdn_attn.h; this package holds the sources (csrc/), the
-build script and thin ctypes bindings (api, attn_api).
+beside it in include/gdn_attn.h, and that of what a stack of both needs around
+its layers in include/gdn_stack.h; this package holds the sources (csrc/), the
+build script and thin ctypes bindings (api, attn_api, stack_api).
 """
 
 from .api import (  # noqa: F401
@@ -44,6 +45,20 @@ from .attn_api import (  # noqa: F401
     gdn_attn_qk_norm_rope_bwd,
     gdn_attn_release,
     gdn_attn_workspace_size,
+)
+from .stack_api import (  # noqa: F401
+    LogitsShape,
+    NormShape,
+    alloc_logits_workspace,
+    alloc_norm_workspace,
+    gdn_stack_add_norm,
+    gdn_stack_add_norm_bwd,
+    gdn_stack_distill,
+    gdn_stack_distill_bwd,
+    gdn_stack_logits_workspace_size,
+    gdn_stack_logprobs,
+    gdn_stack_logprobs_bwd,
+    gdn_stack_norm_workspace_size,
 )
 from ._lib import (  # noqa: F401
     GDN_ATTN_BLOCK,

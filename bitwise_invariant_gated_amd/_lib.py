@@ -1,4 +1,4 @@
-"""ctypes declarations of the C ABI in include/gdn_cpr.h and include/gdn_attn.h.
+"""ctypes declarations of the C ABI in include/gdn_cpr.h, include/gdn_attn.h and include/gdn_stack.h.
 
 Loading fails loudly (RuntimeError) when the shared library has not been
 built: there is no fallback implementation anywhere in this package.
@@ -67,6 +67,18 @@ ATTN_EXPORTED = (
     "gdn_attn_cache_read",
 )
 
+# every symbol gdn_stack.h declares
+STACK_EXPORTED = (
+    "gdn_stack_add_norm",
+    "gdn_stack_add_norm_bwd",
+    "gdn_stack_norm_workspace_size",
+    "gdn_stack_logprobs",
+    "gdn_stack_logprobs_bwd",
+    "gdn_stack_distill",
+    "gdn_stack_distill_bwd",
+    "gdn_stack_logits_workspace_size",
+)
+
 
 class Shape(ctypes.Structure):
     _fields_ = [
@@ -118,6 +130,15 @@ class AttnRopeC(ctypes.Structure):
                 + [("eps", ctypes.c_float)])
 
 
+class NormShapeC(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("width", "dtype", "residual_dtype", "group", "zero_centered")]
+                + [("eps", ctypes.c_float)])
+
+
+class LogitsShapeC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("vocab", "dtype", "top", "teacher_logprobs")]
+
+
 _vp = ctypes.c_void_p
 _lib = None
 
@@ -141,6 +162,25 @@ def _declare_attn(lib: ctypes.CDLL) -> None:
         getattr(lib, name).argtypes = types
     lib.gdn_attn_workspace_size.restype = size
     lib.gdn_attn_workspace_size.argtypes = [shape, i32, i64, i32, i32]
+
+
+def _declare_stack(lib: ctypes.CDLL) -> None:
+    i64, size = ctypes.c_int64, ctypes.c_size_t
+    norm, logits = ctypes.POINTER(NormShapeC), ctypes.POINTER(LogitsShapeC)
+    args = {
+        "gdn_stack_add_norm": [norm, i64, _vp, i64, _vp, i64, _vp, _vp, i64, _vp, i64, _vp, _vp, _vp],
+        "gdn_stack_add_norm_bwd": [norm, i64, _vp, i64, _vp, _vp, i64, _vp, i64, _vp, i64, _vp, i64, _vp, _vp, size, _vp],
+        "gdn_stack_logprobs": [logits, i64, _vp, i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, size, _vp],
+        "gdn_stack_logprobs_bwd": [logits, i64, _vp, i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, i64, _vp],
+        "gdn_stack_distill": [logits, i64, _vp, i64, _vp, _vp, _vp, _vp, _vp, _vp, size, _vp],
+        "gdn_stack_distill_bwd": [logits, i64, _vp, i64, _vp, _vp, _vp, _vp, _vp, _vp, i64, _vp],
+    }
+    for name, types in args.items():
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = types
+    for name, shape in (("gdn_stack_norm_workspace_size", norm), ("gdn_stack_logits_workspace_size", logits)):
+        getattr(lib, name).restype = size
+        getattr(lib, name).argtypes = [shape, i64]
 
 
 def load() -> ctypes.CDLL:
@@ -198,6 +238,7 @@ def load() -> ctypes.CDLL:
     lib.gdn_cpr_numerics_id.restype = ctypes.c_char_p
     lib.gdn_cpr_numerics_id.argtypes = []
     _declare_attn(lib)
+    _declare_stack(lib)
     _lib = lib
     return lib
 

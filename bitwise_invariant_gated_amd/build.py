@@ -15,7 +15,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", n) for n in ("gdn_cpr.hip", "gdn_attn.hip")]
+SRCS = [os.path.join(HERE, "csrc", n) for n in ("gdn_cpr.hip", "gdn_attn.hip", "gdn_stack.hip")]
 OUT = os.path.join(HERE, "libgdn_cpr.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -84,12 +84,12 @@ def check_dpp_hazards(asm_text: str) -> list:
     return bad
 
 
-# kernels on the bf16 hot paths (prefill, decode, continuation, fwd_bwd, and the
-# attention layer), by mangled-name fragment; register spills there cost a
+# kernels on the bf16 hot paths (prefill, decode, continuation, fwd_bwd, the
+# attention layer and what is around the layers), by mangled-name fragment; register spills there cost a
 # scratch set-up per launch and memory traffic per spill, so the build rejects them
 HOT_KERNELS = ("k_scanIN3cpr4Bf16", "k_chain_scan_bf16", "k_decodeIN3cpr4Bf16", "k_resync_bf16",
                "k_cont_headIN3cpr4Bf16", "k_chunk_local_prefill_bf16", "k_chain_prefill_bf16", "k_bwd_local_bf16",
-               "k_bwd_chain_bf16", "k_bwd_state_grads_bf16", "k_plan", "k_attn_")
+               "k_bwd_chain_bf16", "k_bwd_state_grads_bf16", "k_plan", "k_attn_", "k_stack_")
 
 # three of them fill the registers, and spill: up to this many.  k_attn_prefill
 # reloads one value beside the score MFMAs of a tile, and its fold at the end of a partition

@@ -1,0 +1,587 @@
+// From rows of logits: log probabilities, entropy, top alternatives, the
+// divergence from a teacher's entries, and their gradients.
+//
+// A row is cut into parts of 2,048 columns, a wave to a part.  A part's record
+// is its largest logit m, l = sum e^(c (s - m)) and a = sum (s - m) e^(c (s - m)),
+// c the row's scale; the records of a row are joined by one wave,
+//   M = max m,  f = e^(c (m - M)),  l' = sum l f,  a' = sum (a + l (m - M)) f,
+// in an order that the row's length fixes.  Then log q = c (s - M) - log l' and
+// the entropy is log l' - c a' / l'.  A record needs no running maximum: the
+// wave holds its part in registers, so its maximum comes first.
+//
+// Top alternatives, by (logit, then lowest index): the parts also note the
+// largest logit of every 128 columns.  The k best columns lie in the k best
+// groups of 128 by (largest logit, lowest group): a column outside has k groups
+// that each hold a better one.  So the joining wave picks the k best parts, of
+// their groups the k best, and reads those again: k * 128 columns of a row.
+//
+// Bound by memory: the logits are read once (gradients: and written once).
+#pragma once
+
+#include "stack_device.hpp"
+
+namespace stack {
+
+constexpr int kPart = 2048;                     // columns of a record: 4 vectors of 8 to a lane
+constexpr int kVecs = kPart / 512;
+constexpr int kGroup = 128;                     // columns of a noted maximum
+constexpr int kGroups = kPart / kGroup;
+constexpr int kMaxParts = (1 << 20) / kPart;
+constexpr int kWaves = 4;                       // waves of a work-group
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct LogitsArgs {
+  const void* logits;
+  int64_t stride;
+  int64_t rows;
+  int vocab, parts, top;
+  const int32_t* targets;
+  const float* scale;
+  f32x4* rec;        // [rows][parts]: m, l, a
+  float* group_max;  // [rows][parts][kGroups]
+  float *logprobs, *entropy, *stats, *top_logprobs;
+  int32_t* top_ids;
+  // distill
+  const int32_t* ids;
+  const float* values;
+  int given_logprobs;
+  float* loss;
+  // gradients
+  const float *in_stats, *in_entropy, *d_logprobs, *d_entropy, *d_loss;
+  void* d_logits;
+  int64_t d_stride;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// a lane's columns of a part: vector j holds 512 j + 8 lane .. + 7
+template <class E>
+__device__ __forceinline__ void load_part(const typename E::T* p, int n, int lane, F8 (&x)[kVecs]) {
+  typename E::RAW raw[kVecs];
+  if (n >= kPart) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) raw[j] = E::template load<true>(p + j * 512 + lane * 8);
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) x[j] = E::wide(raw[j]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int c = j * 512 + lane * 8;
+    const float none = -__builtin_inff();
+    x[j] = F8{{none, none, none, none}, {none, none, none, none}};
+    if (c + 8 <= n) {
+      x[j] = E::wide(E::template load<true>(p + c));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < n) x[j][i] = E::one(p[c + i]);
+    }
+  }
+}
+
+__device__ __forceinline__ float max8(const F8& f) {
+  return max3(max3(f.a[0], f.a[1], f.a[2]), max3(f.a[3], f.b[0], f.b[1]), max3(f.b[2], f.b[3], f.b[3]));
+}
+
+// row and part of this wave; false past the last
+__device__ __forceinline__ bool my_part(const LogitsArgs& a, int64_t& row, int& part) {
+  const uint32_t w = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
+  row = w / (uint32_t)a.parts;
+  part = w - (uint32_t)row * a.parts;
+  return row < a.rows;
+}
+
+__device__ __forceinline__ bool left_out(const LogitsArgs& a, int64_t row) {
+  return a.targets && (uint32_t)a.targets[row] >= (uint32_t)a.vocab;
+}
+
+template <class E, bool ENTROPY, bool TOP>
+__global__ __launch_bounds__(64 * kWaves) void k_stack_parts(const LogitsArgs a) {
+  int64_t row;
+  int part;
+  if (!my_part(a, row, part) || left_out(a, row)) return;
+  const int lane = threadIdx.x & 63;
+  const float c = (a.scale ? a.scale[row] : 1.f) * kLog2e;
+  F8 x[kVecs];
+  load_part<E>((const typename E::T*)a.logits + row * a.stride + part * kPart, a.vocab - part * kPart, lane, x);
+  float m8[kVecs];
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) m8[j] = max8(x[j]);
+  float m;
+  if constexpr (TOP) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      m8[j] = max_16(m8[j]);
+      if ((lane & 15) == 0) a.group_max[(row * a.parts + part) * kGroups + j * 4 + (lane >> 4)] = m8[j];
+    }
+    m = max_groups(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])));
+  } else {
+    m = max_groups(max_16(max3(max3(m8[0], m8[1], m8[2]), m8[3], m8[3])));
+  }
+  const float ref = m == -__builtin_inff() ? 0.f : m;
+  float l[kVecs], s[kVecs];
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    l[j] = s[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = x[j][i] - ref;
+      const float e = exp2_fast(d * c);
+      l[j] += e;
+      // a masked column counts 0 * finite, not 0 * -inf
+      if constexpr (ENTROPY) s[j] = __builtin_fmaf(e, fmaxf(d, -0x1p100f), s[j]);
+    }
+  }
+  const float lt = sum_lanes<64>((l[0] + l[1]) + (l[2] + l[3]));
+  const float st = ENTROPY ? sum_lanes<64>((s[0] + s[1]) + (s[2] + s[3])) : 0.f;
+  if (lane == 0) a.rec[row * a.parts + part] = f32x4{m, lt, st, 0.f};
+}
+
+// What a row's records add up to.
+struct RowSum {
+  float m, l, a;   // largest logit, sum of exponentials, and with weights s - m
+  float log_l;     // 0 in a row of -inf only
+  bool none;       // such a row
+};
+
+struct RowRecords {
+  f32x4 r[kMaxParts / 64];
+};
+
+__device__ __forceinline__ RowSum join_records(const LogitsArgs& a, int64_t row, float c, int lane, RowRecords& q) {
+  const f32x4* rec = a.rec + row * a.parts;
+  float m = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < kMaxParts / 64; ++i) {
+    q.r[i] = f32x4{-__builtin_inff(), 0.f, 0.f, 0.f};
+    if (i * 64 + lane < a.parts) q.r[i] = rec[i * 64 + lane];
+  }
+#pragma unroll
+  for (int i = 0; i < kMaxParts / 64; ++i) m = fmaxf(m, q.r[i][0]);
+  m = max_groups(max_16(m));
+  float l = 0.f, s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxParts / 64; ++i) {
+    if (i * 64 >= a.parts) break;
+    if (q.r[i][1] != 0.f) {  // a part of masked columns only has nothing to add
+      const float d = q.r[i][0] - m, f = exp2_fast(d * c);
+      l = __builtin_fmaf(q.r[i][1], f, l);
+      s = __builtin_fmaf(__builtin_fmaf(q.r[i][1], fmaxf(d, -0x1p100f), q.r[i][2]), f, s);
+    }
+  }
+  RowSum t;
+  t.m = m;
+  t.l = sum_lanes<64>(l);
+  t.a = sum_lanes<64>(s);
+  t.none = t.l == 0.f;
+  t.log_l = t.none ? 0.f : logf(t.l);
+  return t;
+}
+
+// log q of a logit
+__device__ __forceinline__ float log_q(const RowSum& t, float scale, float x) {
+  return t.none ? -__builtin_inff() : __builtin_fmaf(x - t.m, scale, -t.log_l);
+}
+
+// A float's place in ascending order as a whole number; -0 is 0, a NaN is -inf.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  x = x != x ? -__builtin_inff() : x + 0.f;
+  const uint32_t u = __float_as_uint(x);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float of_order(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// The wave's LDS writes before this are seen by its reads after it.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Of the n <= 64 * N keys (key i * 64 + lane in k[i], 0 past the end, where all
+// real ones are larger) the `want` <= n largest, equal ones by ascending index:
+// their indices go to `list` in ascending order.  Returns the least of their
+// keys.  The least is found bit by bit, from counts.
+template <int N>
+__device__ __forceinline__ uint32_t select_largest(const uint32_t (&k)[N], int n, int want, int lane, int* list) {
+  const int used = (n + 63) / 64;
+  uint32_t least = 0;
+  for (int b = 31; b >= 0; --b) {
+    const uint32_t t = least | 1u << b;
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < used) count += __builtin_popcountll(__ballot(k[i] >= t));
+    if (count >= want) least = t;
+  }
+  int above = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < used) above += __builtin_popcountll(__ballot(k[i] > least));
+  int equal = want - above, at = 0;  // how many of the equal ones are taken
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i >= used) continue;
+    const uint64_t eq = __ballot(k[i] == least);
+    const bool take = k[i] > least || (k[i] == least && lanes_below(eq) < equal);
+    const uint64_t taken = __ballot(take);
+    if (take) list[at + lanes_below(taken)] = i * 64 + lane;
+    at += __builtin_popcountll(taken);
+    equal = max(0, equal - (int)__builtin_popcountll(eq));
+  }
+  return least;
+}
+
+constexpr int kFound = 256;  // columns held while the best are sought
+
+struct TopScratch {
+  uint64_t found[kFound];
+  int parts[64], groups[64];
+};
+
+// Keeps the `want` largest of the `count` different values found, in order.
+__device__ __forceinline__ int keep_largest(uint64_t* found, int count, int want, int lane) {
+  uint64_t v[kFound / 64];
+  int rank[kFound / 64];
+  const int used = (count + 63) / 64;
+  wave_sync();
+#pragma unroll
+  for (int i = 0; i < kFound / 64; ++i) {
+    rank[i] = 0;
+    v[i] = i * 64 + lane < count ? found[i * 64 + lane] : 0;
+  }
+  for (int t = 0; t < count; ++t) {
+    const uint64_t o = found[t];
+#pragma unroll
+    for (int i = 0; i < kFound / 64; ++i)
+      if (i < used) rank[i] += o > v[i];
+  }
+  wave_sync();
+#pragma unroll
+  for (int i = 0; i < kFound / 64; ++i)
+    if (v[i] && rank[i] < want) found[rank[i]] = v[i];
+  wave_sync();
+  return min(count, want);
+}
+
+// The row's a.top best columns, in order, in found[]: order_of(logit) above the
+// index's complement.  A column holds no 0 there, as order_of(-inf) is not 0.
+template <class E>
+__device__ __forceinline__ void top_columns(const LogitsArgs& a, int64_t row, int lane, const RowRecords& q, TopScratch& t) {
+  // parts
+  uint32_t pk[kMaxParts / 64];
+#pragma unroll
+  for (int i = 0; i < kMaxParts / 64; ++i) pk[i] = i * 64 + lane < a.parts ? order_of(q.r[i][0]) : 0;
+  const int np = min(a.top, a.parts);
+  select_largest<kMaxParts / 64>(pk, a.parts, np, lane, t.parts);
+  wave_sync();
+  // their groups of 128 columns
+  constexpr int G = 64 * kGroups / 64;
+  uint32_t gk[G];
+  const float* gm = a.group_max + row * a.parts * kGroups;
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const int at = i * 64 + lane;
+    gk[i] = 0;
+    if (i * 4 < np && at < np * kGroups) {
+      const int g = t.parts[at / kGroups] * kGroups + at % kGroups;
+      if (g * kGroup < a.vocab) gk[i] = order_of(gm[g]);
+    }
+  }
+  const int all = (a.vocab + kGroup - 1) / kGroup, ng = min(a.top, all);
+  const uint32_t least = select_largest<G>(gk, np * kGroups, ng, lane, t.groups);
+  wave_sync();
+  // and their columns: at least as many as asked for reach the least of as many groups
+  uint64_t bar = ng == a.top ? (uint64_t)least << 32 : 0;
+  int count = 0;
+  const typename E::T* x = (const typename E::T*)a.logits + row * a.stride;
+  for (int s = 0; s < ng; s += 4) {
+    const int which = s + (lane >> 4);
+    int c = a.vocab;
+    if (which < ng) {
+      const int at = t.groups[which];
+      c = (t.parts[at / kGroups] * kGroups + at % kGroups) * kGroup + (lane & 15) * 8;
+    }
+    F8 f;
+    if (c + 8 <= a.vocab) {
+      f = E::wide(E::template load<true>(x + c));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = c + i < a.vocab ? E::one(x[c + i]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t v = (uint64_t)order_of(f[i]) << 32 | (uint32_t)~(c + i);
+      const bool take = c + i < a.vocab && v > bar;
+      const uint64_t taken = __ballot(take);
+      if (taken == 0) continue;
+      if (take) t.found[count + lanes_below(taken)] = v;
+      count += __builtin_popcountll(taken);
+      if (count > kFound - 64) {
+        count = keep_largest(t.found, count, a.top, lane);
+        if (count == a.top) bar = t.found[count - 1];
+      }
+    }
+  }
+  keep_largest(t.found, count, a.top, lane);
+}
+
+template <class E, bool TOP>
+__global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs(const LogitsArgs a) {
+  __shared__ TopScratch scratch[TOP ? kWaves : 1];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * kWaves + wave;
+  if (row >= a.rows) return;
+  if (left_out(a, row)) {
+    if (lane == 0) {
+      a.logprobs[row] = 0.f;
+      if (a.entropy) a.entropy[row] = 0.f;
+      if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.f;
+    }
+    if (TOP && lane < a.top) {
+      a.top_ids[row * a.top + lane] = -1;
+      a.top_logprobs[row * a.top + lane] = 0.f;
+    }
+    return;
+  }
+  const float scale = a.scale ? a.scale[row] : 1.f;
+  const typename E::T* x = (const typename E::T*)a.logits + row * a.stride;
+  const float at_target = a.targets ? E::one(x[a.targets[row]]) : 0.f;
+  RowRecords q;
+  const RowSum t = join_records(a, row, scale * kLog2e, lane, q);
+  if (lane == 0) {
+    if (a.targets) a.logprobs[row] = log_q(t, scale, at_target);
+    if (a.entropy) a.entropy[row] = t.none ? 0.f : t.log_l - scale * (t.a / t.l);
+    if (a.stats) {
+      a.stats[2 * row] = t.m;
+      a.stats[2 * row + 1] = t.log_l;
+    }
+  }
+  if constexpr (TOP) {
+    TopScratch& s = scratch[wave];
+    top_columns<E>(a, row, lane, q, s);
+    if (lane < a.top) {
+      const uint64_t v = s.found[lane];
+      a.top_ids[row * a.top + lane] = (int32_t)~(uint32_t)v;
+      a.top_logprobs[row * a.top + lane] = log_q(t, scale, of_order((uint32_t)(v >> 32)));
+    }
+  }
+}
+
+// Gradient of log probability and entropy: a wave to a part, as above.
+template <class E, bool ENTROPY>
+__global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs_bwd(const LogitsArgs a) {
+  int64_t row;
+  int part;
+  if (!my_part(a, row, part)) return;
+  const int lane = threadIdx.x & 63, n = a.vocab - part * kPart;
+  typename E::T* out = (typename E::T*)a.d_logits + row * a.d_stride + part * kPart;
+  const float m = a.in_stats[2 * row], log_l = a.in_stats[2 * row + 1];
+  const bool zero = left_out(a, row) || (m == -__builtin_inff() && log_l == 0.f);
+  const float scale = a.scale ? a.scale[row] : 1.f;
+  const float g = a.d_logprobs ? a.d_logprobs[row] * scale : 0.f;
+  const float f = ENTROPY ? a.d_entropy[row] * scale : 0.f, h = ENTROPY ? a.in_entropy[row] : 0.f;
+  F8 x[kVecs];
+  if (zero) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) x[j] = F8{{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  } else {
+    load_part<E>((const typename E::T*)a.logits + row * a.stride + part * kPart, n, lane, x);
+    const float c = scale * kLog2e, off = -log_l * kLog2e, up = h - log_l;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = x[j][i] - m;
+        const float p = exp2_fast(__builtin_fmaf(d, c, off));
+        float k = g;
+        // of a masked column: q is 0, and log q is held to what is finite
+        if constexpr (ENTROPY) k = __builtin_fmaf(f, fmaxf(__builtin_fmaf(d, scale, up), -0x1p100f), g);
+        x[j][i] = -p * k;
+      }
+    }
+    if (a.targets && a.d_logprobs) {
+      const int at = a.targets[row] - part * kPart;
+      if (at >= 0 && at < kPart) {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+          if (at / 512 == j && (at % 512) / 8 == lane) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[j][i] += at % 8 == i ? g : 0.f;
+          }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int col = j * 512 + lane * 8;
+    if (col + 8 <= n) {
+      E::template store<true, false>(out + col, E::narrow(x[j]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (col + i < n) out[col + i] = E::round(x[j][i]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// distillation
+
+constexpr int kEntries = 256 / 64;  // teacher's entries to a lane
+
+struct Teacher {
+  int id[kEntries];       // -1: not there
+  float logp[kEntries];   // -inf: not there
+};
+
+__device__ __forceinline__ void load_teacher(const LogitsArgs& a, int64_t row, int lane, Teacher& t) {
+#pragma unroll
+  for (int i = 0; i < kEntries; ++i) {
+    const int e = i * 64 + lane;
+    t.id[i] = -1;
+    t.logp[i] = -__builtin_inff();
+    if (e < a.top) {
+      const int id = a.ids[row * a.top + e];
+      if ((uint32_t)id < (uint32_t)a.vocab) {
+        t.id[i] = id;
+        t.logp[i] = a.values[row * a.top + e];
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void normalise(Teacher& t, float scale, float m, float log_l) {
+#pragma unroll
+  for (int i = 0; i < kEntries; ++i) t.logp[i] = __builtin_fmaf(t.logp[i] - m, scale, -log_l);
+}
+
+template <class E>
+__global__ __launch_bounds__(64 * kWaves) void k_stack_distill(const LogitsArgs a) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * kWaves + wave;
+  if (row >= a.rows) return;
+  const float scale = a.scale ? a.scale[row] : 1.f;
+  const typename E::T* x = (const typename E::T*)a.logits + row * a.stride;
+  Teacher te;
+  load_teacher(a, row, lane, te);
+  float s[kEntries];
+#pragma unroll
+  for (int i = 0; i < kEntries; ++i) s[i] = te.id[i] >= 0 ? E::one(x[te.id[i]]) : 0.f;
+  RowRecords q;
+  const RowSum t = join_records(a, row, scale * kLog2e, lane, q);
+  float m = 0.f, log_l = 0.f;
+  if (!a.given_logprobs) {
+    m = te.logp[0];
+#pragma unroll
+    for (int i = 1; i < kEntries; ++i) m = fmaxf(m, te.logp[i]);
+    m = max_groups(max_16(m));
+    if (m == -__builtin_inff()) m = 0.f;
+    float l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kEntries; ++i) l += expf((te.logp[i] - m) * scale);
+    l = sum_lanes<64>(l);
+    log_l = l == 0.f ? 0.f : logf(l);
+    normalise(te, scale, m, log_l);
+  }
+  float loss = 0.f;
+#pragma unroll
+  for (int i = 0; i < kEntries; ++i) {
+    const float p = expf(te.logp[i]);
+    if (p != 0.f) loss = __builtin_fmaf(p, te.logp[i] - log_q(t, scale, s[i]), loss);
+  }
+  loss = sum_lanes<64>(loss);
+  if (lane == 0) {
+    a.loss[row] = loss;
+    if (a.stats) *(f32x4*)(a.stats + 4 * row) = f32x4{t.m, t.log_l, m, log_l};
+  }
+}
+
+// Gradient.  Every column is first stored as if it were no entry; the wave then
+// writes over those that are.
+template <class E>
+__global__ __launch_bounds__(64 * kWaves) void k_stack_distill_bwd(const LogitsArgs a) {
+  int64_t row;
+  int part;
+  if (!my_part(a, row, part)) return;
+  const int lane = threadIdx.x & 63, n = a.vocab - part * kPart;
+  const typename E::T* in = (const typename E::T*)a.logits + row * a.stride + part * kPart;
+  typename E::T* out = (typename E::T*)a.d_logits + row * a.d_stride + part * kPart;
+  const f32x4 st = *(const f32x4*)(a.in_stats + 4 * row);
+  const float m = st[0], log_l = st[1];
+  const float scale = a.scale ? a.scale[row] : 1.f, g = a.d_loss[row] * scale;
+  F8 x[kVecs];
+  load_part<E>(in, n, lane, x);
+  Teacher te;
+  load_teacher(a, row, lane, te);
+  if (!a.given_logprobs) normalise(te, scale, st[2], st[3]);
+  float p[kEntries], s[kEntries], total = 0.f;
+  uint64_t here[kEntries], any = 0;
+#pragma unroll
+  for (int i = 0; i < kEntries; ++i) {
+    p[i] = expf(te.logp[i]);
+    total += p[i];
+    te.id[i] -= part * kPart;
+    const bool mine = te.id[i] >= 0 && te.id[i] < kPart;
+    here[i] = __ballot(mine);
+    any |= here[i];
+    s[i] = mine ? E::one(in[te.id[i]]) : 0.f;
+  }
+  total = sum_lanes<64>(total);
+  const bool zero = total == 0.f || (m == -__builtin_inff() && log_l == 0.f);
+  const float c = scale * kLog2e, off = -log_l * kLog2e, k = g * total;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[j][i] = zero ? 0.f : exp2_fast(__builtin_fmaf(x[j][i] - m, c, off)) * k;
+    const int col = j * 512 + lane * 8;
+    if (col + 8 <= n) {
+      E::template store<true, false>(out + col, E::narrow(x[j]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (col + i < n) out[col + i] = E::round(x[j][i]);
+    }
+  }
+  if (any == 0 || zero) return;
+  // the part's entries, one index at a time: its first entry takes the sum of all of its p
+  float sum[kEntries];
+  bool first[kEntries];
+#pragma unroll
+  for (int i = 0; i < kEntries; ++i) {
+    sum[i] = 0.f;
+    first[i] = false;
+  }
+#pragma unroll
+  for (int i = 0; i < kEntries; ++i) {
+    while (here[i]) {
+      const int who = __builtin_ctzll(here[i]);
+      const int id = __builtin_amdgcn_readlane(te.id[i], who);
+      float t = 0.f;
+#pragma unroll
+      for (int j = i; j < kEntries; ++j) {
+        uint64_t same = __ballot(te.id[j] == id);
+        here[j] &= ~same;
+        for (; same; same &= same - 1)
+          t += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p[j]), __builtin_ctzll(same)));
+      }
+      if (lane == who) {
+        sum[i] = t;
+        first[i] = true;
+      }
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the stores above are done
+#pragma unroll
+  for (int i = 0; i < kEntries; ++i)
+    if (first[i]) out[te.id[i]] = E::round(g * (exp2_fast(__builtin_fmaf(s[i] - m, c, off)) * total - sum[i]));
+}
+
+}  // namespace stack

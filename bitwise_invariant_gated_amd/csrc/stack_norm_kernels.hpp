@@ -1,0 +1,271 @@
+// The residual's addition with the root-mean-square norm, and its gradient.
+//
+// h = x + residual, rounded as it is stored; r = 1 / sqrt(sum(h^2) / width + eps);
+// n = h r w.  Gradient: dn = dy w, dh = d_residual_out + r (dn - h (r^2 / width)
+// sum(dn h)), dw = sum over rows of dy h r: two sums over the row, sum(h^2) and
+// sum(dn h), in one pass.
+//
+// Bound by memory: a row is read once, kept in registers and written once.
+#pragma once
+
+#include "stack_device.hpp"
+
+namespace stack {
+
+struct NormArgs {
+  const void *x, *res, *dy;  // gradient: x is h, res is d_residual_out
+  const float* w;
+  void *h, *y;               // gradient: d_residual, dx
+  uint8_t* y8;
+  float* y_scale;
+  int64_t x_stride, res_stride, dy_stride, h_stride, y_stride;
+  int64_t rows;
+  int width, group;
+  float eps, w_add;
+  float* partial;            // gradient: [work-group][width]
+};
+
+constexpr int kNormThreads = 256;
+
+// Sum over the LANES threads of a row; `red`: 4 floats of LDS that no thread
+// still reads from an earlier call.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float x, float* red) {
+  if constexpr (LANES <= 64) {
+    return sum_lanes<LANES>(x);
+  } else {
+    x = sum_lanes<64>(x);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
+  }
+}
+
+// two sums at once; red: 8 floats
+template <int LANES>
+__device__ __forceinline__ void row_sums(float& x, float& y, float* red) {
+  if constexpr (LANES <= 64) {
+    x = sum_lanes<LANES>(x);
+    y = sum_lanes<LANES>(y);
+  } else {
+    x = sum_lanes<64>(x);
+    y = sum_lanes<64>(y);
+    if ((threadIdx.x & 63) == 0) {
+      red[threadIdx.x >> 6] = x;
+      red[4 + (threadIdx.x >> 6)] = y;
+    }
+    __syncthreads();
+    x = (red[0] + red[1]) + (red[2] + red[3]);
+    y = (red[4] + red[5]) + (red[6] + red[7]);
+  }
+}
+
+template <int LANES>
+__device__ __forceinline__ float row_max(float x, float* red) {
+  x = max_16(x);
+  if constexpr (LANES > 16) x = max_groups(x);
+  if constexpr (LANES > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  }
+  return x;
+}
+
+__device__ __forceinline__ float dot4(f32x4 a, f32x4 b, float s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s = __builtin_fmaf(a[i], b[i], s);
+  return s;
+}
+
+__device__ __forceinline__ float amax8(const F8& f) {
+  float m = max3(__builtin_fabsf(f.a[0]), __builtin_fabsf(f.a[1]), __builtin_fabsf(f.a[2]));
+  m = max3(m, __builtin_fabsf(f.a[3]), __builtin_fabsf(f.b[0]));
+  m = max3(m, __builtin_fabsf(f.b[1]), __builtin_fabsf(f.b[2]));
+  return fmaxf(m, __builtin_fabsf(f.b[3]));
+}
+
+__device__ __forceinline__ u32x2 to_e4m3(const F8& f, float s) {
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f.a[0] * s, f.a[1] * s, 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(f.a[2] * s, f.a[3] * s, lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(f.b[0] * s, f.b[1] * s, 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(f.b[2] * s, f.b[3] * s, hi, true);
+  return u32x2{(uint32_t)lo, (uint32_t)hi};
+}
+
+// A row to LANES threads, NV vectors of eight columns to a thread, the vectors
+// LANES * 8 columns apart.
+template <class X, class R, int LANES, int NV>
+__global__ __launch_bounds__(kNormThreads) void k_stack_add_norm(const NormArgs a) {
+  __shared__ float red[8];
+  const int l = threadIdx.x % LANES;
+  const int64_t row = (int64_t)blockIdx.x * (kNormThreads / LANES) + threadIdx.x / LANES;
+  if (row >= a.rows) return;  // with LANES = 256 there is none
+  const typename X::T* x = (const typename X::T*)a.x + row * a.x_stride;
+  const typename R::T* res = (const typename R::T*)a.res + row * a.res_stride;
+  typename R::T* h_out = (typename R::T*)a.h + row * a.h_stride;
+  F8 h[NV];
+  typename X::RAW xr[NV];
+  typename R::RAW rr[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * LANES + l) * 8;
+    if (c < a.width) {
+      xr[j] = X::template load<false>(x + c);
+      if (a.res) rr[j] = R::template load<false>(res + c);
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * LANES + l) * 8;
+    h[j] = F8{{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    if (c < a.width) {
+      h[j] = X::wide(xr[j]);
+      if (a.res) {
+        const F8 f = R::wide(rr[j]);
+        h[j].a += f.a;
+        h[j].b += f.b;
+      }
+      const typename R::RAW n = R::narrow(h[j]);
+      h[j] = R::wide(n);
+      if (a.h) R::template store<false, false>(h_out + c, n);
+      ss = dot4(h[j].b, h[j].b, dot4(h[j].a, h[j].a, ss));
+    }
+  }
+  ss = row_sum<LANES>(ss, red);
+  const float r = 1.f / __builtin_sqrtf(ss * (1.f / (float)a.width) + a.eps);
+  float most = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * LANES + l) * 8;
+    if (c >= a.width) continue;
+    const f32x4 w1 = *(const f32x4*)(a.w + c) + a.w_add, w2 = *(const f32x4*)(a.w + c + 4) + a.w_add;
+    h[j].a = h[j].a * r * w1;
+    h[j].b = h[j].b * r * w2;
+    if (a.y) X::template store<false, false>((typename X::T*)a.y + row * a.y_stride + c, X::narrow(h[j]));
+    if (a.y8 && a.group == 0) most = fmaxf(most, amax8(h[j]));
+  }
+  if (!a.y8) return;
+  const float least = 0x1p-100f;
+  if (a.group == 0) {
+    most = fmaxf(row_max<LANES>(most, red + 4), least);
+    if (l == 0) a.y_scale[row] = most / 448.f;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * LANES + l) * 8;
+    if (c >= a.width) continue;  // sixteen lanes of a group together
+    if (a.group) {
+      most = fmaxf(max_16(amax8(h[j])), least);
+      if ((l & 15) == 0) a.y_scale[row * (a.width / 128) + c / 128] = most / 448.f;
+    }
+    *(u32x2*)(a.y8 + row * a.width + c) = to_e4m3(h[j], 448.f / most);
+  }
+}
+
+// Gradient.  Work-groups go over the rows in steps of the grid; a thread keeps
+// dw of its columns in registers for all of its rows, so dw costs one partial
+// sum of a row's width per work-group.
+template <class X, class R, int LANES, int NV>
+__global__ __launch_bounds__(kNormThreads) void k_stack_add_norm_bwd(const NormArgs a) {
+  constexpr int G = kNormThreads / LANES;
+  __shared__ float red[2][8];
+  __shared__ f32x4 part[G > 1 ? 2 * kNormThreads : 1];
+  const int l = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+  F8 g[NV], w[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * LANES + l) * 8;
+    g[j] = F8{{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    w[j] = g[j];
+    if (c < a.width) w[j] = F8{*(const f32x4*)(a.w + c) + a.w_add, *(const f32x4*)(a.w + c + 4) + a.w_add};
+  }
+  const float inv = 1.f / (float)a.width;
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * G + sub; row < a.rows; row += (int64_t)gridDim.x * G, turn ^= 1) {
+    const typename R::T* hp = (const typename R::T*)a.x + row * a.x_stride;
+    const typename X::T* yp = (const typename X::T*)a.dy + row * a.dy_stride;
+    const typename R::T* dp = (const typename R::T*)a.res + row * a.res_stride;
+    typename R::RAW hr[NV], dr[NV];
+    typename X::RAW yr[NV];
+    float ss = 0.f, hx = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * LANES + l) * 8;
+      if (c < a.width) {
+        hr[j] = R::template load<false>(hp + c);
+        yr[j] = X::template load<false>(yp + c);
+        if (a.res) dr[j] = R::template load<false>(dp + c);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if ((j * LANES + l) * 8 >= a.width) continue;
+      const F8 h = R::wide(hr[j]), y = X::wide(yr[j]);
+      ss = dot4(h.b, h.b, dot4(h.a, h.a, ss));
+      hx = dot4(y.b * w[j].b, h.b, dot4(y.a * w[j].a, h.a, hx));
+    }
+    row_sums<LANES>(ss, hx, red[turn]);
+    const float r = 1.f / __builtin_sqrtf(ss * inv + a.eps);
+    const float m = hx * r * r * inv;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * LANES + l) * 8;
+      if (c >= a.width) continue;
+      const F8 h = R::wide(hr[j]), y = X::wide(yr[j]);
+      F8 d = {r * (y.a * w[j].a - h.a * m), r * (y.b * w[j].b - h.b * m)};
+      g[j].a += y.a * (h.a * r);
+      g[j].b += y.b * (h.b * r);
+      if (a.res) {
+        const F8 f = R::wide(dr[j]);
+        d.a += f.a;
+        d.b += f.b;
+      }
+      if (a.y) X::template store<false, false>((typename X::T*)a.y + row * a.y_stride + c, X::narrow(d));
+      if (a.h) R::template store<false, false>((typename R::T*)a.h + row * a.h_stride + c, R::narrow(d));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * LANES + l) * 8;
+    if constexpr (G > 1) {  // the work-group's rows, one after the other
+      __syncthreads();
+      part[threadIdx.x] = g[j].a;
+      part[kNormThreads + threadIdx.x] = g[j].b;
+      __syncthreads();
+      if (sub == 0) {
+#pragma unroll
+        for (int i = 1; i < G; ++i) {
+          g[j].a += part[i * LANES + l];
+          g[j].b += part[kNormThreads + i * LANES + l];
+        }
+      }
+    }
+    if (sub == 0 && c < a.width) {
+      float* to = a.partial + (int64_t)blockIdx.x * a.width + c;
+      *(f32x4*)to = g[j].a;
+      *(f32x4*)(to + 4) = g[j].b;
+    }
+  }
+}
+
+// dw = the partial sums added up: 32 columns per work-group, 32 runs of
+// partials each, then the runs in order.
+__global__ __launch_bounds__(1024) void k_stack_norm_dw(const float* partial, int n, int width, float* dw) {
+  __shared__ float red[32][33];
+  const int col = threadIdx.x & 31, run = threadIdx.x >> 5, at = blockIdx.x * 32 + col;
+  float t = 0.f;
+  if (at < width) {
+#pragma unroll 8
+    for (int i = run; i < n; i += 32) t += partial[(int64_t)i * width + at];
+  }
+  red[run][col] = t;
+  __syncthreads();
+  if (run == 0 && at < width) {
+    for (int i = 1; i < 32; ++i) t += red[i][col];
+    dw[at] = t;
+  }
+}
+
+}  // namespace stack

@@ -149,14 +149,17 @@ struct RowRecords {
   f32x4 r[kMaxParts / 64];
 };
 
-__device__ __forceinline__ RowSum join_records(const LogitsArgs& a, int64_t row, float c, int lane, RowRecords& q) {
+__device__ __forceinline__ void load_records(const LogitsArgs& a, int64_t row, int lane, RowRecords& q) {
   const f32x4* rec = a.rec + row * a.parts;
-  float m = -__builtin_inff();
 #pragma unroll
   for (int i = 0; i < kMaxParts / 64; ++i) {
     q.r[i] = f32x4{-__builtin_inff(), 0.f, 0.f, 0.f};
     if (i * 64 + lane < a.parts) q.r[i] = rec[i * 64 + lane];
   }
+}
+
+__device__ __forceinline__ RowSum join_records(const LogitsArgs& a, float c, const RowRecords& q) {
+  float m = -__builtin_inff();
 #pragma unroll
   for (int i = 0; i < kMaxParts / 64; ++i) m = fmaxf(m, q.r[i][0]);
   m = max_groups(max_16(m));
@@ -205,41 +208,77 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Of the n <= 64 * N keys (key i * 64 + lane in k[i], 0 past the end, where all
-// real ones are larger) the `want` <= n largest, equal ones by ascending index:
-// their indices go to `list` in ascending order.  Returns the least of their
-// keys.  The least is found bit by bit, from counts.
-template <int N>
-__device__ __forceinline__ uint32_t select_largest(const uint32_t (&k)[N], int n, int want, int lane, int* list) {
-  const int used = (n + 63) / 64;
-  uint32_t least = 0;
-  for (int b = 31; b >= 0; --b) {
-    const uint32_t t = least | 1u << b;
-    int count = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < used) count += __builtin_popcountll(__ballot(k[i] >= t));
-    if (count >= want) least = t;
-  }
-  int above = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (i < used) above += __builtin_popcountll(__ballot(k[i] > least));
-  int equal = want - above, at = 0;  // how many of the equal ones are taken
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (i >= used) continue;
-    const uint64_t eq = __ballot(k[i] == least);
-    const bool take = k[i] > least || (k[i] == least && lanes_below(eq) < equal);
-    const uint64_t taken = __ballot(take);
-    if (take) list[at + lanes_below(taken)] = i * 64 + lane;
-    at += __builtin_popcountll(taken);
-    equal = max(0, equal - (int)__builtin_popcountll(eq));
-  }
-  return least;
+// Sum over the lanes up to and with this one.
+__device__ __forceinline__ int sum_up_to(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);   // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);   // row_shr:2
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);   // row_shr:4
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);   // row_shr:8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast15: into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // row_bcast31: into rows 2 and 3
+  return x;
 }
 
-constexpr int kFound = 256;  // columns held while the best are sought
+// Of up to 64 * N values (value N * lane + i in x[i], NaN where there is none)
+// the `want` <= 64 largest, equal ones by ascending index: their indices go to
+// `list` in ascending order.  None is above `best`.  Returns the key, in units
+// of STEP, of a value that exactly they reach, or, where others are equal to
+// the least of them, of that.  It is found by halving an interval of keys and
+// counting, and the search ends once the count is right.  (Rolled up, as its
+// code is run once and has to be fetched first.)
+template <uint32_t STEP, int N>
+__device__ __forceinline__ uint32_t select_largest(const float (&x)[N], int want, float best, int lane, int* list) {
+  // the lower half of a bf16 value's order is its sign's
+  const auto value = [](uint32_t k) { return of_order(k * STEP + ((int32_t)(k * STEP) < 0 ? 0 : STEP - 1)); };
+  const auto reach = [&](float f) {
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) c += x[i] >= f;
+    return __builtin_amdgcn_readlane(sum_up_to(c), 63);
+  };
+  // as many values as lanes have any reach the least of the lanes' largest
+  float low = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) low = fmaxf(low, x[i]);
+  low = __builtin_popcountll(__ballot(low == low)) < want ? -__builtin_inff() : -max_groups(max_16(-low));
+  uint32_t lo = __builtin_amdgcn_readfirstlane(order_of(low) / STEP), hi = __builtin_amdgcn_readfirstlane(order_of(best) / STEP);
+  int count = reach(value(lo));
+#pragma unroll 1
+  while (lo < hi && count != want) {
+    const uint32_t t = lo + (hi - lo + 1) / 2;
+    const int c = reach(value(t));
+    if (c >= want) {
+      lo = t;
+      count = c;
+    } else {
+      hi = t - 1;
+    }
+  }
+  uint32_t take = 0;
+  const float f = value(lo);
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i) take = 2 * take + (x[i] >= f);
+  if (count != want) {  // of those equal to the least, the first
+    uint32_t above = 0;
+    const float g = value(lo + 1);
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i) above = 2 * above + (x[i] >= g);
+    const int over = __builtin_amdgcn_readlane(sum_up_to(__builtin_popcount(above)), 63);
+    uint32_t equal = take & ~above;
+    const int mine = __builtin_popcount(equal);
+    int room = want - over - (sum_up_to(mine) - mine);
+    take = above;
+#pragma unroll 1
+    for (; equal && room > 0; --room, equal &= equal - 1) take |= equal & -equal;
+  }
+  const int mine = __builtin_popcount(take);
+  int at = sum_up_to(mine) - mine;
+#pragma unroll 1
+  for (; take; take &= take - 1) list[at++] = N * lane + __builtin_ctz(take);
+  return lo;
+}
+
+constexpr int kFound = 1024;  // columns held while the best are sought
 
 struct TopScratch {
   uint64_t found[kFound];
@@ -248,20 +287,34 @@ struct TopScratch {
 
 // Keeps the `want` largest of the `count` different values found, in order.
 __device__ __forceinline__ int keep_largest(uint64_t* found, int count, int want, int lane) {
+  wave_sync();
+  if (count <= 64) {  // the usual case: hardly more than are wanted
+    const uint64_t v = lane < count ? found[lane] : 0;
+    int rank = 0;
+#pragma unroll 1
+    for (int t = 0; t < count; ++t) {
+      const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), t) << 32 |
+                         (uint32_t)__builtin_amdgcn_readlane((int)v, t);
+      rank += o > v;
+    }
+    wave_sync();
+    if (lane < count && rank < want) found[rank] = v;
+    wave_sync();
+    return min(count, want);
+  }
   uint64_t v[kFound / 64];
   int rank[kFound / 64];
-  const int used = (count + 63) / 64;
-  wave_sync();
 #pragma unroll
   for (int i = 0; i < kFound / 64; ++i) {
     rank[i] = 0;
     v[i] = i * 64 + lane < count ? found[i * 64 + lane] : 0;
   }
+#pragma unroll 4
   for (int t = 0; t < count; ++t) {
     const uint64_t o = found[t];
 #pragma unroll
     for (int i = 0; i < kFound / 64; ++i)
-      if (i < used) rank[i] += o > v[i];
+      if (i * 64 < count) rank[i] += o > v[i];
   }
   wave_sync();
 #pragma unroll
@@ -271,66 +324,111 @@ __device__ __forceinline__ int keep_largest(uint64_t* found, int count, int want
   return min(count, want);
 }
 
+constexpr int kHeld = 16;  // values of a lane among which the largest are sought
+
+// The noted maxima of a row of up to 64 parts, those of a part to a lane.
+__device__ __forceinline__ void load_groups(const LogitsArgs& a, int64_t row, int part, bool there, float (&x)[kHeld]) {
+  const f32x4* gm = (const f32x4*)(a.group_max + (row * a.parts + part) * kGroups);
+#pragma unroll
+  for (int i = 0; i < kHeld / 4; ++i) {
+    const float none = __uint_as_float(0x7fc00000u);
+    f32x4 v = {none, none, none, none};
+    if (there) v = gm[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x[4 * i + e] = there && part * kPart + (4 * i + e) * kGroup < a.vocab ? fmaxf(v[e], -__builtin_inff()) : none;
+  }
+}
+
 // The row's a.top best columns, in order, in found[]: order_of(logit) above the
-// index's complement.  A column holds no 0 there, as order_of(-inf) is not 0.
+// index's complement.  g: the noted maxima, of a row of up to 64 parts.
 template <class E>
-__device__ __forceinline__ void top_columns(const LogitsArgs& a, int64_t row, int lane, const RowRecords& q, TopScratch& t) {
-  // parts
-  uint32_t pk[kMaxParts / 64];
+__device__ __forceinline__ void top_columns(const LogitsArgs& a, int64_t row, int lane, const RowRecords& q,
+                                            float (&g)[kHeld], float best, TopScratch& t) {
+  constexpr uint32_t STEP = 1u << (32 - 8 * sizeof(typename E::T));  // keys of bf16 values are so far apart
+  const int all = (a.vocab + kGroup - 1) / kGroup, ng = min(a.top, all);
+  const bool direct = a.parts <= 64;
+  if (!direct) {  // the best parts first, as many as there are alternatives: to lane l parts 8 l .. 8 l + 7
+    float* m = (float*)t.found;
 #pragma unroll
-  for (int i = 0; i < kMaxParts / 64; ++i) pk[i] = i * 64 + lane < a.parts ? order_of(q.r[i][0]) : 0;
-  const int np = min(a.top, a.parts);
-  select_largest<kMaxParts / 64>(pk, a.parts, np, lane, t.parts);
-  wave_sync();
-  // their groups of 128 columns
-  constexpr int G = 64 * kGroups / 64;
-  uint32_t gk[G];
-  const float* gm = a.group_max + row * a.parts * kGroups;
+    for (int i = 0; i < kMaxParts / 64; ++i) m[i * 64 + lane] = q.r[i][0];
+    wave_sync();
 #pragma unroll
-  for (int i = 0; i < G; ++i) {
-    const int at = i * 64 + lane;
-    gk[i] = 0;
-    if (i * 4 < np && at < np * kGroups) {
-      const int g = t.parts[at / kGroups] * kGroups + at % kGroups;
-      if (g * kGroup < a.vocab) gk[i] = order_of(gm[g]);
+    for (int i = 0; i < kHeld; ++i) {
+      const int at = kHeld * lane + i;
+      g[i] = at < a.parts ? fmaxf(m[at & (kMaxParts - 1)], -__builtin_inff()) : __uint_as_float(0x7fc00000u);
     }
   }
-  const int all = (a.vocab + kGroup - 1) / kGroup, ng = min(a.top, all);
-  const uint32_t least = select_largest<G>(gk, np * kGroups, ng, lane, t.groups);
-  wave_sync();
+  uint32_t least = 0;
+#pragma unroll 1
+  for (int level = direct; level < 2; ++level) {
+    least = select_largest<STEP, kHeld>(g, level ? ng : a.top, best, lane, t.groups);
+    wave_sync();
+    if (level == 0) {
+      t.parts[lane] = lane < a.top ? t.groups[lane] : 0;
+      load_groups(a, row, min((uint32_t)t.parts[lane], (uint32_t)a.parts - 1), lane < a.top, g);
+    } else if (!direct && lane < ng) {
+      const int at = t.groups[lane];
+      t.groups[lane] = t.parts[(at / kGroups) & 63] * kGroups + at % kGroups;
+    }
+    wave_sync();
+  }
   // and their columns: at least as many as asked for reach the least of as many groups
-  uint64_t bar = ng == a.top ? (uint64_t)least << 32 : 0;
+  uint64_t bar = ng == a.top ? (uint64_t)(least * STEP) << 32 : 0;
   int count = 0;
   const typename E::T* x = (const typename E::T*)a.logits + row * a.stride;
-  for (int s = 0; s < ng; s += 4) {
-    const int which = s + (lane >> 4);
-    int c = a.vocab;
-    if (which < ng) {
-      const int at = t.groups[which];
-      c = (t.parts[at / kGroups] * kGroups + at % kGroups) * kGroup + (lane & 15) * 8;
+  const auto column = [&](int which) {
+    which += lane >> 4;
+    if (which >= ng) return a.vocab;
+    return (int)min((uint32_t)t.groups[which] * kGroup + (lane & 15) * 8, (uint32_t)a.vocab);
+  };
+  constexpr int B = 4;  // loads of a lane under way: one is used, as many are ahead
+  typename E::RAW raw[B];
+  int col[B];
+#pragma unroll
+  for (int j = 0; j < B; ++j) {
+    col[j] = column(4 * j);
+    if (col[j] + 8 <= a.vocab) raw[j] = E::template load<true>(x + col[j]);
+  }
+#pragma unroll 1
+  for (int s = 0;; s += 4) {
+    if (count > kFound - 512 || s >= ng) {
+      count = keep_largest(t.found, count, a.top, lane);
+      if (count == a.top) bar = t.found[count - 1];
     }
-    F8 f;
-    if (c + 8 <= a.vocab) {
-      f = E::wide(E::template load<true>(x + c));
-    } else {
+    if (s >= ng) break;
+    const int c = col[0];
+    F8 f = E::wide(raw[0]);
+    const float floor = of_order(max((uint32_t)(bar >> 32), order_of(-__builtin_inff())));
+#pragma unroll
+    for (int j = 1; j < B; ++j) {
+      col[j - 1] = col[j];
+      raw[j - 1] = raw[j];
+    }
+    col[B - 1] = column(s + 4 * B);
+    if (col[B - 1] + 8 <= a.vocab) raw[B - 1] = E::template load<true>(x + col[B - 1]);
+    if (c + 8 > a.vocab) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = c + i < a.vocab ? E::one(x[c + i]) : 0.f;
     }
+    // few reach the floor: a lane's are taken one after the other
+    uint32_t some = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint64_t v = (uint64_t)order_of(f[i]) << 32 | (uint32_t)~(c + i);
-      const bool take = c + i < a.vocab && v > bar;
+    for (int i = 0; i < 8; ++i) some |= !(f[i] < floor) && c + i < a.vocab ? 1u << i : 0u;
+#pragma unroll 1
+    while (__ballot(some != 0)) {
+      const int at = __builtin_ctz(some | 256u);
+      float g = f[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) g = at == i ? f[i] : g;
+      const uint64_t v = (uint64_t)order_of(g) << 32 | (uint32_t)~(c + at);
+      const bool take = some != 0 && v > bar;
       const uint64_t taken = __ballot(take);
-      if (taken == 0) continue;
       if (take) t.found[count + lanes_below(taken)] = v;
       count += __builtin_popcountll(taken);
-      if (count > kFound - 64) {
-        count = keep_largest(t.found, count, a.top, lane);
-        if (count == a.top) bar = t.found[count - 1];
-      }
+      some &= some - 1;
     }
   }
-  keep_largest(t.found, count, a.top, lane);
 }
 
 template <class E, bool TOP>
@@ -339,6 +437,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs(const LogitsArgs
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * kWaves + wave;
   if (row >= a.rows) return;
+  RowRecords q;
+  load_records(a, row, lane, q);
+  float g[kHeld];
+  if (TOP && a.parts <= 64) load_groups(a, row, min(lane, a.parts - 1), lane < a.parts, g);
   if (left_out(a, row)) {
     if (lane == 0) {
       a.logprobs[row] = 0.f;
@@ -354,8 +456,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs(const LogitsArgs
   const float scale = a.scale ? a.scale[row] : 1.f;
   const typename E::T* x = (const typename E::T*)a.logits + row * a.stride;
   const float at_target = a.targets ? E::one(x[a.targets[row]]) : 0.f;
-  RowRecords q;
-  const RowSum t = join_records(a, row, scale * kLog2e, lane, q);
+  const RowSum t = join_records(a, scale * kLog2e, q);
   if (lane == 0) {
     if (a.targets) a.logprobs[row] = log_q(t, scale, at_target);
     if (a.entropy) a.entropy[row] = t.none ? 0.f : t.log_l - scale * (t.a / t.l);
@@ -366,7 +467,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs(const LogitsArgs
   }
   if constexpr (TOP) {
     TopScratch& s = scratch[wave];
-    top_columns<E>(a, row, lane, q, s);
+    top_columns<E>(a, row, lane, q, g, t.m, s);
     if (lane < a.top) {
       const uint64_t v = s.found[lane];
       a.top_ids[row * a.top + lane] = (int32_t)~(uint32_t)v;
@@ -446,15 +547,15 @@ __device__ __forceinline__ void load_teacher(const LogitsArgs& a, int64_t row, i
 #pragma unroll
   for (int i = 0; i < kEntries; ++i) {
     const int e = i * 64 + lane;
-    t.id[i] = -1;
-    t.logp[i] = -__builtin_inff();
+    int id = -1;
+    float value = 0.f;
     if (e < a.top) {
-      const int id = a.ids[row * a.top + e];
-      if ((uint32_t)id < (uint32_t)a.vocab) {
-        t.id[i] = id;
-        t.logp[i] = a.values[row * a.top + e];
-      }
+      id = a.ids[row * a.top + e];
+      value = a.values[row * a.top + e];
     }
+    const bool there = (uint32_t)id < (uint32_t)a.vocab;
+    t.id[i] = there ? id : -1;
+    t.logp[i] = there ? value : -__builtin_inff();
   }
 }
 
@@ -470,13 +571,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_distill(const LogitsArgs 
   if (row >= a.rows) return;
   const float scale = a.scale ? a.scale[row] : 1.f;
   const typename E::T* x = (const typename E::T*)a.logits + row * a.stride;
+  RowRecords q;
+  load_records(a, row, lane, q);
   Teacher te;
   load_teacher(a, row, lane, te);
   float s[kEntries];
 #pragma unroll
   for (int i = 0; i < kEntries; ++i) s[i] = te.id[i] >= 0 ? E::one(x[te.id[i]]) : 0.f;
-  RowRecords q;
-  const RowSum t = join_records(a, row, scale * kLog2e, lane, q);
+  const RowSum t = join_records(a, scale * kLog2e, q);
   float m = 0.f, log_l = 0.f;
   if (!a.given_logprobs) {
     m = te.logp[0];

@@ -124,27 +124,66 @@ gdn_status check_norm(const char* fn, const gdn_norm_shape* s, int64_t rows) {
   return check_rows(fn, rows);
 }
 
-// Work-groups of the gradient's row pass, each with a partial dw.
-constexpr int kNormBwdGroups = 512;
+// Calls that move more than this read past the caches what is read for the last
+// time (x, the residual, the gradients that come in, logits), us past / into them:
+//   norm      10,240 x 2,048 (168 MB) 32.4 / 39.3   6,144 (101 MB) 17.6 / 21.1   4,096 (67 MB) 12.4 / 11.8
+//   gradient                          33.0 / 36.8                  21.8 / 22.4                 17.3 / 15.4
+//   parts     2,048 x 131,072 (537 MB) 84.6 / 95.4; with entropy 4,096 168 / 173; fp32 1,024 87 / 91
+// Outputs of the norm stay in the caches, as a product reads them next: stored past
+// them, 10,240 x 2,048 would take 26 us, but norm, product and norm 139 and not 123.
+// Gradients of logits do not fit and go past them too, 2,048 x 131,072 165 / 180, fp32
+// 513 x 50,001 (103 MB) 38.7 / 42.7; with the product that reads them, of width 1,024,
+// 1,024 rows (268 MB) 768 / 783, 4,096 1,556 / 1,609, but 256 rows (67 MB) 459 / 457.
+constexpr int64_t kOnceFrom = int64_t(96) << 20;
 
-// threads to a row
-int row_lanes(int width) { return width <= 128 ? 16 : width <= 2048 ? 64 : 256; }
-
+// Work-groups of the gradient's row pass, each with a partial dw: enough to fill
+// the card, few enough that adding them up is short (us with 256 / 512 / 1,024 of them:
+// 10,240 x 2,048 37.9 / 35.3 / 38.3, 5,120 x 4,096 39.1 / 37.3 / 39.5, 2,500 x 8,192 38.5 / 41.6 / 47.4,
+// 1,200 x 16,384 42.5 / 48.6 / 60.4).
 int norm_bwd_groups(const gdn_norm_shape& s, int64_t rows) {
-  const int64_t per = kNormThreads / row_lanes(s.width);
-  return (int)std::min<int64_t>(kNormBwdGroups, (rows + per - 1) / per);
+  const int64_t per = s.width <= 128 ? 32 : s.width <= 1024 ? 8 : s.width <= 4096 ? 2 : 1;
+  return (int)std::min<int64_t>(s.width <= 4096 ? 512 : 256, (rows + per - 1) / per);
+}
+
+template <class X, class R>
+bool norm_reads_once(const NormArgs& a) {
+  const int64_t bytes = sizeof(typename X::T) * ((a.y ? 1 : 0) + 1) +
+                        sizeof(typename R::T) * ((a.res ? 1 : 0) + (a.h ? 1 : 0) + (a.dy ? 1 : 0));
+  return a.rows * a.width * bytes >= kOnceFrom;
 }
 
 template <class X, class R, int LANES, int NV>
 struct NormFn {
   static void forward(const NormArgs& a, hipStream_t st) {
     const int64_t per = kNormThreads / LANES;
-    hipLaunchKernelGGL((k_stack_add_norm<X, R, LANES, NV>), dim3((unsigned)((a.rows + per - 1) / per)), dim3(kNormThreads), 0, st, a);
-  }
-  static void backward(const NormArgs& a, int groups, hipStream_t st) {
-    hipLaunchKernelGGL((k_stack_add_norm_bwd<X, R, LANES, NV>), dim3(groups), dim3(kNormThreads), 0, st, a);
+    const dim3 grid((unsigned)((a.rows + per - 1) / per)), wg(kNormThreads);
+    if (norm_reads_once<X, R>(a))
+      hipLaunchKernelGGL((k_stack_add_norm<X, R, LANES, NV, true>), grid, wg, 0, st, a);
+    else
+      hipLaunchKernelGGL((k_stack_add_norm<X, R, LANES, NV, false>), grid, wg, 0, st, a);
   }
 };
+
+template <class X, class R, int LANES, int NV>
+struct NormBwdFn {
+  static void backward(const NormArgs& a, int groups, hipStream_t st) {
+    if (norm_reads_once<X, R>(a))
+      hipLaunchKernelGGL((k_stack_add_norm_bwd<X, R, LANES, NV, true>), dim3(groups), dim3(kNormBwdThreads<LANES>), 0, st, a);
+    else
+      hipLaunchKernelGGL((k_stack_add_norm_bwd<X, R, LANES, NV, false>), dim3(groups), dim3(kNormBwdThreads<LANES>), 0, st, a);
+  }
+};
+
+#define GDN_STACK_NORM_BWD_WIDTH(X, R, width, call)           \
+  do {                                                        \
+    if ((width) <= 128) NormBwdFn<X, R, 16, 1>::call;            \
+    else if ((width) <= 512) NormBwdFn<X, R, 64, 1>::call;       \
+    else if ((width) <= 1024) NormBwdFn<X, R, 64, 2>::call;      \
+    else if ((width) <= 2048) NormBwdFn<X, R, 256, 1>::call;     \
+    else if ((width) <= 4096) NormBwdFn<X, R, 256, 2>::call;     \
+    else if ((width) <= 8192) NormBwdFn<X, R, 1024, 1>::call;    \
+    else NormBwdFn<X, R, 1024, 2>::call;                         \
+  } while (0)
 
 // A row's threads follow from its width alone, so that its bits do.
 #define GDN_STACK_NORM_WIDTH(X, R, width, call)               \
@@ -158,11 +197,11 @@ struct NormFn {
     else NormFn<X, R, 256, 8>::call;                          \
   } while (0)
 
-#define GDN_STACK_NORM(shape, call)                                                                  \
+#define GDN_STACK_NORM(WIDTH, shape, call)                                                                  \
   do {                                                                                               \
-    if ((shape).dtype == GDN_DTYPE_F32) GDN_STACK_NORM_WIDTH(F32, F32, (shape).width, call);         \
-    else if ((shape).residual_dtype == GDN_DTYPE_F32) GDN_STACK_NORM_WIDTH(B16, F32, (shape).width, call); \
-    else GDN_STACK_NORM_WIDTH(B16, B16, (shape).width, call);                                        \
+    if ((shape).dtype == GDN_DTYPE_F32) WIDTH(F32, F32, (shape).width, call);         \
+    else if ((shape).residual_dtype == GDN_DTYPE_F32) WIDTH(B16, F32, (shape).width, call); \
+    else WIDTH(B16, B16, (shape).width, call);                                        \
   } while (0)
 
 }  // namespace
@@ -213,7 +252,7 @@ extern "C" gdn_status gdn_stack_add_norm(const gdn_norm_shape* shape, int64_t nu
   a.group = shape->group;
   a.eps = shape->eps;
   a.w_add = shape->zero_centered ? 1.f : 0.f;
-  GDN_STACK_NORM(*shape, forward(a, (hipStream_t)stream));
+  GDN_STACK_NORM(GDN_STACK_NORM_WIDTH, *shape, forward(a, (hipStream_t)stream));
   return launch_status(fn);
 }
 
@@ -263,7 +302,7 @@ extern "C" gdn_status gdn_stack_add_norm_bwd(const gdn_norm_shape* shape, int64_
   a.partial = (float*)workspace;
   const int groups = norm_bwd_groups(*shape, num_rows);
   hipStream_t st = (hipStream_t)stream;
-  if (groups > 0) GDN_STACK_NORM(*shape, backward(a, groups, st));
+  if (groups > 0) GDN_STACK_NORM(GDN_STACK_NORM_BWD_WIDTH, *shape, backward(a, groups, st));
   hipLaunchKernelGGL(k_stack_norm_dw, dim3((W + 31) / 32), dim3(1024), 0, st, a.partial, groups, W, dw);
   return launch_status(fn);
 }
@@ -332,40 +371,59 @@ dim3 part_grid(const LogitsArgs& a) { return dim3((unsigned)((a.rows * a.parts +
 dim3 row_grid(const LogitsArgs& a) { return dim3((unsigned)((a.rows + kWaves - 1) / kWaves)); }
 
 template <class E>
+bool reads_once(const LogitsArgs& a) {
+  return a.rows * a.vocab * (int64_t)sizeof(typename E::T) >= kOnceFrom;
+}
+
+template <class E, bool ENTROPY, bool TOP>
+void run_parts(const LogitsArgs& a, hipStream_t st) {
+  if (reads_once<E>(a))
+    hipLaunchKernelGGL((k_stack_parts<E, ENTROPY, TOP, true>), part_grid(a), dim3(64 * kWaves), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_stack_parts<E, ENTROPY, TOP, false>), part_grid(a), dim3(64 * kWaves), 0, st, a);
+}
+
+template <class E>
 void run_logprobs(const LogitsArgs& a, hipStream_t st) {
   const dim3 wg(64 * kWaves);
-  if (a.top) {
-    if (a.entropy)
-      hipLaunchKernelGGL((k_stack_parts<E, true, true>), part_grid(a), wg, 0, st, a);
-    else
-      hipLaunchKernelGGL((k_stack_parts<E, false, true>), part_grid(a), wg, 0, st, a);
-    hipLaunchKernelGGL((k_stack_logprobs<E, true>), row_grid(a), wg, 0, st, a);
-  } else {
-    if (a.entropy)
-      hipLaunchKernelGGL((k_stack_parts<E, true, false>), part_grid(a), wg, 0, st, a);
-    else
-      hipLaunchKernelGGL((k_stack_parts<E, false, false>), part_grid(a), wg, 0, st, a);
-    hipLaunchKernelGGL((k_stack_logprobs<E, false>), row_grid(a), wg, 0, st, a);
+  const int mode = top_mode(a.vocab, a.top);
+  if (mode == kTopGroups)
+    a.entropy ? run_parts<E, true, true>(a, st) : run_parts<E, false, true>(a, st);
+  else
+    a.entropy ? run_parts<E, true, false>(a, st) : run_parts<E, false, false>(a, st);
+  switch (mode) {
+    case kNoTop: hipLaunchKernelGGL((k_stack_logprobs<E, kNoTop>), row_grid(a), wg, 0, st, a); break;
+    case kTopColumns: hipLaunchKernelGGL((k_stack_logprobs<E, kTopColumns>), row_grid(a), wg, 0, st, a); break;
+    case kTopEights: hipLaunchKernelGGL((k_stack_logprobs<E, kTopEights>), row_grid(a), wg, 0, st, a); break;
+    default: hipLaunchKernelGGL((k_stack_logprobs<E, kTopGroups>), row_grid(a), wg, 0, st, a); break;
   }
+}
+
+template <class E, bool ONCE>
+void launch_logprobs_bwd(const LogitsArgs& a, hipStream_t st) {
+  if (a.d_entropy)
+    hipLaunchKernelGGL((k_stack_logprobs_bwd<E, true, ONCE>), part_grid(a), dim3(64 * kWaves), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_stack_logprobs_bwd<E, false, ONCE>), part_grid(a), dim3(64 * kWaves), 0, st, a);
 }
 
 template <class E>
 void run_logprobs_bwd(const LogitsArgs& a, hipStream_t st) {
-  if (a.d_entropy)
-    hipLaunchKernelGGL((k_stack_logprobs_bwd<E, true>), part_grid(a), dim3(64 * kWaves), 0, st, a);
-  else
-    hipLaunchKernelGGL((k_stack_logprobs_bwd<E, false>), part_grid(a), dim3(64 * kWaves), 0, st, a);
+  reads_once<E>(a) ? launch_logprobs_bwd<E, true>(a, st) : launch_logprobs_bwd<E, false>(a, st);
 }
 
 template <class E>
 void run_distill(const LogitsArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_stack_parts<E, false, false>), part_grid(a), dim3(64 * kWaves), 0, st, a);
+  run_parts<E, false, false>(a, st);
   hipLaunchKernelGGL((k_stack_distill<E>), row_grid(a), dim3(64 * kWaves), 0, st, a);
 }
 
 template <class E>
 void run_distill_bwd(const LogitsArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_stack_distill_bwd<E>), part_grid(a), dim3(64 * kWaves), 0, st, a);
+  if (reads_once<E>(a))
+    hipLaunchKernelGGL((k_stack_distill_bwd<E, true>), part_grid(a), dim3(64 * kWaves), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_stack_distill_bwd<E, false>), part_grid(a), dim3(64 * kWaves), 0, st, a);
 }
 
 #define GDN_STACK_LOGITS(shape, fn_, ...) \

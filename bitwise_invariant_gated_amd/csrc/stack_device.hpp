@@ -33,13 +33,14 @@ struct F8 {
   __device__ __forceinline__ float& operator[](int i) { return i < 4 ? ((float*)&a)[i] : ((float*)&b)[i - 4]; }
 };
 
-// Element access: T the stored type, RAW eight of them as loaded.  STREAM: not to
-// be kept in the caches.
+// Element access: T the stored type, RAW eight of them as loaded.  ONCE, STREAM: not
+// to be kept in the caches.
 struct B16 {
   typedef uint16_t T;
   typedef u32x4 RAW;
-  template <bool ANY>
+  template <bool ANY, bool ONCE = false>
   static __device__ __forceinline__ RAW load(const T* p) {
+    if constexpr (ONCE) return __builtin_nontemporal_load((const typename Pick<ANY>::U*)p);
     return *(const typename Pick<ANY>::U*)p;
   }
   static __device__ __forceinline__ float one(T x) { return __uint_as_float((uint32_t)x << 16); }
@@ -55,6 +56,12 @@ struct B16 {
     }
     return f;
   }
+  // a vector of eight from and to runs of 16 bytes
+  template <class U>
+  static __device__ __forceinline__ void widen(F8& f, const U* r) {
+    f = wide(r[0]);
+  }
+  static __device__ __forceinline__ void narrow_to(const F8& f, u32x4* r) { r[0] = narrow(f); }
   static __device__ __forceinline__ RAW narrow(F8 f) {
     return RAW{pack2(f.a[0], f.a[1]), pack2(f.a[2], f.a[3]), pack2(f.b[0], f.b[1]), pack2(f.b[2], f.b[3])};
   }
@@ -71,15 +78,24 @@ struct B16 {
 struct F32 {
   typedef float T;
   typedef F8 RAW;
-  template <bool ANY>
+  template <bool ANY, bool ONCE = false>
   static __device__ __forceinline__ RAW load(const T* p) {
     typedef typename Pick<ANY>::F V;
+    if constexpr (ONCE) return F8{__builtin_nontemporal_load((const V*)p), __builtin_nontemporal_load((const V*)(p + 4))};
     return F8{*(const V*)p, *(const V*)(p + 4)};
   }
   static __device__ __forceinline__ float one(T x) { return x; }
   static __device__ __forceinline__ T round(float x) { return x; }
   static __device__ __forceinline__ F8 wide(RAW r) { return r; }
   static __device__ __forceinline__ RAW narrow(F8 f) { return f; }
+  template <class U>
+  static __device__ __forceinline__ void widen(F8& f, const U* r) {
+    f = F8{__builtin_bit_cast(f32x4, (u32x4)r[0]), __builtin_bit_cast(f32x4, (u32x4)r[1])};
+  }
+  static __device__ __forceinline__ void narrow_to(const F8& f, u32x4* r) {
+    r[0] = __builtin_bit_cast(u32x4, f.a);
+    r[1] = __builtin_bit_cast(u32x4, f.b);
+  }
   template <bool ANY, bool STREAM>
   static __device__ __forceinline__ void store(T* p, RAW r) {
     typedef typename Pick<ANY>::F V;

@@ -12,8 +12,9 @@
 // Top alternatives, by (logit, then lowest index): the parts also note the
 // largest logit of every 128 columns.  The k best columns lie in the k best
 // groups of 128 by (largest logit, lowest group): a column outside has k groups
-// that each hold a better one.  So the joining wave picks the k best parts, of
-// their groups the k best, and reads those again: k * 128 columns of a row.
+// that each hold a better one.  So the joining wave picks the k best groups (of
+// more than 64 parts, first the k best parts), and reads those again: k * 128
+// columns of a row.  Short rows are read again whole.
 //
 // Bound by memory: the logits are read once (gradients: and written once).
 #pragma once
@@ -55,12 +56,12 @@ struct LogitsArgs {
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // a lane's columns of a part: vector j holds 512 j + 8 lane .. + 7
-template <class E>
+template <class E, bool ONCE>
 __device__ __forceinline__ void load_part(const typename E::T* p, int n, int lane, F8 (&x)[kVecs]) {
   typename E::RAW raw[kVecs];
   if (n >= kPart) {
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) raw[j] = E::template load<true>(p + j * 512 + lane * 8);
+    for (int j = 0; j < kVecs; ++j) raw[j] = E::template load<true, ONCE>(p + j * 512 + lane * 8);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) x[j] = E::wide(raw[j]);
     return;
@@ -96,7 +97,7 @@ __device__ __forceinline__ bool left_out(const LogitsArgs& a, int64_t row) {
   return a.targets && (uint32_t)a.targets[row] >= (uint32_t)a.vocab;
 }
 
-template <class E, bool ENTROPY, bool TOP>
+template <class E, bool ENTROPY, bool TOP, bool ONCE>
 __global__ __launch_bounds__(64 * kWaves) void k_stack_parts(const LogitsArgs a) {
   int64_t row;
   int part;
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_parts(const LogitsArgs a)
   const int lane = threadIdx.x & 63;
   const float c = (a.scale ? a.scale[row] : 1.f) * kLog2e;
   F8 x[kVecs];
-  load_part<E>((const typename E::T*)a.logits + row * a.stride + part * kPart, a.vocab - part * kPart, lane, x);
+  load_part<E, ONCE>((const typename E::T*)a.logits + row * a.stride + part * kPart, a.vocab - part * kPart, lane, x);
   float m8[kVecs];
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) m8[j] = max8(x[j]);
@@ -219,6 +220,13 @@ __device__ __forceinline__ int sum_up_to(int x) {
   return x;
 }
 
+// The value of a key in units of STEP: the lower half of a bf16 value's order is
+// its sign's.
+template <uint32_t STEP>
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return of_order(k * STEP + ((int32_t)(k * STEP) < 0 ? 0 : STEP - 1));
+}
+
 // Of up to 64 * N values (value N * lane + i in x[i], NaN where there is none)
 // the `want` <= 64 largest, equal ones by ascending index: their indices go to
 // `list` in ascending order.  None is above `best`.  Returns the key, in units
@@ -228,8 +236,6 @@ __device__ __forceinline__ int sum_up_to(int x) {
 // code is run once and has to be fetched first.)
 template <uint32_t STEP, int N>
 __device__ __forceinline__ uint32_t select_largest(const float (&x)[N], int want, float best, int lane, int* list) {
-  // the lower half of a bf16 value's order is its sign's
-  const auto value = [](uint32_t k) { return of_order(k * STEP + ((int32_t)(k * STEP) < 0 ? 0 : STEP - 1)); };
   const auto reach = [&](float f) {
     int c = 0;
 #pragma unroll
@@ -242,11 +248,11 @@ __device__ __forceinline__ uint32_t select_largest(const float (&x)[N], int want
   for (int i = 1; i < N; ++i) low = fmaxf(low, x[i]);
   low = __builtin_popcountll(__ballot(low == low)) < want ? -__builtin_inff() : -max_groups(max_16(-low));
   uint32_t lo = __builtin_amdgcn_readfirstlane(order_of(low) / STEP), hi = __builtin_amdgcn_readfirstlane(order_of(best) / STEP);
-  int count = reach(value(lo));
+  int count = reach(value_of<STEP>(lo));
 #pragma unroll 1
   while (lo < hi && count != want) {
     const uint32_t t = lo + (hi - lo + 1) / 2;
-    const int c = reach(value(t));
+    const int c = reach(value_of<STEP>(t));
     if (c >= want) {
       lo = t;
       count = c;
@@ -255,12 +261,12 @@ __device__ __forceinline__ uint32_t select_largest(const float (&x)[N], int want
     }
   }
   uint32_t take = 0;
-  const float f = value(lo);
+  const float f = value_of<STEP>(lo);
 #pragma unroll
   for (int i = N - 1; i >= 0; --i) take = 2 * take + (x[i] >= f);
   if (count != want) {  // of those equal to the least, the first
     uint32_t above = 0;
-    const float g = value(lo + 1);
+    const float g = value_of<STEP>(lo + 1);
 #pragma unroll
     for (int i = N - 1; i >= 0; --i) above = 2 * above + (x[i] >= g);
     const int over = __builtin_amdgcn_readlane(sum_up_to(__builtin_popcount(above)), 63);
@@ -278,17 +284,27 @@ __device__ __forceinline__ uint32_t select_largest(const float (&x)[N], int want
   return lo;
 }
 
-constexpr int kFound = 1024;  // columns held while the best are sought
+// Where a row's alternatives are sought: nowhere; among its columns themselves;
+// among the largest of every 8 columns, then in the best of those; or among the
+// noted largest of every 128, then in the best of those.
+enum TopMode { kNoTop, kTopColumns, kTopEights, kTopGroups };
 
+inline int top_mode(int vocab, int top) {
+  return top == 0 ? kNoTop : vocab <= 1024 ? kTopColumns : vocab <= 8192 ? kTopEights : kTopGroups;
+}
+
+template <int MODE>
 struct TopScratch {
-  uint64_t found[kFound];
-  int parts[64], groups[64];
+  static constexpr int N = MODE == kTopColumns ? 64 : 1024;
+  uint64_t found[N];  // columns held while the best are sought
+  int parts[64], units[64];
 };
 
 // Keeps the `want` largest of the `count` different values found, in order.
-__device__ __forceinline__ int keep_largest(uint64_t* found, int count, int want, int lane) {
+template <int N>
+__device__ __forceinline__ int keep_largest(uint64_t (&found)[N], int count, int want, int lane) {
   wave_sync();
-  if (count <= 64) {  // the usual case: hardly more than are wanted
+  if (N == 64 || count <= 64) {  // the usual case: hardly more than are wanted
     const uint64_t v = lane < count ? found[lane] : 0;
     int rank = 0;
 #pragma unroll 1
@@ -302,10 +318,10 @@ __device__ __forceinline__ int keep_largest(uint64_t* found, int count, int want
     wave_sync();
     return min(count, want);
   }
-  uint64_t v[kFound / 64];
-  int rank[kFound / 64];
+  uint64_t v[N / 64];
+  int rank[N / 64];
 #pragma unroll
-  for (int i = 0; i < kFound / 64; ++i) {
+  for (int i = 0; i < N / 64; ++i) {
     rank[i] = 0;
     v[i] = i * 64 + lane < count ? found[i * 64 + lane] : 0;
   }
@@ -313,12 +329,12 @@ __device__ __forceinline__ int keep_largest(uint64_t* found, int count, int want
   for (int t = 0; t < count; ++t) {
     const uint64_t o = found[t];
 #pragma unroll
-    for (int i = 0; i < kFound / 64; ++i)
+    for (int i = 0; i < N / 64; ++i)
       if (i * 64 < count) rank[i] += o > v[i];
   }
   wave_sync();
 #pragma unroll
-  for (int i = 0; i < kFound / 64; ++i)
+  for (int i = 0; i < N / 64; ++i)
     if (v[i] && rank[i] < want) found[rank[i]] = v[i];
   wave_sync();
   return min(count, want);
@@ -326,29 +342,75 @@ __device__ __forceinline__ int keep_largest(uint64_t* found, int count, int want
 
 constexpr int kHeld = 16;  // values of a lane among which the largest are sought
 
-// The noted maxima of a row of up to 64 parts, those of a part to a lane.
+// A value to seek among: a NaN ranks as -inf, and there is none where it ends.
+__device__ __forceinline__ float held(float x, bool there) {
+  return there ? fmaxf(x, -__builtin_inff()) : __uint_as_float(0x7fc00000u);
+}
+
+// eight columns of a row; past its end 0
+template <class E>
+__device__ __forceinline__ F8 load_eight(const typename E::T* x, int c, int vocab) {
+  F8 f = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  if (c + 8 <= vocab) {
+    f = E::wide(E::template load<true>(x + c));
+  } else if (c < vocab) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < vocab) f[i] = E::one(x[c + i]);
+  }
+  return f;
+}
+
+// The noted maxima of a part of a row.
 __device__ __forceinline__ void load_groups(const LogitsArgs& a, int64_t row, int part, bool there, float (&x)[kHeld]) {
   const f32x4* gm = (const f32x4*)(a.group_max + (row * a.parts + part) * kGroups);
 #pragma unroll
   for (int i = 0; i < kHeld / 4; ++i) {
-    const float none = __uint_as_float(0x7fc00000u);
-    f32x4 v = {none, none, none, none};
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (there) v = gm[i];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      x[4 * i + e] = there && part * kPart + (4 * i + e) * kGroup < a.vocab ? fmaxf(v[e], -__builtin_inff()) : none;
+    for (int e = 0; e < 4; ++e) x[4 * i + e] = held(v[e], there && part * kPart + (4 * i + e) * kGroup < a.vocab);
+  }
+}
+
+// The values of a row's first search: lane l's are those of columns 16 l .. 16 l
+// + 15, of units 16 l .. of 8 columns, or of part l (of up to 64 parts).
+template <class E, int MODE>
+__device__ __forceinline__ void load_values(const LogitsArgs& a, int64_t row, int lane, float (&x)[kHeld]) {
+  const typename E::T* p = (const typename E::T*)a.logits + row * a.stride;
+  if constexpr (MODE == kTopColumns) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      F8 f = load_eight<E>(p, kHeld * lane + 8 * h, a.vocab);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[8 * h + i] = held(f[i], kHeld * lane + 8 * h + i < a.vocab);
+    }
+  } else if constexpr (MODE == kTopEights) {
+#pragma unroll 4
+    for (int i = 0; i < kHeld; ++i) {
+      const int c = (kHeld * lane + i) * 8;
+      F8 f = load_eight<E>(p, c, a.vocab);
+      float m = -__builtin_inff();
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < a.vocab) m = fmaxf(m, f[e]);
+      x[i] = held(m, c < a.vocab);
+    }
+  } else if constexpr (MODE == kTopGroups) {
+    if (a.parts <= 64) load_groups(a, row, min(lane, a.parts - 1), lane < a.parts, x);
   }
 }
 
 // The row's a.top best columns, in order, in found[]: order_of(logit) above the
-// index's complement.  g: the noted maxima, of a row of up to 64 parts.
-template <class E>
+// index's complement.  v: load_values.
+template <class E, int MODE>
 __device__ __forceinline__ void top_columns(const LogitsArgs& a, int64_t row, int lane, const RowRecords& q,
-                                            float (&g)[kHeld], float best, TopScratch& t) {
+                                            float (&v)[kHeld], float best, TopScratch<MODE>& t) {
   constexpr uint32_t STEP = 1u << (32 - 8 * sizeof(typename E::T));  // keys of bf16 values are so far apart
-  const int all = (a.vocab + kGroup - 1) / kGroup, ng = min(a.top, all);
-  const bool direct = a.parts <= 64;
-  if (!direct) {  // the best parts first, as many as there are alternatives: to lane l parts 8 l .. 8 l + 7
+  const typename E::T* x = (const typename E::T*)a.logits + row * a.stride;
+  const auto entry = [&](float f, int c) { return (uint64_t)order_of(f) << 32 | (uint32_t)~c; };
+  const bool direct = MODE != kTopGroups || a.parts <= 64;
+  if (!direct) {  // the best parts first, as many as there are alternatives
     float* m = (float*)t.found;
 #pragma unroll
     for (int i = 0; i < kMaxParts / 64; ++i) m[i * 64 + lane] = q.r[i][0];
@@ -356,103 +418,122 @@ __device__ __forceinline__ void top_columns(const LogitsArgs& a, int64_t row, in
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int at = kHeld * lane + i;
-      g[i] = at < a.parts ? fmaxf(m[at & (kMaxParts - 1)], -__builtin_inff()) : __uint_as_float(0x7fc00000u);
+      v[i] = held(m[at & (kMaxParts - 1)], at < a.parts);
     }
   }
   uint32_t least = 0;
 #pragma unroll 1
   for (int level = direct; level < 2; ++level) {
-    least = select_largest<STEP, kHeld>(g, level ? ng : a.top, best, lane, t.groups);
+    least = select_largest<STEP, kHeld>(v, a.top, best, lane, t.units);
     wave_sync();
-    if (level == 0) {
-      t.parts[lane] = lane < a.top ? t.groups[lane] : 0;
-      load_groups(a, row, min((uint32_t)t.parts[lane], (uint32_t)a.parts - 1), lane < a.top, g);
-    } else if (!direct && lane < ng) {
-      const int at = t.groups[lane];
-      t.groups[lane] = t.parts[(at / kGroups) & 63] * kGroups + at % kGroups;
+    if (level == 0) {  // then the groups of part l of those in lane l
+      t.parts[lane] = lane < a.top ? t.units[lane] : 0;
+      load_groups(a, row, min((uint32_t)t.parts[lane], (uint32_t)a.parts - 1), lane < a.top, v);
+    } else if (!direct && lane < a.top) {
+      const int at = t.units[lane];
+      t.units[lane] = t.parts[(at / kGroups) & 63] * kGroups + at % kGroups;
     }
     wave_sync();
   }
-  // and their columns: at least as many as asked for reach the least of as many groups
-  uint64_t bar = ng == a.top ? (uint64_t)(least * STEP) << 32 : 0;
-  int count = 0;
-  const typename E::T* x = (const typename E::T*)a.logits + row * a.stride;
+  if constexpr (MODE == kTopColumns) {
+    if (lane < a.top) {
+      const int c = min((uint32_t)t.units[lane], (uint32_t)a.vocab - 1);
+      t.found[lane] = entry(E::one(x[c]), c);
+    }
+    keep_largest(t.found, a.top, a.top, lane);
+    return;
+  }
+  // Their columns.  At least as many as asked for reach the least of as many
+  // units; of those equal to it, no more than asked for are needed, the first
+  // ones, and the units come in ascending order.
+  constexpr int W = MODE == kTopGroups ? 16 : 1, U = 64 / W;  // lanes to a unit, units at a time
+  const float exact = value_of<STEP>(least);
+  uint64_t bar = 0;
+  int count = 0, equal = 0;
   const auto column = [&](int which) {
-    which += lane >> 4;
-    if (which >= ng) return a.vocab;
-    return (int)min((uint32_t)t.groups[which] * kGroup + (lane & 15) * 8, (uint32_t)a.vocab);
+    which += lane / W;
+    return which < a.top ? (int)min(((uint32_t)t.units[which] * W + lane % W) * 8, (uint32_t)a.vocab) : a.vocab;
   };
-  constexpr int B = 4;  // loads of a lane under way: one is used, as many are ahead
+  constexpr int B = MODE == kTopGroups ? 4 : 1;  // loads of a lane under way: one is used, the others are ahead
   typename E::RAW raw[B];
   int col[B];
 #pragma unroll
   for (int j = 0; j < B; ++j) {
-    col[j] = column(4 * j);
+    col[j] = column(U * j);
     if (col[j] + 8 <= a.vocab) raw[j] = E::template load<true>(x + col[j]);
   }
 #pragma unroll 1
-  for (int s = 0;; s += 4) {
-    if (count > kFound - 512 || s >= ng) {
+  for (int s = 0;; s += U) {
+    if (count > t.N - 512 - 64 || s >= a.top) {
       count = keep_largest(t.found, count, a.top, lane);
       if (count == a.top) bar = t.found[count - 1];
     }
-    if (s >= ng) break;
+    if (s >= a.top) break;
     const int c = col[0];
     F8 f = E::wide(raw[0]);
-    const float floor = of_order(max((uint32_t)(bar >> 32), order_of(-__builtin_inff())));
 #pragma unroll
     for (int j = 1; j < B; ++j) {
       col[j - 1] = col[j];
       raw[j - 1] = raw[j];
     }
-    col[B - 1] = column(s + 4 * B);
-    if (col[B - 1] + 8 <= a.vocab) raw[B - 1] = E::template load<true>(x + col[B - 1]);
-    if (c + 8 > a.vocab) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = c + i < a.vocab ? E::one(x[c + i]) : 0.f;
+    if constexpr (B > 1) {
+      col[B - 1] = column(s + U * B);
+      if (col[B - 1] + 8 <= a.vocab) raw[B - 1] = E::template load<true>(x + col[B - 1]);
     }
-    // few reach the floor: a lane's are taken one after the other
-    uint32_t some = 0;
+    if (c + 8 > a.vocab) f = load_eight<E>(x, c, a.vocab);
+    uint32_t some = 0, same = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) some |= !(f[i] < floor) && c + i < a.vocab ? 1u << i : 0u;
+    for (int i = 0; i < 8; ++i) {
+      const float g = held(f[i], c + i < a.vocab);
+      some |= g > exact ? 1u << i : 0u;
+      same |= g == exact ? 1u << i : 0u;
+    }
+    if (equal < a.top && __ballot(same != 0)) {
+      const int mine = __builtin_popcount(same), upto = sum_up_to(mine);
+      int room = a.top - equal - (upto - mine);
+#pragma unroll 1
+      for (; same && room > 0; --room, same &= same - 1) some |= same & -same;
+      equal += __builtin_amdgcn_readlane(upto, 63);
+    }
+    // few are left: a lane's are taken one after the other
 #pragma unroll 1
     while (__ballot(some != 0)) {
       const int at = __builtin_ctz(some | 256u);
       float g = f[0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) g = at == i ? f[i] : g;
-      const uint64_t v = (uint64_t)order_of(g) << 32 | (uint32_t)~(c + at);
-      const bool take = some != 0 && v > bar;
+      const uint64_t e = entry(g, c + at);
+      const bool take = some != 0 && e > bar;
       const uint64_t taken = __ballot(take);
-      if (take) t.found[count + lanes_below(taken)] = v;
+      if (take) t.found[count + lanes_below(taken)] = e;
       count += __builtin_popcountll(taken);
       some &= some - 1;
     }
   }
 }
 
-template <class E, bool TOP>
+template <class E, int MODE>
 __global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs(const LogitsArgs a) {
-  __shared__ TopScratch scratch[TOP ? kWaves : 1];
+  __shared__ TopScratch<MODE> scratch[MODE ? kWaves : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * kWaves + wave;
   if (row >= a.rows) return;
   RowRecords q;
   load_records(a, row, lane, q);
-  float g[kHeld];
-  if (TOP && a.parts <= 64) load_groups(a, row, min(lane, a.parts - 1), lane < a.parts, g);
   if (left_out(a, row)) {
     if (lane == 0) {
       a.logprobs[row] = 0.f;
       if (a.entropy) a.entropy[row] = 0.f;
       if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.f;
     }
-    if (TOP && lane < a.top) {
+    if (MODE && lane < a.top) {
       a.top_ids[row * a.top + lane] = -1;
       a.top_logprobs[row * a.top + lane] = 0.f;
     }
     return;
   }
+  float v[kHeld];
+  load_values<E, MODE>(a, row, lane, v);
   const float scale = a.scale ? a.scale[row] : 1.f;
   const typename E::T* x = (const typename E::T*)a.logits + row * a.stride;
   const float at_target = a.targets ? E::one(x[a.targets[row]]) : 0.f;
@@ -465,19 +546,83 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs(const LogitsArgs
       a.stats[2 * row + 1] = t.log_l;
     }
   }
-  if constexpr (TOP) {
-    TopScratch& s = scratch[wave];
-    top_columns<E>(a, row, lane, q, g, t.m, s);
+  if constexpr (MODE != kNoTop) {
+    TopScratch<MODE>& s = scratch[wave];
+    top_columns<E, MODE>(a, row, lane, q, v, t.m, s);
     if (lane < a.top) {
-      const uint64_t v = s.found[lane];
-      a.top_ids[row * a.top + lane] = (int32_t)~(uint32_t)v;
-      a.top_logprobs[row * a.top + lane] = log_q(t, scale, of_order((uint32_t)(v >> 32)));
+      const uint64_t e = s.found[lane];
+      a.top_ids[row * a.top + lane] = (int32_t)~(uint32_t)e;
+      a.top_logprobs[row * a.top + lane] = log_q(t, scale, of_order((uint32_t)(e >> 32)));
     }
   }
 }
 
-// Gradient of log probability and entropy: a wave to a part, as above.
-template <class E, bool ENTROPY>
+// Gradients: a wave to a part, column by column, so a lane's columns may be
+// others: as many runs of 16 bytes as its eight elements are, a wave's runs side
+// by side.  (Two loads of a lane side by side, as above, share their lines; read
+// or written past the caches those would move twice.)
+template <class E>
+struct Runs {
+  static constexpr int N = 16 / (int)sizeof(typename E::T), R = 8 / N;  // elements of a run, runs of a vector
+  static __device__ __forceinline__ int column(int j, int r, int lane) { return j * 512 + r * (512 / R) + lane * N; }
+};
+
+template <class E, bool ONCE>
+__device__ __forceinline__ void load_runs(const typename E::T* p, int n, int lane, F8 (&x)[kVecs]) {
+  typedef Runs<E> L;
+  u32x4 raw[kVecs * L::R];
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+    for (int r = 0; r < L::R; ++r) {
+      const int c = L::column(j, r, lane);
+      if (n >= kPart || c + L::N <= n) {
+        const auto* at = (const typename Pick<true>::U*)(p + c);
+        raw[j * L::R + r] = ONCE ? __builtin_nontemporal_load(at) : *at;
+      }
+    }
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    E::widen(x[j], raw + j * L::R);
+    if (n >= kPart) continue;
+#pragma unroll
+    for (int r = 0; r < L::R; ++r) {
+      const int c = L::column(j, r, lane);
+      if (c + L::N > n) {
+#pragma unroll
+        for (int i = 0; i < L::N; ++i) x[j][r * L::N + i] = c + i < n ? E::one(p[c + i]) : -__builtin_inff();
+      }
+    }
+  }
+}
+
+template <class E, bool ONCE>
+__device__ __forceinline__ void store_runs(typename E::T* p, int n, int lane, F8 (&x)[kVecs]) {
+  typedef Runs<E> L;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    u32x4 raw[L::R];
+    E::narrow_to(x[j], raw);
+#pragma unroll
+    for (int r = 0; r < L::R; ++r) {
+      const int c = L::column(j, r, lane);
+      if (c + L::N <= n) {
+        auto* at = (typename Pick<true>::U*)(p + c);
+        if constexpr (ONCE)
+          __builtin_nontemporal_store(raw[r], at);
+        else
+          *at = raw[r];
+      } else {
+#pragma unroll
+        for (int i = 0; i < L::N; ++i)
+          if (c + i < n) p[c + i] = E::round(x[j][r * L::N + i]);
+      }
+    }
+  }
+}
+
+// Gradient of log probability and entropy.
+template <class E, bool ENTROPY, bool ONCE>
 __global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs_bwd(const LogitsArgs a) {
   int64_t row;
   int part;
@@ -494,7 +639,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs_bwd(const Logits
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) x[j] = F8{{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
   } else {
-    load_part<E>((const typename E::T*)a.logits + row * a.stride + part * kPart, n, lane, x);
+    load_runs<E, ONCE>((const typename E::T*)a.logits + row * a.stride + part * kPart, n, lane, x);
     const float c = scale * kLog2e, off = -log_l * kLog2e, up = h - log_l;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
@@ -511,26 +656,21 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs_bwd(const Logits
     if (a.targets && a.d_logprobs) {
       const int at = a.targets[row] - part * kPart;
       if (at >= 0 && at < kPart) {
+        typedef Runs<E> L;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j)
-          if (at / 512 == j && (at % 512) / 8 == lane) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[j][i] += at % 8 == i ? g : 0.f;
+          for (int r = 0; r < L::R; ++r) {
+            const int e = at - L::column(j, r, lane);
+            if (e >= 0 && e < L::N) {
+#pragma unroll
+              for (int i = 0; i < L::N; ++i) x[j][r * L::N + i] += e == i ? g : 0.f;
+            }
           }
       }
     }
   }
-#pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    const int col = j * 512 + lane * 8;
-    if (col + 8 <= n) {
-      E::template store<true, false>(out + col, E::narrow(x[j]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col + i < n) out[col + i] = E::round(x[j][i]);
-    }
-  }
+  store_runs<E, ONCE>(out, n, lane, x);
 }
 
 // ---------------------------------------------------------------------------
@@ -608,7 +748,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_distill(const LogitsArgs 
 
 // Gradient.  Every column is first stored as if it were no entry; the wave then
 // writes over those that are.
-template <class E>
+template <class E, bool ONCE>
 __global__ __launch_bounds__(64 * kWaves) void k_stack_distill_bwd(const LogitsArgs a) {
   int64_t row;
   int part;
@@ -620,7 +760,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_distill_bwd(const LogitsA
   const float m = st[0], log_l = st[1];
   const float scale = a.scale ? a.scale[row] : 1.f, g = a.d_loss[row] * scale;
   F8 x[kVecs];
-  load_part<E>(in, n, lane, x);
+  load_runs<E, ONCE>(in, n, lane, x);
   Teacher te;
   load_teacher(a, row, lane, te);
   if (!a.given_logprobs) normalise(te, scale, st[2], st[3]);
@@ -643,15 +783,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_distill_bwd(const LogitsA
   for (int j = 0; j < kVecs; ++j) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[j][i] = zero ? 0.f : exp2_fast(__builtin_fmaf(x[j][i] - m, c, off)) * k;
-    const int col = j * 512 + lane * 8;
-    if (col + 8 <= n) {
-      E::template store<true, false>(out + col, E::narrow(x[j]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col + i < n) out[col + i] = E::round(x[j][i]);
-    }
   }
+  store_runs<E, ONCE>(out, n, lane, x);
   if (any == 0 || zero) return;
   // the part's entries, one index at a time: its first entry takes the sum of all of its p
   float sum[kEntries];

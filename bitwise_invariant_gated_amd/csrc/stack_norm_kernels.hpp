@@ -27,6 +27,12 @@ struct NormArgs {
 
 constexpr int kNormThreads = 256;
 
+// What is read past the caches: in fp32 a lane's two loads share their lines,
+// which would be fetched for each.
+template <class E, bool ONCE>
+constexpr bool once = ONCE && sizeof(typename E::T) == 2;
+
+
 // Sum over the LANES threads of a row; `red`: 4 floats of LDS that no thread
 // still reads from an earlier call.
 template <int LANES>
@@ -41,22 +47,26 @@ __device__ __forceinline__ float row_sum(float x, float* red) {
   }
 }
 
-// two sums at once; red: 8 floats
+// two sums at once; red: LANES / 32 floats
 template <int LANES>
 __device__ __forceinline__ void row_sums(float& x, float& y, float* red) {
-  if constexpr (LANES <= 64) {
-    x = sum_lanes<LANES>(x);
-    y = sum_lanes<LANES>(y);
-  } else {
-    x = sum_lanes<64>(x);
-    y = sum_lanes<64>(y);
+  constexpr int W = LANES / 64;
+  x = sum_lanes<(LANES < 64 ? LANES : 64)>(x);
+  y = sum_lanes<(LANES < 64 ? LANES : 64)>(y);
+  if constexpr (W > 1) {
+    const int wave = (threadIdx.x >> 6) % W;
     if ((threadIdx.x & 63) == 0) {
-      red[threadIdx.x >> 6] = x;
-      red[4 + (threadIdx.x >> 6)] = y;
+      red[wave] = x;
+      red[W + wave] = y;
     }
     __syncthreads();
-    x = (red[0] + red[1]) + (red[2] + red[3]);
-    y = (red[4] + red[5]) + (red[6] + red[7]);
+    x = red[0];
+    y = red[W];
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      x += red[i];
+      y += red[W + i];
+    }
   }
 }
 
@@ -95,7 +105,7 @@ __device__ __forceinline__ u32x2 to_e4m3(const F8& f, float s) {
 
 // A row to LANES threads, NV vectors of eight columns to a thread, the vectors
 // LANES * 8 columns apart.
-template <class X, class R, int LANES, int NV>
+template <class X, class R, int LANES, int NV, bool ONCE>
 __global__ __launch_bounds__(kNormThreads) void k_stack_add_norm(const NormArgs a) {
   __shared__ float red[8];
   const int l = threadIdx.x % LANES;
@@ -111,8 +121,8 @@ __global__ __launch_bounds__(kNormThreads) void k_stack_add_norm(const NormArgs 
   for (int j = 0; j < NV; ++j) {
     const int c = (j * LANES + l) * 8;
     if (c < a.width) {
-      xr[j] = X::template load<false>(x + c);
-      if (a.res) rr[j] = R::template load<false>(res + c);
+      xr[j] = X::template load<false, once<X, ONCE>>(x + c);
+      if (a.res) rr[j] = R::template load<false, once<R, ONCE>>(res + c);
     }
   }
   float ss = 0.f;
@@ -167,23 +177,28 @@ __global__ __launch_bounds__(kNormThreads) void k_stack_add_norm(const NormArgs 
 // Gradient.  Work-groups go over the rows in steps of the grid; a thread keeps
 // dw of its columns in registers for all of its rows, so dw costs one partial
 // sum of a row's width per work-group.
-template <class X, class R, int LANES, int NV>
-__global__ __launch_bounds__(kNormThreads) void k_stack_add_norm_bwd(const NormArgs a) {
-  constexpr int G = kNormThreads / LANES;
-  __shared__ float red[2][8];
-  __shared__ f32x4 part[G > 1 ? 2 * kNormThreads : 1];
+// Threads of a work-group: 512, or a row's 1,024.
+template <int LANES>
+constexpr int kNormBwdThreads = LANES == 1024 ? 1024 : 512;
+
+template <class X, class R, int LANES, int NV, bool ONCE>
+__global__ __launch_bounds__(kNormBwdThreads<LANES>, 4) void k_stack_add_norm_bwd(const NormArgs a) {
+  constexpr int kT = kNormBwdThreads<LANES>, G = kT / LANES;
+  __shared__ float red[2][G][LANES < 256 ? 1 : LANES / 32];
+  __shared__ f32x4 part[G > 1 ? 2 * kT : 1];
   const int l = threadIdx.x % LANES, sub = threadIdx.x / LANES;
-  F8 g[NV], w[NV];
+  __shared__ f32x4 wl[2 * LANES * NV];
+  F8 g[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * LANES + l) * 8;
-    g[j] = F8{{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    w[j] = g[j];
-    if (c < a.width) w[j] = F8{*(const f32x4*)(a.w + c) + a.w_add, *(const f32x4*)(a.w + c + 4) + a.w_add};
-  }
+  for (int j = 0; j < NV; ++j) g[j] = F8{{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  for (int i = threadIdx.x; i < a.width / 4; i += kT) wl[i] = *(const f32x4*)(a.w + 4 * i) + a.w_add;
+  __syncthreads();
+  const auto weight = [&](int c) { return F8{wl[c / 4], wl[c / 4 + 1]}; };
   const float inv = 1.f / (float)a.width;
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * G + sub; row < a.rows; row += (int64_t)gridDim.x * G, turn ^= 1) {
+  for (int64_t first = (int64_t)blockIdx.x * G; first < a.rows; first += (int64_t)gridDim.x * G, turn ^= 1) {
+    const int64_t row = first + sub;
+    const int width = row < a.rows ? a.width : 0;  // no row: no columns
     const typename R::T* hp = (const typename R::T*)a.x + row * a.x_stride;
     const typename X::T* yp = (const typename X::T*)a.dy + row * a.dy_stride;
     const typename R::T* dp = (const typename R::T*)a.res + row * a.res_stride;
@@ -193,28 +208,29 @@ __global__ __launch_bounds__(kNormThreads) void k_stack_add_norm_bwd(const NormA
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * LANES + l) * 8;
-      if (c < a.width) {
-        hr[j] = R::template load<false>(hp + c);
-        yr[j] = X::template load<false>(yp + c);
-        if (a.res) dr[j] = R::template load<false>(dp + c);
+      if (c < width) {
+        hr[j] = R::template load<false, once<R, ONCE>>(hp + c);
+        yr[j] = X::template load<false, once<X, ONCE>>(yp + c);
+        if (a.res) dr[j] = R::template load<false, once<R, ONCE>>(dp + c);
       }
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if ((j * LANES + l) * 8 >= a.width) continue;
-      const F8 h = R::wide(hr[j]), y = X::wide(yr[j]);
+      const int c = (j * LANES + l) * 8;
+      if (c >= width) continue;
+      const F8 h = R::wide(hr[j]), y = X::wide(yr[j]), w = weight(c);
       ss = dot4(h.b, h.b, dot4(h.a, h.a, ss));
-      hx = dot4(y.b * w[j].b, h.b, dot4(y.a * w[j].a, h.a, hx));
+      hx = dot4(y.b * w.b, h.b, dot4(y.a * w.a, h.a, hx));
     }
-    row_sums<LANES>(ss, hx, red[turn]);
+    row_sums<LANES>(ss, hx, red[turn][sub]);
     const float r = 1.f / __builtin_sqrtf(ss * inv + a.eps);
     const float m = hx * r * r * inv;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * LANES + l) * 8;
-      if (c >= a.width) continue;
-      const F8 h = R::wide(hr[j]), y = X::wide(yr[j]);
-      F8 d = {r * (y.a * w[j].a - h.a * m), r * (y.b * w[j].b - h.b * m)};
+      if (c >= width) continue;
+      const F8 h = R::wide(hr[j]), y = X::wide(yr[j]), w = weight(c);
+      F8 d = {r * (y.a * w.a - h.a * m), r * (y.b * w.b - h.b * m)};
       g[j].a += y.a * (h.a * r);
       g[j].b += y.b * (h.b * r);
       if (a.res) {
@@ -232,13 +248,13 @@ __global__ __launch_bounds__(kNormThreads) void k_stack_add_norm_bwd(const NormA
     if constexpr (G > 1) {  // the work-group's rows, one after the other
       __syncthreads();
       part[threadIdx.x] = g[j].a;
-      part[kNormThreads + threadIdx.x] = g[j].b;
+      part[kT + threadIdx.x] = g[j].b;
       __syncthreads();
       if (sub == 0) {
 #pragma unroll
         for (int i = 1; i < G; ++i) {
           g[j].a += part[i * LANES + l];
-          g[j].b += part[kNormThreads + i * LANES + l];
+          g[j].b += part[kT + i * LANES + l];
         }
       }
     }

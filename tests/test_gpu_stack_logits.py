@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 B, F = torch.bfloat16, torch.float32
 INF = float("inf")
 # at, before and behind the borders of a vector, a group and a part, and a row of many parts
-VOCABS = [1, 2, 7, 8, 9, 100, 128, 129, 511, 2047, 2048, 2049, 4100, 10007, 131072]
+VOCABS = [1, 2, 7, 8, 9, 100, 128, 129, 511, 1024, 1025, 2047, 2048, 2049, 4100, 8192, 8193, 10007, 131072, 131080]
 
 
 def make(t, v, dtype, seed=0, masked=False, std=2.5):
@@ -116,14 +116,36 @@ def test_equal_logits(v, dtype):
 
 
 @pytest.mark.parametrize("dtype", [B, F])
-@pytest.mark.parametrize("v", [100, 6000])
+@pytest.mark.parametrize("v", [100, 1025, 6000, 20000, 200000])
 def test_ascending_logits(v, dtype):
     """Each better than all before it."""
     note(f"logprobs ascending {v} {dtype}")
-    x = dev(np.stack([np.arange(v) * 0.25, -np.arange(v) * 0.25]), dtype)
+    x = dev(np.stack([np.arange(v) * 0.01, -np.arange(v) * 0.01]), dtype)
     for top in (3, 64):
         s = gdn.LogitsShape(v, dtype, top)
         t = dev(np.array([v - 2, 1]), torch.int32)
+        check_forward(s, x, t, None, logprobs(s, x, t))
+
+
+@pytest.mark.parametrize("dtype", [B, F])
+@pytest.mark.parametrize("v", [64, 1024, 1025, 8192, 8193, 131073, 300000])
+def test_few_tokens_left(v, dtype):
+    """A grammar leaves three tokens of the vocabulary, or none; all the best lie together, or all
+    in one block; more alternatives are asked for than have any probability."""
+    note(f"logprobs few left {v} {dtype}")
+    rng = np.random.default_rng(v)
+    x = np.full((5, v), -np.inf)
+    x[0, rng.permutation(v)[:3]] = [1, -2, 1]
+    x[2] = rng.standard_normal(v)
+    x[2, v // 3: v // 3 + 130] += 20
+    x[3] = rng.standard_normal(v)
+    x[3, :min(v, 9000)] += 8 + 0.001 * np.arange(min(v, 9000))
+    x[4] = -3
+    x[4, v - 1] = -2
+    x = dev(x, dtype)
+    t = dev(np.argmax(f64(x), 1), torch.int32)
+    for top in (1, 20, 64):
+        s = gdn.LogitsShape(v, dtype, top)
         check_forward(s, x, t, None, logprobs(s, x, t))
 
 

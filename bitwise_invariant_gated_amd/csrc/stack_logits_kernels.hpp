@@ -1,12 +1,12 @@
 // From rows of logits: log probabilities, entropy, top alternatives, the
 // divergence from a teacher's entries, and their gradients.
 //
-// A row is cut into parts of 2,048 columns, a wave to a part.  A part's record
-// is its largest logit m, l = sum e^(c (s - m)) and a = sum (s - m) e^(c (s - m)),
-// c the row's scale; the records of a row are joined by one wave,
-//   M = max m,  f = e^(c (m - M)),  l' = sum l f,  a' = sum (a + l (m - M)) f,
-// in an order that the row's length fixes.  Then log q = c (s - M) - log l' and
-// the entropy is log l' - c a' / l'.  A record needs no running maximum: the
+// A row is cut into parts of 2,048 columns, a wave to a part.  With c the row's
+// scale times log2 e, a part's record is its largest logit m, l = sum 2^t and a =
+// sum t 2^t over t = c (x - m); the records of a row are joined by one wave,
+//   M = max m,  u = c (m - M),  l' = sum l 2^u,  a' = sum (a + l u) 2^u,
+// in an order that the row's length fixes.  Then log q = scale (x - M) - log l'
+// and the entropy is log l' - ln 2 a' / l'.  A record needs no running maximum: the
 // wave holds its part in registers, so its maximum comes first.
 //
 // Top alternatives, by (logit, then lowest index): the parts also note the
@@ -29,7 +29,7 @@ constexpr int kGroup = 128;                     // columns of a noted maximum
 constexpr int kGroups = kPart / kGroup;
 constexpr int kMaxParts = (1 << 20) / kPart;
 constexpr int kWaves = 4;                       // waves of a work-group
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct LogitsArgs {
   const void* logits;
@@ -121,27 +121,64 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_parts(const LogitsArgs a)
     m = max_groups(max_16(max3(max3(m8[0], m8[1], m8[2]), m8[3], m8[3])));
   }
   const float ref = m == -__builtin_inff() ? 0.f : m;
-  float l[kVecs], s[kVecs];
+  // The exponent in one operation, t = c x - fl(c m): what rounding left of c m is
+  // common to all and taken off the sums.  Where c m is so large that t would lose
+  // its bits, in two.
+  const float cm = c * ref, rest = __builtin_fmaf(c, ref, -cm);
+  const bool large = __builtin_amdgcn_readfirstlane(!(__builtin_fabsf(cm) < 256.f));
+  float l[kVecs], s[kVecs], lt, st = 0.f;
+  if (!large) {
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    l[j] = s[j] = 0.f;
+    for (int j = 0; j < kVecs; ++j) {
+      l[j] = s[j] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = x[j][i] - ref;
-      const float e = exp2_fast(d * c);
-      l[j] += e;
-      // a masked column counts 0 * finite, not 0 * -inf
-      if constexpr (ENTROPY) s[j] = __builtin_fmaf(e, fmaxf(d, -0x1p100f), s[j]);
+      for (int i = 0; i < 8; ++i) {
+        const float t = __builtin_fmaf(x[j][i], c, -cm), e = exp2_fast(t);
+        l[j] += e;
+        if constexpr (ENTROPY) s[j] = __builtin_fmaf(e, t, s[j]);
+      }
     }
+    lt = sum_lanes<64>((l[0] + l[1]) + (l[2] + l[3]));
+    if constexpr (ENTROPY) {
+      st = sum_lanes<64>((s[0] + s[1]) + (s[2] + s[3]));
+      if (__builtin_amdgcn_readfirstlane(st != st)) {  // masked columns: 0 * -inf is to count 0
+        float again = cm;
+        asm("" : "+v"(again));  // or the exponentials above would be kept for this, in 64 more registers
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+          s[j] = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float t = __builtin_fmaf(x[j][i], c, -again);
+            s[j] = __builtin_fmaf(exp2_fast(t), fmaxf(t, -0x1p100f), s[j]);
+          }
+        }
+        st = sum_lanes<64>((s[0] + s[1]) + (s[2] + s[3]));
+      }
+    }
+    const float f = 1.f - rest * kLn2;
+    st = (st - rest * lt) * f;
+    lt *= f;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      l[j] = s[j] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = (x[j][i] - ref) * c, e = exp2_fast(t);
+        l[j] += e;
+        if constexpr (ENTROPY) s[j] = __builtin_fmaf(e, fmaxf(t, -0x1p100f), s[j]);
+      }
+    }
+    lt = sum_lanes<64>((l[0] + l[1]) + (l[2] + l[3]));
+    if constexpr (ENTROPY) st = sum_lanes<64>((s[0] + s[1]) + (s[2] + s[3]));
   }
-  const float lt = sum_lanes<64>((l[0] + l[1]) + (l[2] + l[3]));
-  const float st = ENTROPY ? sum_lanes<64>((s[0] + s[1]) + (s[2] + s[3])) : 0.f;
   if (lane == 0) a.rec[row * a.parts + part] = f32x4{m, lt, st, 0.f};
 }
 
 // What a row's records add up to.
 struct RowSum {
-  float m, l, a;   // largest logit, sum of exponentials, and with weights s - m
+  float m, l, a;   // largest logit, sum of exponentials, sum of exponents times exponentials
   float log_l;     // 0 in a row of -inf only
   bool none;       // such a row
 };
@@ -169,9 +206,9 @@ __device__ __forceinline__ RowSum join_records(const LogitsArgs& a, float c, con
   for (int i = 0; i < kMaxParts / 64; ++i) {
     if (i * 64 >= a.parts) break;
     if (q.r[i][1] != 0.f) {  // a part of masked columns only has nothing to add
-      const float d = q.r[i][0] - m, f = exp2_fast(d * c);
+      const float t = (q.r[i][0] - m) * c, f = exp2_fast(t);
       l = __builtin_fmaf(q.r[i][1], f, l);
-      s = __builtin_fmaf(__builtin_fmaf(q.r[i][1], fmaxf(d, -0x1p100f), q.r[i][2]), f, s);
+      s = __builtin_fmaf(__builtin_fmaf(q.r[i][1], fmaxf(t, -0x1p100f), q.r[i][2]), f, s);
     }
   }
   RowSum t;
@@ -179,6 +216,7 @@ __device__ __forceinline__ RowSum join_records(const LogitsArgs& a, float c, con
   t.l = sum_lanes<64>(l);
   t.a = sum_lanes<64>(s);
   t.none = t.l == 0.f;
+  if (t.l < 1.f && !t.none) t.l = 1.f;  // the largest logit's own share, but for rounding: log q is never above 0
   t.log_l = t.none ? 0.f : logf(t.l);
   return t;
 }
@@ -540,7 +578,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs(const LogitsArgs
   const RowSum t = join_records(a, scale * kLog2e, q);
   if (lane == 0) {
     if (a.targets) a.logprobs[row] = log_q(t, scale, at_target);
-    if (a.entropy) a.entropy[row] = t.none ? 0.f : t.log_l - scale * (t.a / t.l);
+    if (a.entropy) a.entropy[row] = t.none ? 0.f : t.log_l - kLn2 * (t.a / t.l);
     if (a.stats) {
       a.stats[2 * row] = t.m;
       a.stats[2 * row + 1] = t.log_l;

@@ -90,14 +90,14 @@ def _row_args(t, rows, width: int, dtype, name: str):
         raise ValueError(f"{name}: [{'rows' if rows is None else rows}, {width}] of {dtype} expected, "
                          f"{tuple(shape)} of {t.dtype} given")
     n = shape[0]
+    if t.is_contiguous():  # the usual case, and a fifth cheaper than to ask for the strides
+        return n, t.data_ptr(), 0
     s0, s1 = t.stride()
-    if n and width > 1 and s1 != 1:
+    if width > 1 and s1 != 1:
         raise ValueError(f"{name}: a row's elements must be contiguous")
-    if n <= 1:
-        s0 = 0  # a single row's stride is not used
-    elif s0 < width:
+    if n > 1 and s0 < width:
         raise ValueError(f"{name}: rows overlap")
-    return n, t.data_ptr(), s0
+    return n, t.data_ptr(), s0 if n > 1 else 0
 
 
 def _whole(t, shape: tuple, dtype, name: str):

@@ -4,9 +4,13 @@ softmax attention over the 8-bit paged cache.
     python examples/hybrid_generate.py
 
 Random weights.  The prompts are prefilled in one packed batch, then tokens are
-generated step by step: one block plan per step serves every attention layer.
-At the end the prompts with what was generated are prefilled again, and the
-hidden states of all generated positions are compared bit for bit.  The
+generated step by step: one block plan per step serves every attention layer,
+one call between two layers adds to the residual stream and norms it, and one
+call after the last gives the best tokens with their log probabilities.
+At the end the prompts with what was generated are prefilled again, as a trainer
+would: the hidden states of all generated positions and the log probabilities of
+their tokens are compared bit for bit, and the divergence of the trainer's
+distributions from the alternatives that generation noted is exactly 0.  The
 projections are library products; they run on tiles of a fixed number of rows,
 so that a row's bits do not depend on the batch it is in.
 """
@@ -37,8 +41,9 @@ def project(x, w):
     return y
 
 
-def rms(x):
-    return torch.nn.functional.rms_norm(x.float(), x.shape[-1:], eps=1e-6).to(x.dtype)
+def same_bits(a, b):
+    view = torch.int16 if a.element_size() == 2 else torch.int32
+    return torch.equal(a.contiguous().view(view), b.contiguous().view(view))
 
 
 class DeltaNetLayer:
@@ -104,6 +109,7 @@ class Model:
             return (torch.randn(shape, generator=gen, device=dev) * shape[0] ** -0.5).bfloat16()
 
         self.dev, self.embed, self.head = dev, rand(vocab, width) * vocab ** 0.5, rand(width, vocab)
+        self.norm, self.weights = gdn.NormShape(width), torch.ones((layers + 1, width), device=dev)
         self.layers = [AttentionLayer(width, attn_heads, kv_heads, attn_d, rand, dev, max_len) if i % 4 == 3
                        else DeltaNetLayer(width, heads, d, rand) for i in range(layers)]
 
@@ -115,47 +121,83 @@ class Model:
             layer.begin(seqs, self.pool, self.dev)
 
     def step(self, tokens, lens, decode=False):
-        """Hidden states of the given new tokens, lens[i] of request i, packed."""
+        """The residual stream after the last layer and its norm for the given new tokens, lens[i] of
+        request i, packed."""
         cu = torch.tensor([0] + list(lens), device=self.dev).cumsum(0).to(torch.int32)
         plan = gdn.alloc_attn_plan(self.pool, len(lens), tokens.numel())
         gdn.gdn_attn_plan(self.pool, cu, plan)
         x = self.embed[tokens]
-        for layer in self.layers:
-            x = x + layer(rms(x), cu, plan, plan.positions, decode)
-        return x
+        y = torch.empty_like(x)
+        gdn.gdn_stack_add_norm(self.norm, x, None, self.weights[0], None, y)
+        for layer, w in zip(self.layers, self.weights[1:]):
+            gdn.gdn_stack_add_norm(self.norm, layer(y, cu, plan, plan.positions, decode), x, w, x, y)
+        return x, y
 
-    def next_tokens(self, hidden):
-        return project(rms(hidden), self.head).argmax(-1)
+    def score(self, y, targets=None, top=0):
+        """(logits, log probabilities of the targets, entropy, ids and log probabilities of the best
+        tokens, statistics) of every row."""
+        logits = project(y, self.head)
+        t, dev = logits.shape[0], self.dev
+        shape = gdn.LogitsShape(self.head.shape[1], top=top)
+        logprobs = None if targets is None else torch.empty(t, device=dev)
+        entropy, stats = torch.empty(t, device=dev), torch.empty((t, 2), device=dev)
+        ids, best = torch.empty((t, top), dtype=torch.int32, device=dev), torch.empty((t, top), device=dev)
+        gdn.gdn_stack_logprobs(shape, logits, targets, logprobs, entropy, ids if top else None, best if top else None, stats,
+                               gdn.alloc_logits_workspace(shape, t, dev))
+        return logits, logprobs, entropy, ids, best, stats
+
+    def head_gradients(self, x, y, targets, g):
+        """Gradients of sum g log p(targets) with respect to the stream x, the last norm's weights and
+        the head, from step's outputs."""
+        logits, _, entropy, _, _, stats = self.score(y, targets)
+        gdn.gdn_stack_logprobs_bwd(gdn.LogitsShape(logits.shape[1]), logits, targets, stats, entropy, g, None, logits)
+        dx, dw = torch.empty_like(x), torch.empty_like(self.weights[-1])
+        gdn.gdn_stack_add_norm_bwd(self.norm, x, self.weights[-1], logits @ self.head.t(), None, dx, None, dw,
+                                   gdn.alloc_norm_workspace(self.norm, x.shape[0], self.dev))
+        return dx, dw, y.t() @ logits
 
 
-def generate(model, prompts, steps):
-    """(tokens [steps + 1, N], hidden states [steps, N, width] of all but the last) after the prompts."""
+def generate(model, prompts, steps, top=8):
+    """After the prompts: tokens [steps + 1, N], the stream [steps, N, width] at all but the last, and
+    of every token the ids and log probabilities of the best, its own first."""
     lens = [p.numel() for p in prompts]
     model.begin(len(prompts), max(lens) + steps + 1)
-    hidden = model.step(torch.cat(prompts), lens)
     last = torch.tensor(lens, device=model.dev).cumsum(0) - 1
-    tokens, states = [model.next_tokens(hidden[last])], []
-    for _ in range(steps):
-        states.append(model.step(tokens[-1], [1] * len(prompts), decode=True))
-        tokens.append(model.next_tokens(states[-1]))
-    return torch.stack(tokens), torch.stack(states)
+    y, states, ids, best = model.step(torch.cat(prompts), lens)[1][last], [], [], []
+    for i in range(steps + 1):
+        _, _, _, k, lp, _ = model.score(y, top=top)
+        ids.append(k)
+        best.append(lp)
+        if i < steps:
+            x, y = model.step(k[:, 0].long(), [1] * len(prompts), decode=True)
+            states.append(x)
+    ids = torch.stack(ids)
+    return ids[:, :, 0].long(), torch.stack(states), ids, torch.stack(best)
 
 
 def main(lens=(5, 64, 200, 1), steps=70, **kw):
     model = Model(**kw)
     gen = torch.Generator(model.dev).manual_seed(1)
     prompts = [torch.randint(0, model.embed.shape[0], (n,), generator=gen, device=model.dev) for n in lens]
-    tokens, states = generate(model, prompts, steps)
-    assert torch.isfinite(states).all()
+    tokens, states, ids, best = generate(model, prompts, steps)
+    assert torch.isfinite(states).all() and torch.isfinite(best).all()
     # all of it again, as one prefill
     whole = [torch.cat([p, tokens[:steps, i]]) for i, p in enumerate(prompts)]
     total = [w.numel() for w in whole]
     model.begin(len(whole), max(total))
-    again = torch.split(model.step(torch.cat(whole), total), total)
-    for i, n in enumerate(lens):
-        same = torch.equal(again[i][n:].view(torch.int16), states[:, i].contiguous().view(torch.int16))
-        assert same, f"request {i}: prefill and decode differ"
-    print(f"{len(lens)} requests, {steps} steps: decode == prefill bit for bit; first tokens {tokens[:4, 0].tolist()}")
+    x, y = model.step(torch.cat(whole), total)
+    for i, (n, hidden, normed) in enumerate(zip(lens, torch.split(x, total), torch.split(y, total))):
+        assert same_bits(hidden[n:], states[:, i]), f"request {i}: prefill and decode differ"
+        # position n - 1 + j gives token j
+        logits, logprobs, _, _, _, _ = model.score(normed[n - 1:], tokens[:, i].to(torch.int32).contiguous())
+        assert same_bits(logprobs, best[:, i, 0]), f"request {i}: log probabilities differ"
+        shape = gdn.LogitsShape(logits.shape[1], top=ids.shape[2], teacher_logprobs=True)
+        loss = torch.empty_like(logprobs)
+        gdn.gdn_stack_distill(shape, logits, ids[:, i].contiguous(), best[:, i].contiguous(), loss, None,
+                              gdn.alloc_logits_workspace(shape, loss.numel(), model.dev))
+        assert (loss == 0).all(), f"request {i}: divergence {loss.max()}"
+    print(f"{len(lens)} requests, {steps} steps: decode == prefill bit for bit, states, log probabilities and {ids.shape[2]} "
+          f"alternatives; first tokens {tokens[:4, 0].tolist()}")
     return tokens
 
 

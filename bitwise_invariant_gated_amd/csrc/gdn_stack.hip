@@ -55,11 +55,13 @@ size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
     if ((uintptr_t)(p) % (to) != 0) return fail(GDN_ERR_INVALID_ARG, "%s: %s is not %d-byte aligned", fn, name, (int)(to)); \
   } while (0)
 
-#define CHECK_PTR(p, name)                                                  \
+#define CHECK_PTR_TO(p, name, to)                                           \
   do {                                                                      \
     if (!(p)) return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, name); \
-    CHECK_ALIGN(p, name, 16);                                               \
+    CHECK_ALIGN(p, name, to);                                               \
   } while (0)
+
+#define CHECK_PTR(p, name) CHECK_PTR_TO(p, name, 16)
 
 #define CHECK(call)               \
   do {                            \
@@ -108,6 +110,9 @@ gdn_status check_in_place(const char* fn, const void* out, int64_t out_stride, i
 // ---------------------------------------------------------------------------
 // norm
 
+// A launch counts its threads in 32 bits.
+constexpr int64_t kMostThreads = (int64_t(1) << 32) - 4096;
+
 gdn_status check_norm(const char* fn, const gdn_norm_shape* s, int64_t rows) {
   if (!s) return fail(GDN_ERR_INVALID_ARG, "%s: shape is NULL", fn);
   if (s->width < 8 || s->width > GDN_STACK_MAX_WIDTH || s->width % 8 != 0)
@@ -121,7 +126,10 @@ gdn_status check_norm(const char* fn, const gdn_norm_shape* s, int64_t rows) {
   if (s->group > 0 && s->width % s->group != 0)
     return fail(GDN_ERR_UNSUPPORTED, "%s: group must divide width", fn);
   if (!(s->eps >= 0.f) || std::isinf(s->eps)) return fail(GDN_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
-  return check_rows(fn, rows);
+  CHECK(check_rows(fn, rows));
+  if (rows * (s->width <= 128 ? 16 : s->width <= 2048 ? 64 : 256) > kMostThreads)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: too many rows", fn);
+  return GDN_OK;
 }
 
 // Calls that move more than this read past the caches what is read for the last
@@ -320,7 +328,7 @@ gdn_status check_logits_shape(const char* fn, const gdn_logits_shape* s, int64_t
   if (s->top < 0 || s->top > GDN_STACK_MAX_TEACHER)
     return fail(GDN_ERR_UNSUPPORTED, "%s: top must be in [0, %d]", fn, GDN_STACK_MAX_TEACHER);
   CHECK(check_rows(fn, rows));
-  if (rows * ((s->vocab + kPart - 1) / kPart) > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%s: too many rows", fn);
+  if (rows * ((s->vocab + kPart - 1) / kPart) > kMostThreads / 64) return fail(GDN_ERR_UNSUPPORTED, "%s: too many rows", fn);
   return GDN_OK;
 }
 
@@ -342,7 +350,7 @@ gdn_status check_logits(const char* fn, const gdn_logits_shape* s, int64_t rows,
   CHECK(check_logits_shape(fn, s, rows));
   CHECK(check_stride(fn, "logits_stride", stride, s->vocab, 1, &a->stride));
   CHECK_ALIGN(logits, "logits", element_size(*s));
-  CHECK_ALIGN(scale, "scale", 16);
+  CHECK_ALIGN(scale, "scale", 4);
   if (rows > 0 && !logits) return fail(GDN_ERR_INVALID_ARG, "%s: logits is NULL", fn);
   a->logits = logits;
   a->rows = rows;
@@ -445,12 +453,12 @@ extern "C" gdn_status gdn_stack_logprobs(const gdn_logits_shape* shape, int64_t 
   LogitsArgs a{};
   CHECK(check_logits(fn, shape, num_rows, logits, logits_stride, scale, &a));
   CHECK(check_top(fn, *shape));
-  CHECK_ALIGN(targets, "targets", 16);
-  CHECK_ALIGN(logprobs, "logprobs", 16);
-  CHECK_ALIGN(entropy, "entropy", 16);
-  CHECK_ALIGN(top_ids, "top_ids", 16);
-  CHECK_ALIGN(top_logprobs, "top_logprobs", 16);
-  CHECK_ALIGN(stats, "stats", 16);
+  CHECK_ALIGN(targets, "targets", 4);
+  CHECK_ALIGN(logprobs, "logprobs", 4);
+  CHECK_ALIGN(entropy, "entropy", 4);
+  CHECK_ALIGN(top_ids, "top_ids", 4);
+  CHECK_ALIGN(top_logprobs, "top_logprobs", 4);
+  CHECK_ALIGN(stats, "stats", 4);
   if (num_rows == 0) return done();
   if (!targets != !logprobs) return fail(GDN_ERR_INVALID_ARG, "%s: targets and logprobs go together", fn);
   if (shape->top && (!top_ids || !top_logprobs))
@@ -478,12 +486,12 @@ extern "C" gdn_status gdn_stack_logprobs_bwd(const gdn_logits_shape* shape, int6
   LogitsArgs a{};
   CHECK(check_logits(fn, shape, num_rows, logits, logits_stride, scale, &a));
   CHECK(check_gradient(fn, *shape, d_logits, d_logits_stride, &a));
-  CHECK_ALIGN(targets, "targets", 16);
-  CHECK_ALIGN(entropy, "entropy", 16);
-  CHECK_ALIGN(d_logprobs, "d_logprobs", 16);
-  CHECK_ALIGN(d_entropy, "d_entropy", 16);
+  CHECK_ALIGN(targets, "targets", 4);
+  CHECK_ALIGN(entropy, "entropy", 4);
+  CHECK_ALIGN(d_logprobs, "d_logprobs", 4);
+  CHECK_ALIGN(d_entropy, "d_entropy", 4);
   if (num_rows == 0) return done();
-  CHECK_PTR(stats, "stats");
+  CHECK_PTR_TO(stats, "stats", 4);
   if (!d_logprobs && !d_entropy) return fail(GDN_ERR_INVALID_ARG, "%s: d_logprobs and d_entropy are both NULL", fn);
   if (d_logprobs && !targets) return fail(GDN_ERR_INVALID_ARG, "%s: d_logprobs needs targets", fn);
   if (d_entropy && !entropy) return fail(GDN_ERR_INVALID_ARG, "%s: d_entropy needs entropy", fn);
@@ -506,9 +514,9 @@ extern "C" gdn_status gdn_stack_distill(const gdn_logits_shape* shape, int64_t n
   CHECK(check_entries(fn, *shape));
   CHECK_ALIGN(stats, "stats", 16);
   if (num_rows == 0) return done();
-  CHECK_PTR(teacher_ids, "teacher_ids");
-  CHECK_PTR(teacher_values, "teacher_values");
-  CHECK_PTR(loss, "loss");
+  CHECK_PTR_TO(teacher_ids, "teacher_ids", 4);
+  CHECK_PTR_TO(teacher_values, "teacher_values", 4);
+  CHECK_PTR_TO(loss, "loss", 4);
   CHECK(check_workspace(fn, workspace, workspace_bytes, gdn_stack_logits_workspace_size(shape, num_rows)));
   a.ids = teacher_ids;
   a.values = teacher_values;
@@ -530,10 +538,10 @@ extern "C" gdn_status gdn_stack_distill_bwd(const gdn_logits_shape* shape, int64
   CHECK(check_entries(fn, *shape));
   CHECK(check_gradient(fn, *shape, d_logits, d_logits_stride, &a));
   if (num_rows == 0) return done();
-  CHECK_PTR(teacher_ids, "teacher_ids");
-  CHECK_PTR(teacher_values, "teacher_values");
+  CHECK_PTR_TO(teacher_ids, "teacher_ids", 4);
+  CHECK_PTR_TO(teacher_values, "teacher_values", 4);
   CHECK_PTR(stats, "stats");
-  CHECK_PTR(d_loss, "d_loss");
+  CHECK_PTR_TO(d_loss, "d_loss", 4);
   a.ids = teacher_ids;
   a.values = teacher_values;
   a.in_stats = stats;

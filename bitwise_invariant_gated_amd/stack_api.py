@@ -15,7 +15,6 @@ import torch
 
 from . import _lib
 from .api import _DTYPES, _ptr
-from .attn_api import _stream
 
 
 @dataclasses.dataclass(frozen=True)
@@ -115,6 +114,22 @@ def _weight(w, width: int, name: str):
     return w.data_ptr()
 
 
+def _stream(stream, *tensors) -> int:
+    """The handle of the stream, or of the current one; the tensors have to be on its device, and that
+    has to be the current one."""
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device or device < 0:
+            raise ValueError(f"a tensor is on {t.device}, the first one on {tensors[0].device}")
+    if device != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{device}, which is not the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is of cuda:{stream.device_index}, the tensors are on cuda:{device}")
+    return stream.cuda_stream
+
+
 def _bytes(workspace):
     return _ptr(workspace), workspace.numel() * workspace.element_size()
 
@@ -129,7 +144,8 @@ def gdn_stack_add_norm(shape: NormShape, x, residual, w, residual_out, y, y8=Non
     _, yp, ys = _row_args(y, n, width, dt, "y")
     _lib.check(_lib.load().gdn_stack_add_norm(
         shape._ref, n, xp, xs, rp, rs, _weight(w, width, "w"), hp, hs, yp, ys, _whole(y8, (n, width), torch.uint8, "y8"),
-        _whole(y_scale, (n, width // shape.group if shape.group > 0 else 1), torch.float32, "y_scale"), _stream(stream)))
+        _whole(y_scale, (n, width // shape.group if shape.group > 0 else 1), torch.float32, "y_scale"),
+        _stream(stream, x, residual, w, residual_out, y, y8, y_scale)))
 
 
 def gdn_stack_add_norm_bwd(shape: NormShape, h, w, dy, d_residual_out, dx, d_residual, dw, workspace,
@@ -145,7 +161,7 @@ def gdn_stack_add_norm_bwd(shape: NormShape, h, w, dy, d_residual_out, dx, d_res
     _, dp, ds = _row_args(d_residual, n, width, rdt, "d_residual")
     _lib.check(_lib.load().gdn_stack_add_norm_bwd(
         shape._ref, n, hp, hs, _weight(w, width, "w"), yp, ys, rp, rs, xp, xs, dp, ds, _weight(dw, width, "dw"),
-        *_bytes(workspace), _stream(stream)))
+        *_bytes(workspace), _stream(stream, h, w, dy, d_residual_out, dx, d_residual, dw, workspace)))
 
 
 def gdn_stack_logprobs(shape: LogitsShape, logits, targets, logprobs, entropy, top_ids, top_logprobs, stats, workspace,
@@ -159,7 +175,8 @@ def gdn_stack_logprobs(shape: LogitsShape, logits, targets, logprobs, entropy, t
         shape._ref, n, lp, ls, _whole(targets, (n,), i32, "targets"), _whole(scale, (n,), f32, "scale"),
         _whole(logprobs, (n,), f32, "logprobs"), _whole(entropy, (n,), f32, "entropy"),
         _whole(top_ids, (n, k), i32, "top_ids"), _whole(top_logprobs, (n, k), f32, "top_logprobs"),
-        _whole(stats, (n, 2), f32, "stats"), *_bytes(workspace), _stream(stream)))
+        _whole(stats, (n, 2), f32, "stats"), *_bytes(workspace),
+        _stream(stream, logits, targets, scale, logprobs, entropy, top_ids, top_logprobs, stats, workspace)))
 
 
 def gdn_stack_logprobs_bwd(shape: LogitsShape, logits, targets, stats, entropy, d_logprobs, d_entropy, d_logits,
@@ -172,7 +189,8 @@ def gdn_stack_logprobs_bwd(shape: LogitsShape, logits, targets, stats, entropy, 
     _lib.check(_lib.load().gdn_stack_logprobs_bwd(
         shape._ref, n, lp, ls, _whole(targets, (n,), torch.int32, "targets"), _whole(scale, (n,), f32, "scale"),
         _whole(stats, (n, 2), f32, "stats"), _whole(entropy, (n,), f32, "entropy"),
-        _whole(d_logprobs, (n,), f32, "d_logprobs"), _whole(d_entropy, (n,), f32, "d_entropy"), dp, ds, _stream(stream)))
+        _whole(d_logprobs, (n,), f32, "d_logprobs"), _whole(d_entropy, (n,), f32, "d_entropy"), dp, ds,
+        _stream(stream, logits, targets, scale, stats, entropy, d_logprobs, d_entropy, d_logits)))
 
 
 def gdn_stack_distill(shape: LogitsShape, logits, teacher_ids, teacher_values, loss, stats, workspace, scale=None,
@@ -183,7 +201,8 @@ def gdn_stack_distill(shape: LogitsShape, logits, teacher_ids, teacher_values, l
     _lib.check(_lib.load().gdn_stack_distill(
         shape._ref, n, lp, ls, _whole(teacher_ids, (n, k), torch.int32, "teacher_ids"),
         _whole(teacher_values, (n, k), f32, "teacher_values"), _whole(scale, (n,), f32, "scale"),
-        _whole(loss, (n,), f32, "loss"), _whole(stats, (n, 4), f32, "stats"), *_bytes(workspace), _stream(stream)))
+        _whole(loss, (n,), f32, "loss"), _whole(stats, (n, 4), f32, "stats"), *_bytes(workspace),
+        _stream(stream, logits, teacher_ids, teacher_values, scale, loss, stats, workspace)))
 
 
 def gdn_stack_distill_bwd(shape: LogitsShape, logits, teacher_ids, teacher_values, stats, d_loss, d_logits, scale=None,
@@ -195,4 +214,5 @@ def gdn_stack_distill_bwd(shape: LogitsShape, logits, teacher_ids, teacher_value
     _lib.check(_lib.load().gdn_stack_distill_bwd(
         shape._ref, n, lp, ls, _whole(teacher_ids, (n, k), torch.int32, "teacher_ids"),
         _whole(teacher_values, (n, k), f32, "teacher_values"), _whole(scale, (n,), f32, "scale"),
-        _whole(stats, (n, 4), f32, "stats"), _whole(d_loss, (n,), f32, "d_loss"), dp, ds, _stream(stream)))
+        _whole(stats, (n, 4), f32, "stats"), _whole(d_loss, (n,), f32, "d_loss"), dp, ds,
+        _stream(stream, logits, teacher_ids, teacher_values, scale, stats, d_loss, d_logits)))

@@ -21,12 +21,16 @@
  * Conventions: those of gdn_cpr.h (device pointers; calls only enqueue on
  * `stream`; nothing is allocated; host-detectable errors return a status
  * before anything is enqueued; gdn_cpr_last_error describes the last one).
- * Pointers are 16-byte aligned; logits and their gradients need the alignment
- * of their elements only, so that they may be any rows of a larger array.
+ * Pointers are 16-byte aligned; logits, their gradients and the arrays of
+ * numbers to a row that go with them (all but distill's stats) need the
+ * alignment of their elements only, so that they may be any rows of larger ones.
  * A stride is the distance in elements between a tensor's rows; 0 means that
  * they are contiguous.  Rows of the norm's tensors have strides that are
  * multiples of 8 and at least the width; those of logits any stride of at
  * least the vocabulary, and what lies between two rows is left as it is.
+ * A launch's threads are counted in 32 bits: rows up to 2^24 - 16 of a width
+ * past 2,048 (2^26 - 64 up to that, 2^28 - 256 up to 128), and of logits rows *
+ * ceil(vocab / 2,048) up to 2^26 - 64.
  */
 #ifndef GDN_STACK_H
 #define GDN_STACK_H

@@ -226,3 +226,17 @@ def test_on_other_streams_at_once():
     gdn.gdn_stack_add_norm(n, c.x, c.res, c.w, c.h, c.y, stream=streams[1])
     streams[1].synchronize()
     assert same_bits(c.h, wants[0][0])
+
+
+def test_rows_of_larger_arrays():
+    """Any rows of the logits with the same rows of what goes with them, at the alignment of an element."""
+    note("later rows")
+    t, v = 13, 10007
+    for dtype in (B, F):
+        x, target, scale = make(t, v, dtype, seed=5)
+        ids, values = make_teacher(t, v, 7)
+        g = dev(np.linspace(-1, 1, t))
+        want = everything(v, dtype, x, target, scale, ids, values, g, k=7)
+        for a in (1, 2, 3, 5):
+            got = everything(v, dtype, *(u[a:] for u in (x, target, scale, ids, values, g)), k=7)
+            assert all(same_bits(p, q[a:]) for p, q in zip(got, want)), a

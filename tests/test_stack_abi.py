@@ -100,6 +100,8 @@ def test_add_norm_refusals(lib):
     assert call(h=P, hs=72) == INVALID and call(y=P, ys=72) == INVALID and call(h=2 * P, hs=72) == INVALID
     assert call(s=norm(residual=F32), h=P) == INVALID and call(s=norm(residual=F32), y=2 * P) == INVALID
     assert call(n=0, x=None, y=None) == OK
+    # a launch's threads are counted in 32 bits
+    assert call(s=norm(4096), n=(1 << 24) - 15) == UNSUPPORTED and "too many" in said(lib)
 
 
 def test_add_norm_bwd_refusals(lib):
@@ -124,13 +126,15 @@ def test_logprobs_refusals(lib):
     assert call(s=None) == INVALID and call(n=-1) == INVALID and call(n=1 << 31) == UNSUPPORTED
     assert call(s=logits(top=65)) == UNSUPPORTED and call(s=logits(vocab=2, top=3)) == UNSUPPORTED and "top" in said(lib)
     for kw, name in ((dict(x=None), "logits"), (dict(x=P + 1), "logits"), (dict(x=P + 2, s=logits(dtype=F32)), "logits"), (dict(xs=99), "logits_stride"),
-                     (dict(t=P + 4), "targets"), (dict(sc=P + 4), "scale"), (dict(lp=P + 4), "logprobs"), (dict(en=P + 4), "entropy"),
-                     (dict(ids=P + 4), "top_ids"), (dict(tlp=P + 4), "top_logprobs"), (dict(st=P + 8), "stats"), (dict(t=None), "together"),
+                     (dict(t=P + 2), "targets"), (dict(sc=P + 2), "scale"), (dict(lp=P + 2), "logprobs"), (dict(en=P + 2), "entropy"),
+                     (dict(ids=P + 2), "top_ids"), (dict(tlp=P + 2), "top_logprobs"), (dict(st=P + 2), "stats"), (dict(t=None), "together"),
                      (dict(lp=None), "together"), (dict(ids=None), "top_ids"), (dict(tlp=None), "top_logprobs"),
                      (dict(s=logits(), t=None, lp=None, en=None, st=None), "no output")):
         assert call(**kw) == INVALID and name in said(lib), kw
     assert call(ws=None) == WORKSPACE and call(size=100) == WORKSPACE and call(ws=P + 8) == INVALID
     assert call(n=0, x=None) == OK
+    assert call(s=logits(vocab=9, top=3), n=(1 << 26) - 63) == UNSUPPORTED and "too many" in said(lib)
+    assert call(s=logits(vocab=4097, top=3), n=1 << 25) == UNSUPPORTED
 
 
 def test_logprobs_bwd_refusals(lib):
@@ -139,7 +143,7 @@ def test_logprobs_bwd_refusals(lib):
 
     for kw, name in ((dict(x=None), "logits"), (dict(d=None), "d_logits"), (dict(d=P + 1), "d_logits"), (dict(ds=50), "d_logits_stride"), (dict(st=None), "stats"),
                      (dict(g=None, f=None), "both"), (dict(t=None), "targets"), (dict(en=None), "entropy"), (dict(d=P, ds=101), "in place"),
-                     (dict(g=P + 4), "d_logprobs"), (dict(f=P + 4), "d_entropy"), (dict(en=P + 4), "entropy"), (dict(t=P + 4), "targets")):
+                     (dict(g=P + 2), "d_logprobs"), (dict(f=P + 2), "d_entropy"), (dict(en=P + 2), "entropy"), (dict(t=P + 2), "targets")):
         assert call(**kw) == INVALID and name in said(lib), kw
     assert call(n=0, x=None, d=None) == OK
 
@@ -153,7 +157,7 @@ def test_distill_refusals(lib):
 
     assert call(s=logits(top=0)) == UNSUPPORTED and back(s=logits(top=0)) == UNSUPPORTED
     for kw, name in ((dict(x=None), "logits"), (dict(ids=None), "teacher_ids"), (dict(v=None), "teacher_values"), (dict(loss=None), "loss"),
-                     (dict(ids=P + 4), "teacher_ids"), (dict(st=P + 8), "stats"), (dict(xs=3), "logits_stride")):
+                     (dict(ids=P + 2), "teacher_ids"), (dict(st=P + 8), "stats"), (dict(xs=3), "logits_stride")):
         assert call(**kw) == INVALID and name in said(lib), kw
     assert call(ws=None) == WORKSPACE and call(size=10) == WORKSPACE
     for kw, name in ((dict(x=None), "logits"), (dict(ids=None), "teacher_ids"), (dict(v=None), "teacher_values"), (dict(g=None), "d_loss"), (dict(st=None), "stats"),
@@ -161,18 +165,21 @@ def test_distill_refusals(lib):
         assert back(**kw) == INVALID and name in said(lib), kw
 
 
+WRONG = "expected|contiguous|overlap"
+
+
 def test_binding_refusals(lib):
     """Tensors of another shape, type or layout are refused before the library sees them."""
     s = gdn.NormShape(64)
     x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.ones(64)
     for bad in (x.float(), x[:, :32], x.t(), x[None], x.expand(1, 4, 64)[0][:1].expand(4, 64)):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match=WRONG):
             gdn.gdn_stack_add_norm(s, bad, None, w, None, x)
     for kw in (dict(residual=x[:3]), dict(residual_out=x.float()), dict(y=x[:2]), dict(w=w[:8]), dict(w=w.double()), dict(w=torch.ones(128)[::2]),
                dict(y8=torch.zeros(4, 64)), dict(y_scale=torch.zeros(4))):
         args = dict(residual=None, w=w, residual_out=None, y=x)
         args.update(kw)
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match=WRONG):
             gdn.gdn_stack_add_norm(s, x, **args)
     z = gdn.LogitsShape(100, torch.float32, top=2)
     lg, i, f, ws = torch.zeros(4, 100), torch.zeros(4, dtype=torch.int32), torch.zeros(4), torch.zeros(1 << 12, dtype=torch.uint8)
@@ -180,16 +187,33 @@ def test_binding_refusals(lib):
                 stats=torch.zeros(4, 2), workspace=ws)
     for kw in (dict(logits=lg[:, :99]), dict(logits=lg.bfloat16()), dict(targets=i.long()), dict(targets=i[:3]), dict(logprobs=f[:2]),
                dict(top_ids=good["top_ids"].t()), dict(top_logprobs=torch.zeros(4, 3)), dict(stats=f), dict(scale=f[:1])):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match=WRONG):
             gdn.gdn_stack_logprobs(z, **{**good, **kw})
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match=WRONG):
         gdn.gdn_stack_distill(z, lg, good["top_ids"].long(), good["top_logprobs"], f, None, ws)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match=WRONG):
         gdn.gdn_stack_distill_bwd(z, lg, good["top_ids"], good["top_logprobs"], torch.zeros(4, 2), f, lg)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="unsupported"):
         gdn.LogitsShape(10, torch.float16)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="unsupported"):
         gdn.NormShape(64, torch.bfloat16, torch.float64)
+
+
+def test_tensors_off_the_current_device_are_refused(lib):
+    """Kernels run on the current device: memory of the host, or of another, is not theirs to read."""
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.ones(64)
+    with pytest.raises(ValueError, match="on cpu"):
+        gdn.gdn_stack_add_norm(gdn.NormShape(64), x, None, w, None, x)
+    with pytest.raises(ValueError, match="on cpu"):
+        gdn.gdn_stack_add_norm_bwd(gdn.NormShape(64), x, w, x, None, x, None, w, torch.zeros(1 << 16, dtype=torch.uint8))
+    s, lg, i, f, ws = gdn.LogitsShape(64, top=2), x, torch.zeros(4, dtype=torch.int32), torch.zeros(4), torch.zeros(1 << 12, dtype=torch.uint8)
+    ids, values = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    for call in (lambda: gdn.gdn_stack_logprobs(s, lg, i, f, None, ids, values, None, ws),
+                 lambda: gdn.gdn_stack_logprobs_bwd(s, lg, i, torch.zeros(4, 2), None, f, None, lg),
+                 lambda: gdn.gdn_stack_distill(s, lg, ids, values, f, None, ws),
+                 lambda: gdn.gdn_stack_distill_bwd(s, lg, ids, values, torch.zeros(4, 4), f, lg)):
+        with pytest.raises(ValueError, match="on cpu"):
+            call()
 
 
 @pytest.mark.parametrize("how", [copy.deepcopy, lambda x: pickle.loads(pickle.dumps(x))])

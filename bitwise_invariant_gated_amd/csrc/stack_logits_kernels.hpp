@@ -412,9 +412,10 @@ __device__ __forceinline__ void load_groups(const LogitsArgs& a, int64_t row, in
 }
 
 // The values of a row's first search: lane l's are those of columns 16 l .. 16 l
-// + 15, of units 16 l .. of 8 columns, or of part l (of up to 64 parts).
+// + 15, of units 16 l .. of 8 columns, or of part l (of up to 64 parts).  turn:
+// LDS for 1,024 of them.
 template <class E, int MODE>
-__device__ __forceinline__ void load_values(const LogitsArgs& a, int64_t row, int lane, float (&x)[kHeld]) {
+__device__ __forceinline__ void load_values(const LogitsArgs& a, int64_t row, int lane, float* turn, float (&x)[kHeld]) {
   const typename E::T* p = (const typename E::T*)a.logits + row * a.stride;
   if constexpr (MODE == kTopColumns) {
 #pragma unroll
@@ -424,16 +425,21 @@ __device__ __forceinline__ void load_values(const LogitsArgs& a, int64_t row, in
       for (int i = 0; i < 8; ++i) x[8 * h + i] = held(f[i], kHeld * lane + 8 * h + i < a.vocab);
     }
   } else if constexpr (MODE == kTopEights) {
-#pragma unroll 4
+    // read unit by unit along the row, handed to their lanes through LDS
+#pragma unroll 8
     for (int i = 0; i < kHeld; ++i) {
-      const int c = (kHeld * lane + i) * 8;
+      const int c = (i * 64 + lane) * 8;
       F8 f = load_eight<E>(p, c, a.vocab);
       float m = -__builtin_inff();
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (c + e < a.vocab) m = fmaxf(m, f[e]);
-      x[i] = held(m, c < a.vocab);
+      turn[i * 64 + lane] = m;
     }
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) x[i] = held(turn[kHeld * lane + i], (kHeld * lane + i) * 8 < a.vocab);
+    wave_sync();
   } else if constexpr (MODE == kTopGroups) {
     if (a.parts <= 64) load_groups(a, row, min(lane, a.parts - 1), lane < a.parts, x);
   }
@@ -571,7 +577,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs(const LogitsArgs
     return;
   }
   float v[kHeld];
-  load_values<E, MODE>(a, row, lane, v);
+  load_values<E, MODE>(a, row, lane, (float*)scratch[MODE ? wave : 0].found, v);
   const float scale = a.scale ? a.scale[row] : 1.f;
   const typename E::T* x = (const typename E::T*)a.logits + row * a.stride;
   const float at_target = a.targets ? E::one(x[a.targets[row]]) : 0.f;
@@ -788,6 +794,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_distill(const LogitsArgs 
 // writes over those that are.
 template <class E, bool ONCE>
 __global__ __launch_bounds__(64 * kWaves) void k_stack_distill_bwd(const LogitsArgs a) {
+  __shared__ uint16_t owner[kWaves][kPart];
   int64_t row;
   int part;
   if (!my_part(a, row, part)) return;
@@ -809,7 +816,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_distill_bwd(const LogitsA
     p[i] = expf(te.logp[i]);
     total += p[i];
     te.id[i] -= part * kPart;
-    const bool mine = te.id[i] >= 0 && te.id[i] < kPart;
+    const bool mine = (uint32_t)te.id[i] < kPart;
     here[i] = __ballot(mine);
     any |= here[i];
     s[i] = mine ? E::one(in[te.id[i]]) : 0.f;
@@ -824,37 +831,45 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_distill_bwd(const LogitsA
   }
   store_runs<E, ONCE>(out, n, lane, x);
   if (any == 0 || zero) return;
-  // the part's entries, one index at a time: its first entry takes the sum of all of its p
+  // An index that comes once takes its own p.  Entries of one index see another's
+  // number where they left theirs; then the part's entries go one after the other,
+  // each adds up the p of those of its index, and the first of them stores.
   float sum[kEntries];
-  bool first[kEntries];
+  bool later[kEntries], twice = false;
+  uint16_t* left = owner[threadIdx.x >> 6];
 #pragma unroll
   for (int i = 0; i < kEntries; ++i) {
-    sum[i] = 0.f;
-    first[i] = false;
+    if ((uint32_t)te.id[i] < kPart) left[te.id[i]] = i * 64 + lane;
+    sum[i] = p[i];
+    later[i] = false;
   }
+  wave_sync();
 #pragma unroll
-  for (int i = 0; i < kEntries; ++i) {
-    while (here[i]) {
-      const int who = __builtin_ctzll(here[i]);
-      const int id = __builtin_amdgcn_readlane(te.id[i], who);
-      float t = 0.f;
+  for (int i = 0; i < kEntries; ++i)
+    if ((uint32_t)te.id[i] < kPart) twice |= left[te.id[i]] != i * 64 + lane;
+  if (__ballot(twice)) {
 #pragma unroll
-      for (int j = i; j < kEntries; ++j) {
-        uint64_t same = __ballot(te.id[j] == id);
-        here[j] &= ~same;
-        for (; same; same &= same - 1)
-          t += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p[j]), __builtin_ctzll(same)));
-      }
-      if (lane == who) {
-        sum[i] = t;
-        first[i] = true;
+    for (int i = 0; i < kEntries; ++i) sum[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kEntries; ++i) {
+#pragma unroll 1
+      for (uint64_t rest = here[i]; rest; rest &= rest - 1) {
+        const int who = __builtin_ctzll(rest);
+        const int id = __builtin_amdgcn_readlane(te.id[i], who);
+        const float pe = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p[i]), who));
+#pragma unroll
+        for (int j = 0; j < kEntries; ++j) {
+          const bool same = te.id[j] == id;
+          sum[j] += same ? pe : 0.f;
+          later[j] |= same && (j > i || (j == i && lane > who));
+        }
       }
     }
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the stores above are done
 #pragma unroll
   for (int i = 0; i < kEntries; ++i)
-    if (first[i]) out[te.id[i]] = E::round(g * (exp2_fast(__builtin_fmaf(s[i] - m, c, off)) * total - sum[i]));
+    if ((uint32_t)te.id[i] < kPart && !later[i]) out[te.id[i]] = E::round(g * (exp2_fast(__builtin_fmaf(s[i] - m, c, off)) * total - sum[i]));
 }
 
 }  // namespace stack

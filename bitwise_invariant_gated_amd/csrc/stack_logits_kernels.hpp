@@ -325,7 +325,7 @@ __device__ __forceinline__ uint32_t select_largest(const float (&x)[N], int want
   const int mine = __builtin_popcount(take);
   int at = sum_up_to(mine) - mine;
 #pragma unroll 1
-  for (; take; take &= take - 1) list[at++] = N * lane + __builtin_ctz(take);
+  for (; take && at < 64; take &= take - 1) list[at++] = N * lane + __builtin_ctz(take);
   return lo;
 }
 

@@ -131,6 +131,8 @@ def _stream(stream, *tensors) -> int:
 
 
 def _bytes(workspace):
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous expected")
     return _ptr(workspace), workspace.numel() * workspace.element_size()
 
 

@@ -189,6 +189,8 @@ def test_binding_refusals(lib):
                dict(top_ids=good["top_ids"].t()), dict(top_logprobs=torch.zeros(4, 3)), dict(stats=f), dict(scale=f[:1])):
         with pytest.raises(ValueError, match=WRONG):
             gdn.gdn_stack_logprobs(z, **{**good, **kw})
+    with pytest.raises(ValueError, match="workspace"):
+        gdn.gdn_stack_logprobs(z, **{**good, "workspace": ws[::2]})
     with pytest.raises(ValueError, match=WRONG):
         gdn.gdn_stack_distill(z, lg, good["top_ids"].long(), good["top_logprobs"], f, None, ws)
     with pytest.raises(ValueError, match=WRONG):

@@ -5,9 +5,9 @@
 // Per call, on the caller's stream:
 //   add_norm        k_stack_add_norm; its gradient k_stack_add_norm_bwd and
 //                   k_stack_norm_dw
-//   logprobs        k_stack_parts, k_stack_logprobs; gradient
-//                   k_stack_logprobs_bwd
-//   distill         k_stack_parts, k_stack_distill; gradient
+//   logprobs        k_stack_parts, k_stack_logprobs (rows of up to 2,048 columns:
+//                   the latter alone); gradient k_stack_logprobs_bwd
+//   distill         k_stack_parts, k_stack_distill (the same); gradient
 //                   k_stack_distill_bwd
 #include <hip/hip_runtime.h>
 
@@ -391,20 +391,27 @@ void run_parts(const LogitsArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((k_stack_parts<E, ENTROPY, TOP, false>), part_grid(a), dim3(64 * kWaves), 0, st, a);
 }
 
+template <class E, int MODE, bool SHORT>
+void run_rows(const LogitsArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((k_stack_logprobs<E, MODE, SHORT>), row_grid(a), dim3(64 * kWaves), 0, st, a);
+}
+
 template <class E>
 void run_logprobs(const LogitsArgs& a, hipStream_t st) {
-  const dim3 wg(64 * kWaves);
   const int mode = top_mode(a.vocab, a.top);
+  if (a.parts == 1) {  // up to 2,048 columns
+    mode == kNoTop ? run_rows<E, kNoTop, true>(a, st)
+    : mode == kTopColumns ? run_rows<E, kTopColumns, true>(a, st)
+                          : run_rows<E, kTopEights, true>(a, st);
+    return;
+  }
   if (mode == kTopGroups)
     a.entropy ? run_parts<E, true, true>(a, st) : run_parts<E, false, true>(a, st);
   else
     a.entropy ? run_parts<E, true, false>(a, st) : run_parts<E, false, false>(a, st);
-  switch (mode) {
-    case kNoTop: hipLaunchKernelGGL((k_stack_logprobs<E, kNoTop>), row_grid(a), wg, 0, st, a); break;
-    case kTopColumns: hipLaunchKernelGGL((k_stack_logprobs<E, kTopColumns>), row_grid(a), wg, 0, st, a); break;
-    case kTopEights: hipLaunchKernelGGL((k_stack_logprobs<E, kTopEights>), row_grid(a), wg, 0, st, a); break;
-    default: hipLaunchKernelGGL((k_stack_logprobs<E, kTopGroups>), row_grid(a), wg, 0, st, a); break;
-  }
+  mode == kNoTop ? run_rows<E, kNoTop, false>(a, st)
+  : mode == kTopEights ? run_rows<E, kTopEights, false>(a, st)
+                       : run_rows<E, kTopGroups, false>(a, st);
 }
 
 template <class E, bool ONCE>
@@ -422,8 +429,12 @@ void run_logprobs_bwd(const LogitsArgs& a, hipStream_t st) {
 
 template <class E>
 void run_distill(const LogitsArgs& a, hipStream_t st) {
-  run_parts<E, false, false>(a, st);
-  hipLaunchKernelGGL((k_stack_distill<E>), row_grid(a), dim3(64 * kWaves), 0, st, a);
+  if (a.parts == 1) {
+    hipLaunchKernelGGL((k_stack_distill<E, true>), row_grid(a), dim3(64 * kWaves), 0, st, a);
+  } else {
+    run_parts<E, false, false>(a, st);
+    hipLaunchKernelGGL((k_stack_distill<E, false>), row_grid(a), dim3(64 * kWaves), 0, st, a);
+  }
 }
 
 template <class E>

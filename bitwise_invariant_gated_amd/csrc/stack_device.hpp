@@ -6,7 +6,6 @@
 
 namespace stack {
 
-using attn::bf16x2;
 using attn::dpp;
 using attn::f32x4;
 using attn::pack2;
@@ -33,8 +32,8 @@ struct F8 {
   __device__ __forceinline__ float& operator[](int i) { return i < 4 ? ((float*)&a)[i] : ((float*)&b)[i - 4]; }
 };
 
-// Element access: T the stored type, RAW eight of them as loaded.  ONCE, STREAM: not
-// to be kept in the caches.
+// Element access: T the stored type, RAW eight of them as loaded.  ANY: at any
+// element's address; ONCE: not to be kept in the caches.
 struct B16 {
   typedef uint16_t T;
   typedef u32x4 RAW;
@@ -57,22 +56,12 @@ struct B16 {
     return f;
   }
   // a vector of eight from and to runs of 16 bytes
-  template <class U>
-  static __device__ __forceinline__ void widen(F8& f, const U* r) {
-    f = wide(r[0]);
-  }
+  static __device__ __forceinline__ void widen(F8& f, const u32x4* r) { f = wide(r[0]); }
   static __device__ __forceinline__ void narrow_to(const F8& f, u32x4* r) { r[0] = narrow(f); }
   static __device__ __forceinline__ RAW narrow(F8 f) {
     return RAW{pack2(f.a[0], f.a[1]), pack2(f.a[2], f.a[3]), pack2(f.b[0], f.b[1]), pack2(f.b[2], f.b[3])};
   }
-  template <bool ANY, bool STREAM>
-  static __device__ __forceinline__ void store(T* p, RAW r) {
-    typedef typename Pick<ANY>::U V;
-    if constexpr (STREAM)
-      __builtin_nontemporal_store(r, (V*)p);
-    else
-      *(V*)p = r;
-  }
+  static __device__ __forceinline__ void store(T* p, RAW r) { *(u32x4*)p = r; }
 };
 
 struct F32 {
@@ -88,27 +77,18 @@ struct F32 {
   static __device__ __forceinline__ T round(float x) { return x; }
   static __device__ __forceinline__ F8 wide(RAW r) { return r; }
   static __device__ __forceinline__ RAW narrow(F8 f) { return f; }
-  template <class U>
-  static __device__ __forceinline__ void widen(F8& f, const U* r) {
-    f = F8{__builtin_bit_cast(f32x4, (u32x4)r[0]), __builtin_bit_cast(f32x4, (u32x4)r[1])};
+  static __device__ __forceinline__ void widen(F8& f, const u32x4* r) {
+    f = F8{__builtin_bit_cast(f32x4, r[0]), __builtin_bit_cast(f32x4, r[1])};
   }
   static __device__ __forceinline__ void narrow_to(const F8& f, u32x4* r) {
     r[0] = __builtin_bit_cast(u32x4, f.a);
     r[1] = __builtin_bit_cast(u32x4, f.b);
   }
-  template <bool ANY, bool STREAM>
   static __device__ __forceinline__ void store(T* p, RAW r) {
-    typedef typename Pick<ANY>::F V;
-    if constexpr (STREAM) {
-      __builtin_nontemporal_store(r.a, (V*)p);
-      __builtin_nontemporal_store(r.b, (V*)(p + 4));
-    } else {
-      *(V*)p = r.a;
-      *(V*)(p + 4) = r.b;
-    }
+    *(f32x4*)p = r.a;
+    *(f32x4*)(p + 4) = r.b;
   }
 };
-
 
 // Sum over aligned groups of L lanes (16 .. 64), the same bits in every lane.
 template <int L>

@@ -146,7 +146,7 @@ __global__ __launch_bounds__(kNormThreads) void k_stack_add_norm(const NormArgs 
       }
       const typename R::RAW n = R::narrow(h[j]);
       h[j] = R::wide(n);
-      if (a.h) R::template store<false, false>(h_out + c, n);
+      if (a.h) R::store(h_out + c, n);
       ss = dot4(h[j].b, h[j].b, dot4(h[j].a, h[j].a, ss));
     }
   }
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(kNormThreads) void k_stack_add_norm(const NormArgs 
     const f32x4 w1 = *(const f32x4*)(a.w + c) + a.w_add, w2 = *(const f32x4*)(a.w + c + 4) + a.w_add;
     h[j].a = h[j].a * r * w1;
     h[j].b = h[j].b * r * w2;
-    if (a.y) X::template store<false, false>((typename X::T*)a.y + row * a.y_stride + c, X::narrow(h[j]));
+    if (a.y) X::store((typename X::T*)a.y + row * a.y_stride + c, X::narrow(h[j]));
     if (a.y8 && a.group == 0) most = fmaxf(most, amax8(h[j]));
   }
   if (!a.y8) return;
@@ -247,8 +247,8 @@ __global__ __launch_bounds__(kNormBwdThreads<LANES>, 4) void k_stack_add_norm_bw
         d.a += f.a;
         d.b += f.b;
       }
-      if (a.y) X::template store<false, false>((typename X::T*)a.y + row * a.y_stride + c, X::narrow(d));
-      if (a.h) R::template store<false, false>((typename R::T*)a.h + row * a.h_stride + c, R::narrow(d));
+      if (a.y) X::store((typename X::T*)a.y + row * a.y_stride + c, X::narrow(d));
+      if (a.h) R::store((typename R::T*)a.h + row * a.h_stride + c, R::narrow(d));
     }
   }
 #pragma unroll

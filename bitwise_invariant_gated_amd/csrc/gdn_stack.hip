@@ -147,7 +147,7 @@ constexpr int64_t kOnceFrom = int64_t(96) << 20;
 // Work-groups of the gradient's row pass, each with a partial dw: enough to fill
 // the card, few enough that adding them up is short (us with 256 / 512 / 1,024 of them:
 // 10,240 x 2,048 37.9 / 35.3 / 38.3, 5,120 x 4,096 39.1 / 37.3 / 39.5, 2,500 x 8,192 38.5 / 41.6 / 47.4,
-// 1,200 x 16,384 42.5 / 48.6 / 60.4).
+// 1,200 x 16,384 42.5 / 48.6 / 60.4, all before rows were read ahead).
 int norm_bwd_groups(const gdn_norm_shape& s, int64_t rows) {
   const int64_t per = s.width <= 128 ? 32 : s.width <= 1024 ? 8 : s.width <= 4096 ? 2 : 1;
   return (int)std::min<int64_t>(s.width <= 4096 ? 512 : 256, (rows + per - 1) / per);

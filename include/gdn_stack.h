@@ -77,9 +77,10 @@ typedef struct {
  *   residual_out  h; may be NULL, and may be residual or x (same type and
  *                 stride)
  *   y             n in dtype; may be x, or residual of that type (same stride)
- *   y8, y_scale   n in e4m3: n / s to the nearest code, s = max(amax, 2^-100) / 448
- *                 over the group's |n|; y8 [rows, width], y_scale fp32 [rows,
- *                 width / group] ([rows, 1] for group 0), both contiguous
+ *   y8, y_scale   n in e4m3: the quotient n / s, in fp32, to the nearest code (half to
+ *                 even), s = max(amax, 2^-100) / 448 over the group's |n|; y8 [rows,
+ *                 width], y_scale fp32 [rows, width / group] ([rows, 1] for group
+ *                 0), both contiguous
  * y or y8 may be NULL (y_scale with y8), not both.  Computed in fp32, rounded
  * once; the sum of h^2 is finite for |h| up to 2^63 / sqrt(width).  Past that,
  * and in a row that holds an infinity, r is 0: n is 0, and NaN in the place of

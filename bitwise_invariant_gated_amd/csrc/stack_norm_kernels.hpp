@@ -247,6 +247,10 @@ __global__ __launch_bounds__(kNormBwdThreads<LANES>, 4) void k_stack_add_norm_bw
       }
     }
   };
+  const auto put = [&](int64_t row, int c, const F8& d) {
+    if (a.y) X::store((typename X::T*)a.y + row * a.y_stride + c, X::narrow(d));
+    if (a.h) R::store((typename R::T*)a.h + row * a.h_stride + c, R::narrow(d));
+  };
   // The next row is asked for before this one is summed, where a row takes a
   // work-group or half of one, so that few are under way, and it fits 24 registers:
   // us with / without, bf16, 1,174 x 8,184 20.9 / 22.3, 2,500 x 8,192 33.8 / 36.9, 1,200 x 16,384 36.6 / 40.3,
@@ -258,7 +262,7 @@ __global__ __launch_bounds__(kNormBwdThreads<LANES>, 4) void k_stack_add_norm_bw
   if (AHEAD) fetch(next, (int64_t)blockIdx.x * G + sub);
   for (int64_t first = (int64_t)blockIdx.x * G; first < a.rows; first += step, turn ^= 1) {
     const int64_t row = first + sub;
-    const int width = row < a.rows ? a.width : 0;  // no row: no columns
+    int width = row < a.rows ? a.width : 0;  // no row: no columns
     Raw q;
     if (AHEAD) {
       q = next;
@@ -278,6 +282,17 @@ __global__ __launch_bounds__(kNormBwdThreads<LANES>, 4) void k_stack_add_norm_bw
     row_sums<LANES>(ss, hx, red[turn][sub]);
     const float r = 1.f / __builtin_sqrtf(ss * inv + a.eps);
     const float m = hx * r * r * inv;
+    if (r == 0.f) {  // the squares pass fp32's range: n is 0 whatever h is, and nothing comes back through it
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * LANES + l) * 8;
+        if (c >= width) continue;
+        F8 d = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        if (a.res) d = R::wide(q.d[j]);
+        put(row, c, d);
+      }
+      width = 0;  // done
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * LANES + l) * 8;
@@ -291,8 +306,7 @@ __global__ __launch_bounds__(kNormBwdThreads<LANES>, 4) void k_stack_add_norm_bw
         d.a += f.a;
         d.b += f.b;
       }
-      if (a.y) X::store((typename X::T*)a.y + row * a.y_stride + c, X::narrow(d));
-      if (a.h) R::store((typename R::T*)a.h + row * a.h_stride + c, R::narrow(d));
+      put(row, c, d);
     }
   }
 #pragma unroll

@@ -97,9 +97,10 @@ gdn_status gdn_stack_add_norm(const gdn_norm_shape* shape, int64_t num_rows, con
  * later readers give it; NULL for none),
  *   dh = d_residual_out + r (dn - h r^2 mean(dn h)),  dn = dy w,
  * the gradient of x and of residual alike: dx in dtype, d_residual in
- * residual_dtype, either may be NULL.  dw fp32 [width] (0 without rows).
- * dx may be dy, d_residual may be d_residual_out, either may be h of its
- * type (same strides).
+ * residual_dtype, either may be NULL.  dw fp32 [width] (0 without rows).  Of a
+ * row with r = 0, dh is d_residual_out and dw has nothing; one whose h holds a
+ * NaN gives NaN everywhere.  dx may be dy, d_residual may be d_residual_out,
+ * either may be h of its type (same strides).
  */
 gdn_status gdn_stack_add_norm_bwd(const gdn_norm_shape* shape, int64_t num_rows, const void* h, int64_t h_stride,
                                   const float* w, const void* dy, int64_t dy_stride, const void* d_residual_out,

@@ -1,7 +1,7 @@
 // The residual's addition with the root-mean-square norm, and its gradient.
 //
-// h = x + residual, rounded as it is stored; r = 1 / sqrt(sum(h^2) / width + eps);
-// n = h r w.  Gradient: dn = dy w, dh = d_residual_out + r (dn - h (r^2 / width)
+// h = x + residual, rounded as it is stored; r = 1 / sqrt(sum(h^2) / width + eps)
+// (0 where the sum passes fp32's range, or is 0 without eps); n = h r w.  Gradient: dn = dy w, dh = d_residual_out + r (dn - h (r^2 / width)
 // sum(dn h)), dw = sum over rows of dy h r: two sums over the row, sum(h^2) and
 // sum(dn h), in one pass.
 //
@@ -75,6 +75,12 @@ __device__ __forceinline__ void row_sums(float& x, float& y, float* red) {
       y += red[W + i];
     }
   }
+}
+
+// r of a row's sum of squares.  A row of zeros without eps: 0, so that its norm is.
+__device__ __forceinline__ float root(float ss, float inv_width, float eps) {
+  const float mean = ss * inv_width + eps;
+  return mean == 0.f ? 0.f : 1.f / __builtin_sqrtf(mean);
 }
 
 template <int LANES>
@@ -174,7 +180,7 @@ __global__ __launch_bounds__(kNormThreads) void k_stack_add_norm(const NormArgs 
     }
   }
   ss = row_sum<LANES>(ss, red);
-  const float r = 1.f / __builtin_sqrtf(ss * (1.f / (float)a.width) + a.eps);
+  const float r = root(ss, 1.f / (float)a.width, a.eps);
   float most = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -280,9 +286,9 @@ __global__ __launch_bounds__(kNormBwdThreads<LANES>, 4) void k_stack_add_norm_bw
       hx = dot4(y.b * w.b, h.b, dot4(y.a * w.a, h.a, hx));
     }
     row_sums<LANES>(ss, hx, red[turn][sub]);
-    const float r = 1.f / __builtin_sqrtf(ss * inv + a.eps);
+    const float r = root(ss, inv, a.eps);
     const float m = hx * r * r * inv;
-    if (r == 0.f) {  // the squares pass fp32's range: n is 0 whatever h is, and nothing comes back through it
+    if (r == 0.f) {  // n is 0 whatever h is, and nothing comes back through it
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (j * LANES + l) * 8;

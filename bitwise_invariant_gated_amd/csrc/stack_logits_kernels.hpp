@@ -721,8 +721,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_logprobs_bwd(const Logits
         const float d = x[j][i] - m;
         const float p = exp2_fast(__builtin_fmaf(d, c, off));
         float k = g;
-        // of a masked column: q is 0, and log q is held to what is finite
-        if constexpr (ENTROPY) k = __builtin_fmaf(f, fmaxf(__builtin_fmaf(d, scale, up), -0x1p100f), g);
+        // where q is 0 (log q below -104, as of a masked column) log q + h is held to -128, so that
+        // no f makes an infinity of it: 0 * inf would be NaN
+        if constexpr (ENTROPY) k = __builtin_fmaf(f, fmaxf(__builtin_fmaf(d, scale, up), -128.f), g);
         x[j][i] = -p * k;
       }
     }

@@ -391,27 +391,32 @@ void run_parts(const LogitsArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((k_stack_parts<E, ENTROPY, TOP, false>), part_grid(a), dim3(64 * kWaves), 0, st, a);
 }
 
-template <class E, int MODE, bool SHORT>
+template <class E, int MODE, RowForm FORM>
 void run_rows(const LogitsArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_stack_logprobs<E, MODE, SHORT>), row_grid(a), dim3(64 * kWaves), 0, st, a);
+  hipLaunchKernelGGL((k_stack_logprobs<E, MODE, FORM>), row_grid(a), dim3(64 * kWaves), 0, st, a);
+}
+
+template <class E, int MODE>
+void run_short(const LogitsArgs& a, hipStream_t st) {
+  a.entropy ? run_rows<E, MODE, kMakeEntropy>(a, st) : run_rows<E, MODE, kMake>(a, st);
 }
 
 template <class E>
 void run_logprobs(const LogitsArgs& a, hipStream_t st) {
   const int mode = top_mode(a.vocab, a.top);
   if (a.parts == 1) {  // up to 2,048 columns
-    mode == kNoTop ? run_rows<E, kNoTop, true>(a, st)
-    : mode == kTopColumns ? run_rows<E, kTopColumns, true>(a, st)
-                          : run_rows<E, kTopEights, true>(a, st);
+    mode == kNoTop ? run_short<E, kNoTop>(a, st)
+    : mode == kTopColumns ? run_short<E, kTopColumns>(a, st)
+                          : run_short<E, kTopEights>(a, st);
     return;
   }
   if (mode == kTopGroups)
     a.entropy ? run_parts<E, true, true>(a, st) : run_parts<E, false, true>(a, st);
   else
     a.entropy ? run_parts<E, true, false>(a, st) : run_parts<E, false, false>(a, st);
-  mode == kNoTop ? run_rows<E, kNoTop, false>(a, st)
-  : mode == kTopEights ? run_rows<E, kTopEights, false>(a, st)
-                       : run_rows<E, kTopGroups, false>(a, st);
+  mode == kNoTop ? run_rows<E, kNoTop, kJoin>(a, st)
+  : mode == kTopEights ? run_rows<E, kTopEights, kJoin>(a, st)
+                       : run_rows<E, kTopGroups, kJoin>(a, st);
 }
 
 template <class E, bool ONCE>
@@ -430,10 +435,10 @@ void run_logprobs_bwd(const LogitsArgs& a, hipStream_t st) {
 template <class E>
 void run_distill(const LogitsArgs& a, hipStream_t st) {
   if (a.parts == 1) {
-    hipLaunchKernelGGL((k_stack_distill<E, true>), row_grid(a), dim3(64 * kWaves), 0, st, a);
+    hipLaunchKernelGGL((k_stack_distill<E, kMake>), row_grid(a), dim3(64 * kWaves), 0, st, a);
   } else {
     run_parts<E, false, false>(a, st);
-    hipLaunchKernelGGL((k_stack_distill<E, false>), row_grid(a), dim3(64 * kWaves), 0, st, a);
+    hipLaunchKernelGGL((k_stack_distill<E, kJoin>), row_grid(a), dim3(64 * kWaves), 0, st, a);
   }
 }
 

@@ -827,6 +827,16 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_distill(const LogitsArgs 
   }
 }
 
+// The wave's stores before this are done when those after it begin.  The fences keep
+// the compiler from moving any across; that of a work-group makes no wait for stores on this
+// target, whose waves' stores to an address stay in order, so the wait is one of its
+// own (2,048 x 131,072, bf16, 64 entries: 175.8 us, without 178.6).
+__device__ __forceinline__ void stores_done() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+}
+
 // Gradient.  Every column is first stored as if it were no entry; the wave then
 // writes over those that are.
 template <class E, bool ONCE>
@@ -903,7 +913,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_stack_distill_bwd(const LogitsA
       }
     }
   }
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the stores above are done
+  stores_done();  // other lanes write to the same places now
 #pragma unroll
   for (int i = 0; i < kEntries; ++i)
     if ((uint32_t)te.id[i] < kPart && !later[i]) out[te.id[i]] = E::round(g * (exp2_fast(__builtin_fmaf(s[i] - m, c, off)) * total - sum[i]));

@@ -134,13 +134,16 @@ gdn_status check_norm(const char* fn, const gdn_norm_shape* s, int64_t rows) {
 
 // Calls that move more than this read past the caches what is read for the last
 // time (x, the residual, the gradients that come in, logits), us past / into them:
-//   norm      10,240 x 2,048 (168 MB) 32.4 / 39.3   6,144 (101 MB) 17.6 / 21.1   4,096 (67 MB) 12.4 / 11.8
-//   gradient                          33.0 / 36.8                  21.8 / 22.4                 17.3 / 15.4
-//   parts     2,048 x 131,072 (537 MB) 84.6 / 95.4; with entropy 4,096 168 / 173; fp32 1,024 87 / 91
+//   norm      10,240 x 2,048 (168 MB) 32.4 / 39.3   6,144 (101 MB) 17.7 / 21.8   4,096 (67 MB) 12.2 / 11.8
+//   gradient                          32.0 / 36.5                  22.1 / 23.9                 17.0 / 15.7
+//   parts     2,048 x 131,072 (537 MB), divergence 84.9 / 95.3; with entropy 4,096 156 / 177; fp32 1,024 87 / 92
+// Of rows that end inside a part the last one is read through the caches, and so are rows
+// of one part, whatever the call's size: past them, 60,000 x 900 51.2 / 52.2 in bf16 but 51.4 / 49.5 in fp32,
+// 60,000 x 2,000 63.2 / 64.8 and 85.9 / 82.5, its divergence in fp32 94.7 / 82.5.
 // Outputs of the norm stay in the caches, as a product reads them next: stored past
 // them, 10,240 x 2,048 would take 26 us, but norm, product and norm 139 and not 123.
-// Gradients of logits do not fit and go past them too, 2,048 x 131,072 165 / 180, fp32
-// 513 x 50,001 (103 MB) 38.7 / 42.7; with the product that reads them, of width 1,024,
+// Gradients of logits do not fit and go past them too, 2,048 x 131,072 170 / 184, fp32
+// 513 x 50,001 (103 MB) 37.6 / 41.6, the divergence's 38.7 / 42.3; with the product that reads them, of width 1,024,
 // 1,024 rows (268 MB) 768 / 783, 4,096 1,556 / 1,609, but 256 rows (67 MB) 459 / 457.
 constexpr int64_t kOnceFrom = int64_t(96) << 20;
 

@@ -20,10 +20,13 @@
 // column costs 8 instructions, so the sums over 4,096 x 131,072 keep the vector
 // units busy four fifths of the time; there is little room for more.
 //
-// Measured: log probabilities and entropy of 4,096 x 131,072, bf16, 156 us, 1.07 GB, 6.9 TB/s;
-// of 256 rows with 20 alternatives 24.4 us (parts 13.9, join 10.6); gradient of 2,048 rows 164 us,
-// 1.0 GB moved, 6.1 TB/s.  Divergence from 64 entries, 2,048 rows, 84.7 us, 538 MB, 6.4 TB/s; its
-// gradient, fp32, 513 x 50,001 38.7 us, 205 MB, 5.3 TB/s.
+// Measured (a kernel that reads 1.07 GB and does nothing else: 154 us): log probabilities and
+// entropy of 4,096 x 131,072, bf16, 155 us, 6.9 TB/s; of 256 rows with 20 alternatives 24.5 us (parts 14.2,
+// join 11.0); gradient of 2,048 rows 164 us, 1.0 GB moved, 6.1 TB/s.  Divergence from 64 entries,
+// 2,048 rows, 84.9 us, 538 MB, 6.3 TB/s; its gradient 175 us, 1.07 GB, 6.1 TB/s, from 256 entries 187; in fp32
+// 513 x 50,001 38.6 us, 205 MB, 5.3 TB/s.  Rows of one part, one launch: log probabilities and entropy of
+// 60,000 x 900 52 us in bf16, 109 MB, 2.1 TB/s, and 50 in fp32, 217 MB, 4.4 TB/s: the vectors of a row's end are
+// loaded one after the other, each waited for before the next, so latency bounds them.
 #pragma once
 
 #include "stack_device.hpp"

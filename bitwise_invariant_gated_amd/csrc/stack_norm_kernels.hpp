@@ -7,12 +7,18 @@
 //
 // Bound by memory: a row is read once, kept in registers and written once.  A row
 // is the work of 16, 64 or 256 threads (gradient: up to 1,024), as its width
-// says, so that a thread holds at most 64 columns and eight waves or more share a
-// SIMD, and so that its bits depend on the width alone.
+// says, so that a thread holds at most 64 columns, and so that its bits depend on
+// the width alone.  The waves that share a SIMD, as their registers let them: eight or more
+// where a lane has up to 16 columns (widths up to 1,024, and from 2,056 to 4,096), and in
+// bf16 up to 8,192; with 32 columns seven in bf16 over a stream in fp32 (67 and 68
+// registers) and four all in fp32 (97 and 100); with 64, past 8,192, four (102 and
+// 124) and two (188).  The gradient is held to four.
 //
-// Measured (the card copies 256 MB at 5.5 TB/s, 2 GB at 5.0): 10,240 x 2,048, bf16, 32.3 us, 168 MB, 5.2 TB/s;
-// 10,240 x 4,096 into 8 bits over a stream in fp32 85 us, 463 MB, 5.4 TB/s; one row 3.2 us (the
-// call 6.4, of the host).  Gradient of 10,240 x 2,048 32.1 us in two launches, 168 MB, 5.2 TB/s.
+// Measured (the card copies 256 MB at 5.5 TB/s, 2 GB at 5.0): 10,240 x 2,048, bf16, 32.4 us, 168 MB, 5.2 TB/s;
+// 10,240 x 4,096 into 8 bits over a stream in fp32 85.5 us, 463 MB, 5.4 TB/s; one row 3.3 us (the
+// call 6.0 to 7.0, of the host).  All in fp32 5,000 x 2,048 37.5 us, 164 MB, 4.4 TB/s, 1,250 x 8,192 35.8 us, 4.6; 1,200 x
+// 16,384 30.4 us in bf16, 157 MB, 5.2 TB/s, 51.1 over a stream in fp32, 236 MB, 4.6, 73.8 all in fp32, 315 MB,
+// 4.3.  Gradient of 10,240 x 2,048 32.0 us in two launches, 168 MB, 5.2 TB/s.
 #pragma once
 
 #include "stack_device.hpp"

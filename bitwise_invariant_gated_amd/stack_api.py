@@ -184,7 +184,8 @@ def gdn_stack_logprobs(shape: LogitsShape, logits, targets, logprobs, entropy, t
 def gdn_stack_logprobs_bwd(shape: LogitsShape, logits, targets, stats, entropy, d_logprobs, d_entropy, d_logits,
                            scale=None, stream=None) -> None:
     """Gradient of the log probabilities and the entropy; one of d_logprobs and d_entropy may be
-    None (entropy with the latter).  d_logits may be logits."""
+    None (entropy with the latter).  targets are those of the forward call, with d_entropy alone too:
+    they say which rows it left out.  d_logits may be logits."""
     f32 = torch.float32
     n, lp, ls = _row_args(logits, None, shape.vocab, shape.dtype, "logits")
     _, dp, ds = _row_args(d_logits, n, shape.vocab, shape.dtype, "d_logits")

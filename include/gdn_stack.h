@@ -111,7 +111,7 @@ gdn_status gdn_stack_add_norm_bwd(const gdn_norm_shape* shape, int64_t num_rows,
                                   void* stream);
 
 /* Bytes of workspace of gdn_stack_add_norm_bwd (host only; 0 for an invalid
- * shape or size). */
+ * shape or size).  Two calls that may run at once need one each. */
 size_t gdn_stack_norm_workspace_size(const gdn_norm_shape* shape, int64_t num_rows);
 
 /*
@@ -120,7 +120,7 @@ size_t gdn_stack_norm_workspace_size(const gdn_norm_shape* shape, int64_t num_ro
  *   targets       int32 [rows], or NULL.  A row whose target is no index of
  *                 the vocabulary is left out: not read, and zeros in all
  *                 outputs (indices -1)
- *   scale         fp32 [rows], positive and finite: one over the row's
+ *   scale         fp32 [rows], positive, at most 2^127: one over the row's
  *                 temperature; NULL for 1
  *   logprobs      [rows] log q of the target; NULL without targets
  *   entropy       [rows] -sum q log q; may be NULL
@@ -142,7 +142,8 @@ gdn_status gdn_stack_logprobs(const gdn_logits_shape* shape, int64_t num_rows, c
  * d_entropy is given), with g = d_logprobs and f = d_entropy, fp32 [rows]:
  *   d_logits = scale (g ([v = target] - q) - f q (log q + entropy)).
  * d_logprobs or d_entropy may be NULL (0), not both; without targets
- * d_logprobs is NULL.  Rows left out, and rows of -inf only, get zeros.
+ * d_logprobs is NULL.  targets are those of the forward call, with d_entropy alone
+ * too: they say which rows it left out.  Such rows, and rows of -inf only, get zeros.
  * d_logits may be logits (same stride).
  */
 gdn_status gdn_stack_logprobs_bwd(const gdn_logits_shape* shape, int64_t num_rows, const void* logits,

@@ -84,8 +84,8 @@ typedef struct {
  * y or y8 may be NULL (y_scale with y8), not both.  Computed in fp32, rounded
  * once; the sum of h^2 is finite for |h| up to 2^63 / sqrt(width).  Past that,
  * and in a row that holds an infinity, r is 0: n is 0, and NaN in the place of
- * the infinity.  r is 0 too where eps is 0 and so is the sum (rows of zeros;
- * squares below 2^-149 are 0, and lose bits below 2^-126).  A NaN makes all of
+ * the infinity.  r is 0 too where eps is 0 and so is the mean (rows of
+ * zeros; squares below 2^-149 are 0, and lose bits below 2^-126).  A NaN makes all of
  * its row NaN (y_scale aside).
  */
 gdn_status gdn_stack_add_norm(const gdn_norm_shape* shape, int64_t num_rows, const void* x, int64_t x_stride,
